@@ -63,6 +63,56 @@ class dcn4_attn_params(ctypes.Structure):
     ]
 
 
+class dcn4_band_params(ctypes.Structure):
+    """Mirror of dcn4_band_params in include/dcn4.h (field order matters)."""
+
+    _fields_ = [
+        ("N", ctypes.c_int), ("Lq", ctypes.c_int), ("Lk", ctypes.c_int),
+        ("Hq", ctypes.c_int), ("Hk", ctypes.c_int), ("D", ctypes.c_int),
+        ("left", ctypes.c_int), ("right", ctypes.c_int), ("sinks", ctypes.c_int),
+        ("scale", ctypes.c_float),
+        ("nb", ctypes.c_int), ("M", ctypes.c_int),
+        ("dtype", ctypes.c_int),
+        ("q_batch", ctypes.c_longlong), ("q_row", ctypes.c_longlong),
+        ("k_batch", ctypes.c_longlong), ("k_row", ctypes.c_longlong),
+        ("v_batch", ctypes.c_longlong), ("v_row", ctypes.c_longlong),
+    ]
+
+
+class dcn4_qknorm_params(ctypes.Structure):
+    """Mirror of dcn4_qknorm_params in include/dcn4.h (field order matters)."""
+
+    _fields_ = [
+        ("N", ctypes.c_int), ("L", ctypes.c_int),
+        ("Hq", ctypes.c_int), ("Hk", ctypes.c_int), ("D", ctypes.c_int),
+        ("R", ctypes.c_int), ("axes", ctypes.c_int), ("interleaved", ctypes.c_int),
+        ("eps", ctypes.c_float),
+        ("dtype", ctypes.c_int),
+        ("q_batch", ctypes.c_longlong), ("q_row", ctypes.c_longlong),
+        ("k_batch", ctypes.c_longlong), ("k_row", ctypes.c_longlong),
+    ]
+
+
+def make_band_params(*, N, Lq, Lk, Hq, D, Hk=None, left=-1, right=-1, sinks=0, scale=None, nb=0, M=0, dtype="f16",
+                     q_batch=0, q_row=0, k_batch=0, k_row=0, v_batch=0, v_row=0) -> dcn4_band_params:
+    """dcn4_band_params of a dense attention over a band of keys; Hk defaults to Hq, scale
+    to 1/sqrt(D), and strides of 0 mean dense tensors."""
+    if isinstance(dtype, str):
+        dtype = DTYPE_NAMES[dtype]
+    return dcn4_band_params(N, Lq, Lk, Hq, Hq if Hk is None else Hk, D, left, right, sinks,
+                            D ** -0.5 if scale is None else float(scale), nb, M, dtype,
+                            q_batch, q_row, k_batch, k_row, v_batch, v_row)
+
+
+def make_qknorm_params(*, N, L, Hq, Hk, D, R=0, axes=1, interleaved=0, eps=1e-6, dtype="f16",
+                       q_batch=0, q_row=0, k_batch=0, k_row=0) -> dcn4_qknorm_params:
+    """dcn4_qknorm_params of a query/key norm with rotation; strides of 0 mean dense tensors."""
+    if isinstance(dtype, str):
+        dtype = DTYPE_NAMES[dtype]
+    return dcn4_qknorm_params(N, L, Hq, Hk, D, R, axes, 1 if interleaved else 0, float(eps), dtype,
+                              q_batch, q_row, k_batch, k_row)
+
+
 def make_attn_params(*, N, H, W, G, Cg, Nq, K, offset_scale=1.0, P=None, dtype="f16") -> dcn4_attn_params:
     """dcn4_attn_params for a single-scale deformable attention call; P defaults to G*3K rounded up to 8."""
     if isinstance(dtype, str):
@@ -92,6 +142,8 @@ def _load() -> ctypes.CDLL:
     L = ctypes.CDLL(LIB_PATH)
     P = ctypes.POINTER(dcn4_params)
     AP = ctypes.POINTER(dcn4_attn_params)
+    BP = ctypes.POINTER(dcn4_band_params)
+    QP = ctypes.POINTER(dcn4_qknorm_params)
     vp, ip = ctypes.c_void_p, ctypes.POINTER(ctypes.c_int)
     sig = {
         "dcn4_version": ([], ctypes.c_int),
@@ -121,6 +173,16 @@ def _load() -> ctypes.CDLL:
         "dcn4_attn_forward": ([AP, vp, vp, vp, vp, vp], ctypes.c_int),
         "dcn4_attn_backward_workspace_size": ([AP], ctypes.c_size_t),
         "dcn4_attn_backward": ([AP, vp, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp], ctypes.c_int),
+        "dcn4_band_check_params": ([BP], ctypes.c_int),
+        "dcn4_rel_buckets": ([ctypes.c_int, ctypes.c_int, ctypes.c_int, ip], ctypes.c_int),
+        "dcn4_band_forward_workspace_size": ([BP], ctypes.c_size_t),
+        "dcn4_band_forward": ([BP] + [vp] * 11 + [ctypes.c_size_t, vp], ctypes.c_int),
+        "dcn4_band_backward_workspace_size": ([BP], ctypes.c_size_t),
+        "dcn4_band_backward": ([BP] + [vp] * 16 + [ctypes.c_size_t, vp], ctypes.c_int),
+        "dcn4_qknorm_check_params": ([QP], ctypes.c_int),
+        "dcn4_qknorm_forward": ([QP] + [vp] * 9, ctypes.c_int),
+        "dcn4_qknorm_backward_workspace_size": ([QP], ctypes.c_size_t),
+        "dcn4_qknorm_backward": ([QP] + [vp] * 13 + [ctypes.c_size_t, vp], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -246,6 +308,53 @@ def dcn4_attn_backward(p: dcn4_attn_params, value, ref_points, offset_logits, gr
                        grad_offset_logits, workspace, workspace_bytes: int, stream=None) -> int:
     return lib.dcn4_attn_backward(ctypes.byref(p), value, ref_points, offset_logits, grad_out, grad_value,
                                   grad_offset_logits, workspace, workspace_bytes, stream)
+
+
+def dcn4_band_check_params(p: dcn4_band_params) -> int:
+    return lib.dcn4_band_check_params(ctypes.byref(p))
+
+
+def dcn4_rel_buckets(nb: int, M: int, both: bool, table) -> int:
+    """`table`: a ctypes array of 2 * M + 1 ints."""
+    return lib.dcn4_rel_buckets(int(nb), int(M), 1 if both else 0, table)
+
+
+def dcn4_band_forward_workspace_size(p: dcn4_band_params) -> int:
+    return lib.dcn4_band_forward_workspace_size(ctypes.byref(p))
+
+
+def dcn4_band_forward(p: dcn4_band_params, q, k, v, bias, buckets, q_start, q_len, k_len, out, lse, workspace,
+                      workspace_bytes: int, stream=None) -> int:
+    return lib.dcn4_band_forward(ctypes.byref(p), q, k, v, bias, buckets, q_start, q_len, k_len, out, lse, workspace,
+                                 workspace_bytes, stream)
+
+
+def dcn4_band_backward_workspace_size(p: dcn4_band_params) -> int:
+    return lib.dcn4_band_backward_workspace_size(ctypes.byref(p))
+
+
+def dcn4_band_backward(p: dcn4_band_params, q, k, v, bias, buckets, q_start, q_len, k_len, out, lse, grad_out, grad_q,
+                       grad_k, grad_v, grad_bias, workspace, workspace_bytes: int, stream=None) -> int:
+    return lib.dcn4_band_backward(ctypes.byref(p), q, k, v, bias, buckets, q_start, q_len, k_len, out, lse, grad_out,
+                                  grad_q, grad_k, grad_v, grad_bias, workspace, workspace_bytes, stream)
+
+
+def dcn4_qknorm_check_params(p: dcn4_qknorm_params) -> int:
+    return lib.dcn4_qknorm_check_params(ctypes.byref(p))
+
+
+def dcn4_qknorm_forward(p: dcn4_qknorm_params, q, k, wq, wk, pos, inv_freq, q_out, k_out, stream=None) -> int:
+    return lib.dcn4_qknorm_forward(ctypes.byref(p), q, k, wq, wk, pos, inv_freq, q_out, k_out, stream)
+
+
+def dcn4_qknorm_backward_workspace_size(p: dcn4_qknorm_params) -> int:
+    return lib.dcn4_qknorm_backward_workspace_size(ctypes.byref(p))
+
+
+def dcn4_qknorm_backward(p: dcn4_qknorm_params, q, k, wq, wk, pos, inv_freq, grad_q_out, grad_k_out, grad_q, grad_k,
+                         grad_wq, grad_wk, workspace, workspace_bytes: int, stream=None) -> int:
+    return lib.dcn4_qknorm_backward(ctypes.byref(p), q, k, wq, wk, pos, inv_freq, grad_q_out, grad_k_out, grad_q,
+                                    grad_k, grad_wq, grad_wk, workspace, workspace_bytes, stream)
 
 
 def dcn4_backward_noalloc(p: dcn4_params, value, offset_mask, grad_out, grad_value, grad_offset_mask,
@@ -445,6 +554,223 @@ def attn_backward(p: dcn4_attn_params, value, ref_points, offset_logits, grad_ou
     return gv, gol
 
 
+def rel_buckets(nb: int, M: int, both: bool = True, device="cuda"):
+    """int32 tensor [2M + 1] of the buckets of relative positions -M..M (dcn4_rel_buckets)."""
+    import torch
+    table = (ctypes.c_int * (2 * max(M, 0) + 1))()
+    check(dcn4_rel_buckets(nb, M, both, table))
+    return torch.tensor(list(table), dtype=torch.int32, device=device)
+
+
+class _on_device:
+    """Makes a tensor's device the current one for a launch, where it is not."""
+
+    def __init__(self, t):
+        import torch
+        self.torch, self.index = torch, t.device.index
+
+    def __enter__(self):
+        self.was = self.torch.cuda.current_device()
+        if self.was != self.index:
+            self.torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        if self.was != self.index:
+            self.torch.cuda.set_device(self.was)
+
+
+def _ptr(t):
+    return t.data_ptr() if t is not None else None
+
+
+def _workspace(need: int, like):
+    import torch
+    return torch.empty(need, dtype=torch.uint8, device=like.device) if need else None
+
+
+def _heads_strides(name, t, dtype, device):
+    """(batch, row) element strides of t [N, L, H, D] whose heads are contiguous; ValueError otherwise.
+    A dimension of length 1 has no stride that matters."""
+    if t.dim() != 4:
+        raise ValueError(f"{name} must be [N, L, H, D]")
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be on the same CUDA device as the others")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must have the same dtype as the others")
+    N, L, H, D = t.shape
+    sb, sl, sh, sd = t.stride()
+    if (D > 1 and sd != 1) or (H > 1 and sh != D):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    row = sl if L > 1 else H * D
+    batch = sb if N > 1 else row * L
+    if t.numel() and ((L > 1 and row < H * D) or (N > 1 and batch < H * D)):
+        raise ValueError(f"{name}: tokens must not overlap (expand()ed tensors need .contiguous())")
+    return batch, row
+
+
+def _int_vector(name, t, N, device):
+    import torch
+    if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != (N,) or not t.is_contiguous() or t.device != device):
+        raise ValueError(f"{name} must be a contiguous int32 tensor [N={N}] on q's device")
+
+
+def _dense(name, t, shape, dtype, device):
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on q's device")
+
+
+def band_params_for(q, k, v, *, left=-1, right=-1, sinks=0, scale=None, bias=None, buckets=None, q_start=None,
+                    q_len=None, k_len=None) -> dcn4_band_params:
+    """dcn4_band_params for CUDA tensors q [N, Lq, Hq, D], k and v [N, Lk, Hk, D] (views whose heads are
+    contiguous, such as parts of one packed projection or of a cache), bias [nb, Hq], buckets [2M + 1]
+    (int32) and q_start, q_len, k_len [N] (int32); checks them on the host (ValueError, Dcn4Error)."""
+    import torch
+    qb, qr = _heads_strides("q", q, q.dtype, q.device)
+    kb, kr = _heads_strides("k", k, q.dtype, q.device)
+    vb, vr = _heads_strides("v", v, q.dtype, q.device)
+    N, Lq, Hq, D = q.shape
+    if k.shape != v.shape or k.shape[0] != N or k.shape[3] != D:
+        raise ValueError("k and v must be [N, Lk, Hk, D] with q's N and D")
+    nb = M = 0
+    if (bias is None) != (buckets is None):
+        raise ValueError("bias and buckets come together")
+    if bias is not None:
+        if bias.dim() != 2 or bias.shape[0] < 1 or buckets.dim() != 1 or buckets.shape[0] < 3 or buckets.shape[0] % 2 == 0:
+            raise ValueError("bias must be [nb, Hq] and buckets [2M + 1]")
+        nb, M = bias.shape[0], buckets.shape[0] // 2
+        _dense("bias", bias, (nb, Hq), q.dtype, q.device)
+        _dense("buckets", buckets, (2 * M + 1,), torch.int32, q.device)
+    for name, t in (("q_start", q_start), ("q_len", q_len), ("k_len", k_len)):
+        _int_vector(name, t, N, q.device)
+    p = dcn4_band_params(N, Lq, k.shape[1], Hq, k.shape[2], D, left, right, sinks,
+                         D ** -0.5 if scale is None else float(scale), nb, M, _dtype_code(q), qb, qr, kb, kr, vb, vr)
+    check(dcn4_band_check_params(p))
+    return p
+
+
+def _same_call(p, *tensors):
+    """ValueError unless each (name, tensor, shape, batch stride, row stride) is what p was made for."""
+    for name, t, shape, batch, row in tensors:
+        sb, sl = t.stride()[:2]
+        if t.shape != shape or t.dtype != _torch_dtype(p.dtype) or (batch and shape[0] > 1 and sb != batch) or (
+                row and shape[1] > 1 and sl != row):
+            raise ValueError(f"{name} is not the tensor these parameters were made for")
+
+
+def _band_call(p, q, k, v):
+    _same_call(p, ("q", q, (p.N, p.Lq, p.Hq, p.D), p.q_batch, p.q_row),
+               ("k", k, (p.N, p.Lk, p.Hk, p.D), p.k_batch, p.k_row), ("v", v, (p.N, p.Lk, p.Hk, p.D), p.v_batch, p.v_row))
+
+
+def band_forward(p: dcn4_band_params, q, k, v, bias=None, buckets=None, q_start=None, q_len=None, k_len=None, out=None):
+    """(out [N, Lq, Hq, D], lse [N, Hq, Lq] fp32) of the dense attention over a band of keys,
+    for CUDA tensors as band_params_for takes them."""
+    import torch
+    _band_call(p, q, k, v)
+    if out is None:
+        out = torch.empty((p.N, p.Lq, p.Hq, p.D), dtype=q.dtype, device=q.device)
+    else:
+        _dense("out", out, (p.N, p.Lq, p.Hq, p.D), q.dtype, q.device)
+    lse = torch.empty((p.N, p.Hq, p.Lq), dtype=torch.float32, device=q.device)
+    need = dcn4_band_forward_workspace_size(p)
+    ws = _workspace(need, q)
+    with _on_device(q):
+        check(dcn4_band_forward(p, q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(bias), _ptr(buckets), _ptr(q_start),
+                                _ptr(q_len), _ptr(k_len), out.data_ptr(), lse.data_ptr(), _ptr(ws), need,
+                                _stream_handle(q.device)))
+    return out, lse
+
+
+def band_backward(p: dcn4_band_params, q, k, v, out, lse, grad_out, bias=None, buckets=None, q_start=None, q_len=None,
+                  k_len=None, want_bias: bool = True):
+    """(grad_q, grad_k, grad_v, grad_bias or None) of band_forward, from its out and lse;
+    grad_out [N, Lq, Hq, D] contiguous.  The gradients are dense."""
+    import torch
+    dev, dt = q.device, q.dtype
+    _band_call(p, q, k, v)
+    for name, t in (("out", out), ("grad_out", grad_out)):
+        _dense(name, t, (p.N, p.Lq, p.Hq, p.D), dt, dev)
+    _dense("lse", lse, (p.N, p.Hq, p.Lq), torch.float32, dev)
+    gq = torch.empty((p.N, p.Lq, p.Hq, p.D), dtype=dt, device=dev)
+    gk = torch.empty((p.N, p.Lk, p.Hk, p.D), dtype=dt, device=dev)
+    gv = torch.empty((p.N, p.Lk, p.Hk, p.D), dtype=dt, device=dev)
+    gb = torch.empty((p.nb, p.Hq), dtype=dt, device=dev) if bias is not None and want_bias else None
+    need = dcn4_band_backward_workspace_size(p)
+    ws = _workspace(need, q)
+    with _on_device(q):
+        check(dcn4_band_backward(p, q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(bias), _ptr(buckets), _ptr(q_start),
+                                 _ptr(q_len), _ptr(k_len), out.data_ptr(), lse.data_ptr(), grad_out.data_ptr(),
+                                 gq.data_ptr(), gk.data_ptr(), gv.data_ptr(), _ptr(gb), _ptr(ws), need,
+                                 _stream_handle(dev)))
+    return gq, gk, gv, gb
+
+
+def qknorm_params_for(q, k, wq=None, wk=None, pos=None, inv_freq=None, *, interleaved: bool = False,
+                      eps: float = 1e-6) -> dcn4_qknorm_params:
+    """dcn4_qknorm_params for CUDA tensors q [N, L, Hq, D] and k [N, L, Hk, D] (views whose heads are
+    contiguous), weights [D] or None, and for a rotation pos [N, L] or [N, L, axes] (float32) and
+    inv_freq [R / 2] (float32); checks them on the host (ValueError, Dcn4Error)."""
+    import torch
+    qb, qr = _heads_strides("q", q, q.dtype, q.device)
+    kb, kr = _heads_strides("k", k, q.dtype, q.device)
+    N, L, Hq, D = q.shape
+    if k.shape[:2] != q.shape[:2] or k.shape[3] != D:
+        raise ValueError("q and k must be [N, L, Hq, D] and [N, L, Hk, D]")
+    for name, w in (("wq", wq), ("wk", wk)):
+        if w is not None:
+            _dense(name, w, (D,), q.dtype, q.device)
+    if (pos is None) != (inv_freq is None):
+        raise ValueError("pos and inv_freq come together")
+    R, axes = 0, 1
+    if pos is not None:
+        if inv_freq.dim() != 1 or pos.dim() not in (2, 3):
+            raise ValueError("pos must be [N, L] or [N, L, axes] and inv_freq [R / 2]")
+        R, axes = 2 * inv_freq.shape[0], (pos.shape[2] if pos.dim() == 3 else 1)
+        _dense("pos", pos, (N, L) + ((axes,) if pos.dim() == 3 else ()), torch.float32, q.device)
+        _dense("inv_freq", inv_freq, (R // 2,), torch.float32, q.device)
+    p = dcn4_qknorm_params(N, L, Hq, k.shape[2], D, R, axes, 1 if interleaved else 0, float(eps), _dtype_code(q),
+                           qb, qr, kb, kr)
+    check(dcn4_qknorm_check_params(p))
+    return p
+
+
+def _qknorm_call(p, q, k):
+    _same_call(p, ("q", q, (p.N, p.L, p.Hq, p.D), p.q_batch, p.q_row), ("k", k, (p.N, p.L, p.Hk, p.D), p.k_batch, p.k_row))
+
+
+def qknorm_forward(p: dcn4_qknorm_params, q, k, wq=None, wk=None, pos=None, inv_freq=None):
+    """(q_out [N, L, Hq, D], k_out [N, L, Hk, D]): the heads of q and k RMS-normed, weighted and
+    rotated by their positions, for CUDA tensors as qknorm_params_for takes them."""
+    import torch
+    _qknorm_call(p, q, k)
+    qo = torch.empty((p.N, p.L, p.Hq, p.D), dtype=q.dtype, device=q.device)
+    ko = torch.empty((p.N, p.L, p.Hk, p.D), dtype=q.dtype, device=q.device)
+    with _on_device(q):
+        check(dcn4_qknorm_forward(p, q.data_ptr(), k.data_ptr(), _ptr(wq), _ptr(wk), _ptr(pos), _ptr(inv_freq),
+                                  qo.data_ptr(), ko.data_ptr(), _stream_handle(q.device)))
+    return qo, ko
+
+
+def qknorm_backward(p: dcn4_qknorm_params, q, k, wq, wk, pos, inv_freq, grad_q_out, grad_k_out):
+    """(grad_q, grad_k, grad_wq or None, grad_wk or None) of qknorm_forward for contiguous
+    gradients of its outputs; a weight that was None gets no gradient."""
+    import torch
+    dev, dt = q.device, q.dtype
+    _qknorm_call(p, q, k)
+    _dense("grad_q_out", grad_q_out, (p.N, p.L, p.Hq, p.D), dt, dev)
+    _dense("grad_k_out", grad_k_out, (p.N, p.L, p.Hk, p.D), dt, dev)
+    gq, gk = torch.empty_like(grad_q_out), torch.empty_like(grad_k_out)
+    gwq = torch.empty_like(wq) if wq is not None else None
+    gwk = torch.empty_like(wk) if wk is not None else None
+    need = dcn4_qknorm_backward_workspace_size(p) if wq is not None or wk is not None else 0
+    ws = _workspace(need, q)
+    with _on_device(q):
+        check(dcn4_qknorm_backward(p, q.data_ptr(), k.data_ptr(), _ptr(wq), _ptr(wk), _ptr(pos), _ptr(inv_freq),
+                                   grad_q_out.data_ptr(), grad_k_out.data_ptr(), gq.data_ptr(), gk.data_ptr(),
+                                   _ptr(gwq), _ptr(gwk), _ptr(ws), need, _stream_handle(dev)))
+    return gq, gk, gwq, gwk
+
+
 def backward_diagnostics(p: dcn4_params, workspace) -> dict:
     """Fallback counters of the last backward on `workspace` (a uint8 CUDA tensor)."""
     st, c = dcn4_backward_diagnostics(p, workspace.data_ptr(), workspace.numel(), _stream_handle(workspace.device))
@@ -529,6 +855,8 @@ def _autograd_function():
 _DCNV4_CORE = None
 _DCNV4_CORE_LINEAR = None
 _DCNV4_CORE_PROJ = None
+_BAND = None
+_QKNORM = None
 
 
 def _autograd_function_proj():
@@ -593,6 +921,81 @@ def _autograd_function_linear():
             return grad_value, grad_x, grad_w, grad_b, None
 
     return DCNv4CoreLinear
+
+
+def _autograd_function_band():
+    import torch
+    from torch.autograd.function import once_differentiable
+
+    class BandAttention(torch.autograd.Function):
+        """Dense attention over a band of keys as a torch.autograd.Function: dcn4_band_forward,
+        keeping its output and log sums, and dcn4_band_backward."""
+
+        @staticmethod
+        def forward(ctx, q, k, v, bias, buckets, q_start, q_len, k_len, p):
+            out, lse = band_forward(p, q, k, v, bias, buckets, q_start, q_len, k_len)
+            ctx.save_for_backward(q, k, v, bias, buckets, q_start, q_len, k_len, out, lse)
+            ctx.p = p
+            return out
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, grad_out):
+            q, k, v, bias, buckets, q_start, q_len, k_len, out, lse = ctx.saved_tensors
+            grads = band_backward(ctx.p, q, k, v, out, lse, grad_out.contiguous(), bias, buckets, q_start, q_len,
+                                  k_len, want_bias=ctx.needs_input_grad[3])
+            return grads + (None,) * 5
+
+    return BandAttention
+
+
+def _autograd_function_qknorm():
+    import torch
+    from torch.autograd.function import once_differentiable
+
+    class QkNorm(torch.autograd.Function):
+        """RMS norm and rotation of query and key heads as a torch.autograd.Function:
+        dcn4_qknorm_forward and dcn4_qknorm_backward, which reads the inputs again."""
+
+        @staticmethod
+        def forward(ctx, q, k, wq, wk, pos, inv_freq, p):
+            ctx.save_for_backward(q, k, wq, wk, pos, inv_freq)
+            ctx.p = p
+            return qknorm_forward(p, q, k, wq, wk, pos, inv_freq)
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, grad_q_out, grad_k_out):
+            q, k, wq, wk, pos, inv_freq = ctx.saved_tensors
+            grads = qknorm_backward(ctx.p, q, k, wq, wk, pos, inv_freq, grad_q_out.contiguous(),
+                                    grad_k_out.contiguous())
+            return grads + (None,) * 3
+
+    return QkNorm
+
+
+def band_attention(q, k, v, *, left=-1, right=-1, sinks=0, scale=None, bias=None, buckets=None, q_start=None,
+                   q_len=None, k_len=None):
+    """out [N, Lq, Hq, D] = dense attention of q [N, Lq, Hq, D] to the keys k, v [N, Lk, Hk, D] in a band
+    around each query (`left` behind and `right` ahead of it, -1: all; the first `sinks` keys stay
+    visible behind the window), with a learned bias [nb, Hq] by the buckets [2M + 1] of the relative
+    position; differentiable in q, k, v and bias (torch.autograd)."""
+    global _BAND
+    p = band_params_for(q, k, v, left=left, right=right, sinks=sinks, scale=scale, bias=bias, buckets=buckets,
+                        q_start=q_start, q_len=q_len, k_len=k_len)
+    if _BAND is None:
+        _BAND = _autograd_function_band()
+    return _BAND.apply(q, k, v, bias, buckets, q_start, q_len, k_len, p)
+
+
+def qk_norm_rotate(q, k, wq=None, wk=None, pos=None, inv_freq=None, *, interleaved: bool = False, eps: float = 1e-6):
+    """(q, k) with every head RMS-normed, weighted (wq, wk [D] or None) and its first 2 * len(inv_freq)
+    entries rotated by pos [N, L] or [N, L, axes]; differentiable in q, k, wq and wk (torch.autograd)."""
+    global _QKNORM
+    p = qknorm_params_for(q, k, wq, wk, pos, inv_freq, interleaved=interleaved, eps=eps)
+    if _QKNORM is None:
+        _QKNORM = _autograd_function_qknorm()
+    return _QKNORM.apply(q, k, wq, wk, pos, inv_freq, p)
 
 
 def dcnv4_core(value, offset_mask, *, group: int, kernel=3, stride=1, pad=1, dilation=1,

@@ -12,6 +12,7 @@
 #include <algorithm>
 
 #include "dcn4.h"
+#include "dcn4_band.cuh"
 #include "dcn4_common.cuh"
 
 namespace {
@@ -325,6 +326,123 @@ int make_attn_geometry(const dcn4_attn_params* p, bool wide, dcn4::Geometry* g) 
         return fail(DCN4_ERR_UNSUPPORTED, "K=%d points and P=%d rows do not fit shared memory", p->K, p->P);
     const long long qb = std::max(1LL, static_cast<long long>(kTargetThreads) / (p->G * nslice));
     if ((queries + qb - 1) / qb > 0x7fffffffLL) return fail(DCN4_ERR_UNSUPPORTED, "grid too large");
+    return DCN4_OK;
+}
+
+// Validates p and fills the band attention's geometry (no pointers).
+int make_band(const dcn4_band_params* p, dcn4::BandArgs* a) {
+    if (!p) return fail(DCN4_ERR_NULL, "params is NULL");
+    if (p->dtype != DCN4_F32 && p->dtype != DCN4_F16 && p->dtype != DCN4_BF16)
+        return fail(DCN4_ERR_DTYPE, "dtype %d is not a dcn4_dtype", p->dtype);
+    if (p->N < 0 || p->Lq < 0 || p->Lk < 0 || p->Hq < 1 || p->Hk < 1 || p->D < 1)
+        return fail(DCN4_ERR_BAD_SHAPE, "need N, Lq, Lk >= 0 and Hq, Hk, D >= 1 (got N=%d Lq=%d Lk=%d Hq=%d Hk=%d D=%d)",
+                    p->N, p->Lq, p->Lk, p->Hq, p->Hk, p->D);
+    if (p->Hq % p->Hk != 0) return fail(DCN4_ERR_BAD_SHAPE, "Hq=%d is not a multiple of Hk=%d", p->Hq, p->Hk);
+    if (p->left < -1 || p->right < -1 || p->sinks < 0)
+        return fail(DCN4_ERR_BAD_SHAPE, "need left, right >= -1 and sinks >= 0");
+    if (!std::isfinite(p->scale)) return fail(DCN4_ERR_BAD_SHAPE, "scale is not finite");
+    if (p->nb < 0) return fail(DCN4_ERR_BAD_SHAPE, "nb must be >= 0");
+    if (p->nb > 0 && p->M < 1) return fail(DCN4_ERR_BAD_SHAPE, "a relative bias needs a reach M >= 1");
+    if (p->nb > dcn4::kBandMaxBuckets || (p->nb > 0 && p->M > dcn4::kBandMaxReach))
+        return fail(DCN4_ERR_UNSUPPORTED, "at most %d buckets and a reach of %d", dcn4::kBandMaxBuckets, dcn4::kBandMaxReach);
+    const int eb = elem_bytes(p->dtype);
+    if (p->D * static_cast<long long>(eb) % 16 != 0 || p->D > 128)
+        return fail(DCN4_ERR_UNSUPPORTED, "D=%d: D*sizeof(dtype) must be a multiple of 16 and D <= 128", p->D);
+    if (p->Hq / p->Hk > 128) return fail(DCN4_ERR_UNSUPPORTED, "Hq/Hk must be <= 128");
+    if (p->Lq >= dcn4::kBandMaxLen || p->Lk >= dcn4::kBandMaxLen)
+        return fail(DCN4_ERR_UNSUPPORTED, "Lq and Lk must be < 2^28");
+    const long long nmax = 1LL << 30;  // rows are counted in 32 bits, a tile past the last one too
+    if (p->N && (static_cast<long long>(p->Lq) * p->Hq > nmax / p->N || static_cast<long long>(p->Lk) * p->Hk > nmax / p->N ||
+                 p->Hq > nmax / p->N))
+        return fail(DCN4_ERR_UNSUPPORTED, "N*Hq, N*Lq*Hq and N*Lk*Hk must be <= 2^30");
+    const long long st[6] = {p->q_batch, p->q_row, p->k_batch, p->k_row, p->v_batch, p->v_row};
+    for (long long s : st) {
+        if (s < 0 || s >= (1LL << 38)) return fail(DCN4_ERR_BAD_SHAPE, "strides must be >= 0 and < 2^38 elements");
+        if (s * eb % 16 != 0) return fail(DCN4_ERR_UNSUPPORTED, "strides must be multiples of 16 bytes");
+    }
+    const long long qd = static_cast<long long>(p->Hq) * p->D, kd = static_cast<long long>(p->Hk) * p->D;
+    if ((p->q_row && p->q_row < qd) || (p->k_row && p->k_row < kd) || (p->v_row && p->v_row < kd))
+        return fail(DCN4_ERR_BAD_SHAPE, "a token's stride must hold its heads");
+    memset(a, 0, sizeof *a);
+    a->N = p->N; a->Lq = p->Lq; a->Lk = p->Lk; a->Hq = p->Hq; a->Hk = p->Hk; a->G = p->Hq / p->Hk; a->D = p->D;
+    // a limit that no pair reaches is no limit (positions differ by less than 2^30)
+    a->left = p->left < 0 ? dcn4::kBandFar : std::min(p->left, dcn4::kBandFar);
+    a->right = p->right < 0 ? dcn4::kBandFar : std::min(p->right, dcn4::kBandFar);
+    a->sinks = std::min(p->sinks, p->Lk);
+    a->scale = p->scale;
+    a->nb = p->nb; a->M = p->nb ? p->M : 0; a->dtype = p->dtype;
+    a->q_row = p->q_row ? p->q_row : qd;
+    a->k_row = p->k_row ? p->k_row : kd;
+    a->v_row = p->v_row ? p->v_row : kd;
+    a->q_batch = p->q_batch ? p->q_batch : a->q_row * p->Lq;
+    a->k_batch = p->k_batch ? p->k_batch : a->k_row * p->Lk;
+    a->v_batch = p->v_batch ? p->v_batch : a->v_row * p->Lk;
+    return DCN4_OK;
+}
+
+// The pointers every band call has; sizes are not empty.
+int band_pointers(dcn4::BandArgs* a, const void* q, const void* k, const void* v, const void* bias, const int* buckets,
+                  const int* q_start, const int* q_len, const int* k_len) {
+    if (!q || !k || !v) return fail(DCN4_ERR_NULL, "q, k and v must be non-NULL");
+    if ((a->nb > 0) != (bias != nullptr) || (a->nb > 0) != (buckets != nullptr))
+        return fail(DCN4_ERR_NULL, "bias and buckets must be given with nb > 0, and only then");
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(bias) || !aligned16(buckets))
+        return fail(DCN4_ERR_MISALIGNED, "every pointer must be 16-byte aligned");
+    for (const int* i : {q_start, q_len, k_len})
+        if (reinterpret_cast<uintptr_t>(i) & 3u) return fail(DCN4_ERR_MISALIGNED, "q_start, q_len and k_len must be 4-byte aligned");
+    a->q = q; a->k = k; a->v = v; a->bias = bias; a->buckets = buckets;
+    a->q_start = q_start; a->q_len = q_len; a->k_len = k_len;
+    return DCN4_OK;
+}
+
+int check_workspace(size_t need, const void* workspace, size_t workspace_bytes) {
+    if (need && (!workspace || workspace_bytes < need))
+        return fail(DCN4_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace_bytes);
+    if (need && !aligned16(workspace)) return fail(DCN4_ERR_MISALIGNED, "workspace must be 16-byte aligned");
+    return DCN4_OK;
+}
+
+int make_qknorm(const dcn4_qknorm_params* p, dcn4::QkNormArgs* a) {
+    if (!p) return fail(DCN4_ERR_NULL, "params is NULL");
+    if (p->dtype != DCN4_F32 && p->dtype != DCN4_F16 && p->dtype != DCN4_BF16)
+        return fail(DCN4_ERR_DTYPE, "dtype %d is not a dcn4_dtype", p->dtype);
+    if (p->N < 0 || p->L < 0 || p->Hq < 0 || p->Hk < 0 || p->D < 1 || (p->Hq == 0 && p->Hk == 0))
+        return fail(DCN4_ERR_BAD_SHAPE, "need N, L, Hq, Hk >= 0, a head and D >= 1 (got N=%d L=%d Hq=%d Hk=%d D=%d)", p->N,
+                    p->L, p->Hq, p->Hk, p->D);
+    if (p->axes != 1 && p->axes != 2) return fail(DCN4_ERR_BAD_SHAPE, "axes must be 1 or 2");
+    if (p->interleaved != 0 && p->interleaved != 1) return fail(DCN4_ERR_BAD_SHAPE, "interleaved must be 0 or 1");
+    if (p->R < 0 || p->R > p->D || p->R % (2 * p->axes) != 0)
+        return fail(DCN4_ERR_BAD_SHAPE, "R=%d must be a multiple of 2*axes and <= D", p->R);
+    if (!std::isfinite(p->eps) || !(p->eps > 0.f)) return fail(DCN4_ERR_BAD_SHAPE, "eps must be > 0");
+    const int eb = elem_bytes(p->dtype);
+    if (p->D * static_cast<long long>(eb) % 16 != 0 || p->D > 256)
+        return fail(DCN4_ERR_UNSUPPORTED, "D=%d: D*sizeof(dtype) must be a multiple of 16 and D <= 256", p->D);
+    if (static_cast<long long>(p->Hq) + p->Hk > 65536) return fail(DCN4_ERR_UNSUPPORTED, "at most 65536 heads");
+    if (static_cast<long long>(p->N) * p->L > (1LL << 40)) return fail(DCN4_ERR_UNSUPPORTED, "N*L too large");
+    for (long long s : {p->q_batch, p->q_row, p->k_batch, p->k_row}) {
+        if (s < 0 || s >= (1LL << 38)) return fail(DCN4_ERR_BAD_SHAPE, "strides must be >= 0 and < 2^38 elements");
+        if (s * eb % 16 != 0) return fail(DCN4_ERR_UNSUPPORTED, "strides must be multiples of 16 bytes");
+    }
+    const long long qd = static_cast<long long>(p->Hq) * p->D, kd = static_cast<long long>(p->Hk) * p->D;
+    if ((p->q_row && p->q_row < qd) || (p->k_row && p->k_row < kd))
+        return fail(DCN4_ERR_BAD_SHAPE, "a token's stride must hold its heads");
+    memset(a, 0, sizeof *a);
+    a->N = p->N; a->L = p->L; a->Hq = p->Hq; a->Hk = p->Hk; a->D = p->D; a->R = p->R; a->axes = p->axes;
+    a->interleaved = p->interleaved; a->eps = p->eps; a->dtype = p->dtype;
+    a->q_row = p->q_row ? p->q_row : qd;
+    a->k_row = p->k_row ? p->k_row : kd;
+    a->q_batch = p->q_batch ? p->q_batch : a->q_row * p->L;
+    a->k_batch = p->k_batch ? p->k_batch : a->k_row * p->L;
+    return DCN4_OK;
+}
+
+int qknorm_pointers(dcn4::QkNormArgs* a, const void* q, const void* k, const void* wq, const void* wk, const float* pos,
+                    const float* inv_freq) {
+    if ((a->Hq && !q) || (a->Hk && !k)) return fail(DCN4_ERR_NULL, "q and k must be non-NULL");
+    if (a->R && (!pos || !inv_freq)) return fail(DCN4_ERR_NULL, "a rotation needs pos and inv_freq");
+    if (!aligned16(q) || !aligned16(k) || !aligned16(wq) || !aligned16(wk) || !aligned16(pos) || !aligned16(inv_freq))
+        return fail(DCN4_ERR_MISALIGNED, "every pointer must be 16-byte aligned");
+    a->q = q; a->k = k; a->wq = wq; a->wk = wk; a->pos = pos; a->inv_freq = inv_freq;
     return DCN4_OK;
 }
 
@@ -683,6 +801,161 @@ int dcn4_attn_backward(const dcn4_attn_params* p, const void* value, const float
     e = dcn4::launch_attn_backward(g, p->dtype, p->Nq, value, ref_points, offset_logits, grad_out, grad_value,
                                    grad_offset_logits, acc, s);
     if (e != cudaSuccess) return fail(DCN4_ERR_LAUNCH, "attention backward launch: %s", cudaGetErrorString(e));
+    return DCN4_OK;
+}
+
+int dcn4_band_check_params(const dcn4_band_params* p) {
+    dcn4::BandArgs a;
+    return make_band(p, &a);
+}
+
+int dcn4_rel_buckets(int nb, int M, int both, int* table) {
+    if (!table) return fail(DCN4_ERR_NULL, "table is NULL");
+    if (nb < 1 || M < 1 || (both && nb % 2 != 0))
+        return fail(DCN4_ERR_BAD_SHAPE, "need nb, M >= 1, and nb even for both sides");
+    if (nb > dcn4::kBandMaxBuckets || M > dcn4::kBandMaxReach)
+        return fail(DCN4_ERR_UNSUPPORTED, "at most %d buckets and a reach of %d", dcn4::kBandMaxBuckets, dcn4::kBandMaxReach);
+    const int side = both ? nb / 2 : nb, exact = std::max(1, side / 2);
+    for (int r = -M; r <= M; ++r) {
+        const int d = r < 0 ? -r : r;
+        int b = d;
+        if (d >= M) {
+            b = side - 1;
+        } else if (d >= exact) {
+            // a distance on a border between two buckets belongs to the farther one: neighbouring
+            // integers differ by over 1e-4 here, rounding by less than 1e-9
+            b = exact + static_cast<int>(std::log(static_cast<double>(d) / exact) / std::log(static_cast<double>(M) / exact) *
+                                             (side - exact) + 1e-9);
+        }
+        b = std::min(b, side - 1);
+        if (!both && r > 0) b = 0;
+        table[r + M] = b + (both && r > 0 ? side : 0);
+    }
+    return DCN4_OK;
+}
+
+size_t dcn4_band_forward_workspace_size(const dcn4_band_params* p) {
+    dcn4::BandArgs a;
+    if (make_band(p, &a) != DCN4_OK || !a.N || !a.Lq || !a.Lk) return 0;
+    return dcn4::band_forward_workspace_bytes(a);
+}
+
+int dcn4_band_forward(const dcn4_band_params* p, const void* q, const void* k, const void* v, const void* bias,
+                      const int* buckets, const int* q_start, const int* q_len, const int* k_len, void* out, float* lse,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+    dcn4::BandArgs a;
+    int st = make_band(p, &a);
+    if (st != DCN4_OK) return st;
+    if (!a.N || !a.Lq) return DCN4_OK;
+    if (!out || !lse) return fail(DCN4_ERR_NULL, "out and lse must be non-NULL");
+    if (!aligned16(out) || !aligned16(lse)) return fail(DCN4_ERR_MISALIGNED, "every pointer must be 16-byte aligned");
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (!a.Lk) {
+        e = dcn4::launch_band_empty(a, out, lse, s);
+    } else {
+        st = band_pointers(&a, q, k, v, bias, buckets, q_start, q_len, k_len);
+        if (st == DCN4_OK) st = check_workspace(dcn4::band_forward_workspace_bytes(a), workspace, workspace_bytes);
+        if (st != DCN4_OK) return st;
+        e = dcn4::launch_band_forward(a, out, lse, workspace, s);
+    }
+    if (e != cudaSuccess) return fail(DCN4_ERR_LAUNCH, "band forward launch: %s", cudaGetErrorString(e));
+    return DCN4_OK;
+}
+
+size_t dcn4_band_backward_workspace_size(const dcn4_band_params* p) {
+    dcn4::BandArgs a;
+    if (make_band(p, &a) != DCN4_OK || !a.N || !a.Lq || !a.Lk) return 0;
+    return dcn4::band_backward_workspace_bytes(a);
+}
+
+int dcn4_band_backward(const dcn4_band_params* p, const void* q, const void* k, const void* v, const void* bias,
+                       const int* buckets, const int* q_start, const int* q_len, const int* k_len, const void* out,
+                       const float* lse, const void* grad_out, void* grad_q, void* grad_k, void* grad_v,
+                       void* grad_bias, void* workspace, size_t workspace_bytes, void* stream) {
+    dcn4::BandArgs a;
+    int st = make_band(p, &a);
+    if (st != DCN4_OK) return st;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const size_t eb = static_cast<size_t>(elem_bytes(p->dtype));
+    const size_t nq = static_cast<size_t>(a.N) * a.Lq * a.Hq * a.D, nk = static_cast<size_t>(a.N) * a.Lk * a.Hk * a.D;
+    if (grad_bias && !a.nb) return fail(DCN4_ERR_NULL, "grad_bias without a bias");
+    if ((nq && !grad_q) || (nk && (!grad_k || !grad_v))) return fail(DCN4_ERR_NULL, "grad_q, grad_k and grad_v must be non-NULL");
+    if (!aligned16(grad_q) || !aligned16(grad_k) || !aligned16(grad_v) || !aligned16(grad_bias))
+        return fail(DCN4_ERR_MISALIGNED, "every pointer must be 16-byte aligned");
+    cudaError_t e = cudaSuccess;
+    if (!nq || !nk) {  // no pair at all: every gradient is an empty sum
+        if (nq) e = cudaMemsetAsync(grad_q, 0, nq * eb, s);
+        if (e == cudaSuccess && nk) e = cudaMemsetAsync(grad_k, 0, nk * eb, s);
+        if (e == cudaSuccess && nk) e = cudaMemsetAsync(grad_v, 0, nk * eb, s);
+        if (e == cudaSuccess && grad_bias) e = cudaMemsetAsync(grad_bias, 0, static_cast<size_t>(a.nb) * a.Hq * eb, s);
+        if (e != cudaSuccess) return fail(DCN4_ERR_LAUNCH, "zeroing the gradients: %s", cudaGetErrorString(e));
+        return DCN4_OK;
+    }
+    if (!out || !lse || !grad_out) return fail(DCN4_ERR_NULL, "out, lse and grad_out must be non-NULL");
+    if (!aligned16(out) || !aligned16(lse) || !aligned16(grad_out))
+        return fail(DCN4_ERR_MISALIGNED, "every pointer must be 16-byte aligned");
+    st = band_pointers(&a, q, k, v, bias, buckets, q_start, q_len, k_len);
+    if (st == DCN4_OK) st = check_workspace(dcn4::band_backward_workspace_bytes(a), workspace, workspace_bytes);
+    if (st != DCN4_OK) return st;
+    e = dcn4::launch_band_backward(a, out, lse, grad_out, grad_q, grad_k, grad_v, grad_bias, workspace, s);
+    if (e != cudaSuccess) return fail(DCN4_ERR_LAUNCH, "band backward launch: %s", cudaGetErrorString(e));
+    return DCN4_OK;
+}
+
+int dcn4_qknorm_check_params(const dcn4_qknorm_params* p) {
+    dcn4::QkNormArgs a;
+    return make_qknorm(p, &a);
+}
+
+int dcn4_qknorm_forward(const dcn4_qknorm_params* p, const void* q, const void* k, const void* wq, const void* wk,
+                        const float* pos, const float* inv_freq, void* q_out, void* k_out, void* stream) {
+    dcn4::QkNormArgs a;
+    int st = make_qknorm(p, &a);
+    if (st != DCN4_OK) return st;
+    if (!a.N || !a.L) return DCN4_OK;
+    st = qknorm_pointers(&a, q, k, wq, wk, pos, inv_freq);
+    if (st != DCN4_OK) return st;
+    if ((a.Hq && !q_out) || (a.Hk && !k_out)) return fail(DCN4_ERR_NULL, "q_out and k_out must be non-NULL");
+    if (!aligned16(q_out) || !aligned16(k_out)) return fail(DCN4_ERR_MISALIGNED, "every pointer must be 16-byte aligned");
+    const cudaError_t e = dcn4::launch_qknorm_forward(a, q_out, k_out, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(DCN4_ERR_LAUNCH, "query/key norm launch: %s", cudaGetErrorString(e));
+    return DCN4_OK;
+}
+
+size_t dcn4_qknorm_backward_workspace_size(const dcn4_qknorm_params* p) {
+    dcn4::QkNormArgs a;
+    if (make_qknorm(p, &a) != DCN4_OK) return 0;
+    return dcn4::qknorm_backward_workspace_bytes(a);
+}
+
+int dcn4_qknorm_backward(const dcn4_qknorm_params* p, const void* q, const void* k, const void* wq, const void* wk,
+                         const float* pos, const float* inv_freq, const void* grad_q_out, const void* grad_k_out,
+                         void* grad_q, void* grad_k, void* grad_wq, void* grad_wk, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+    dcn4::QkNormArgs a;
+    int st = make_qknorm(p, &a);
+    if (st != DCN4_OK) return st;
+    const bool weights = grad_wq || grad_wk;
+    if (!aligned16(grad_wq) || !aligned16(grad_wk)) return fail(DCN4_ERR_MISALIGNED, "every pointer must be 16-byte aligned");
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const size_t wbytes = static_cast<size_t>(a.D) * elem_bytes(p->dtype);
+    if (!a.N || !a.L) {
+        cudaError_t z = grad_wq ? cudaMemsetAsync(grad_wq, 0, wbytes, s) : cudaSuccess;
+        if (z == cudaSuccess && grad_wk) z = cudaMemsetAsync(grad_wk, 0, wbytes, s);
+        if (z != cudaSuccess) return fail(DCN4_ERR_LAUNCH, "zeroing the weight gradients: %s", cudaGetErrorString(z));
+        return DCN4_OK;
+    }
+    st = qknorm_pointers(&a, q, k, wq, wk, pos, inv_freq);
+    if (st != DCN4_OK) return st;
+    if ((a.Hq && (!grad_q_out || !grad_q)) || (a.Hk && (!grad_k_out || !grad_k)))
+        return fail(DCN4_ERR_NULL, "grad_q_out, grad_k_out, grad_q and grad_k must be non-NULL");
+    if (!aligned16(grad_q_out) || !aligned16(grad_k_out) || !aligned16(grad_q) || !aligned16(grad_k))
+        return fail(DCN4_ERR_MISALIGNED, "every pointer must be 16-byte aligned");
+    if (weights) st = check_workspace(dcn4::qknorm_backward_workspace_bytes(a), workspace, workspace_bytes);
+    if (st != DCN4_OK) return st;
+    const cudaError_t e = dcn4::launch_qknorm_backward(a, grad_q_out, grad_k_out, grad_q, grad_k, grad_wq, grad_wk, workspace, s);
+    if (e != cudaSuccess) return fail(DCN4_ERR_LAUNCH, "query/key norm backward launch: %s", cudaGetErrorString(e));
     return DCN4_OK;
 }
 

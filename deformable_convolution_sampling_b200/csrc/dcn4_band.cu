@@ -1,0 +1,122 @@
+// dcn4_band.cu — the band attention's dispatch, workspaces, and the kernels that
+// join partial results.
+#include <cmath>
+
+#include "dcn4_band_parts.cuh"
+#include "dcn4_common.cuh"
+
+namespace dcn4 {
+namespace {
+
+// out = (sum_s o_s e^(m_s - m)) / (sum_s l_s e^(m_s - m)), lse = m + log of that
+// sum: a warp per row, a lane per entry.
+template <typename T>
+__global__ void __launch_bounds__(256) join_kernel(BandArgs a, int splits, BandPart part, T* __restrict__ out,
+                                                   float* __restrict__ lse, long long rows) {
+    const long long r = blockIdx.x * 8ll + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (r >= rows) return;
+    const float2* ml = part.ml + r * splits;
+    float m = -INFINITY;
+    for (int s = 0; s < splits; ++s) m = fmaxf(m, ml[s].x);
+    const float ref = m == -INFINITY ? 0.f : m;
+    float l = 0.f, o[4] = {};
+    const float* po = part.o + r * splits * a.D;
+    for (int s = 0; s < splits; ++s) {
+        const float2 v = ml[s];
+        if (v.y == 0.f) continue;  // this range holds nothing the row sees
+        const float f = expf(v.x - ref);
+        l += v.y * f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            if (lane + 32 * c < a.D) o[c] = fmaf(po[static_cast<long long>(s) * a.D + lane + 32 * c], f, o[c]);
+    }
+    const int i = static_cast<int>(r % a.Lq);
+    const long long nh = r / a.Lq, n = nh / a.Hq, h = nh - n * a.Hq;
+    const float f = l == 0.f ? 0.f : 1.f / l;
+    T* to = out + ((n * a.Lq + i) * a.Hq + h) * a.D;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        if (lane + 32 * c < a.D) to[lane + 32 * c] = from_f32<T>(o[c] * f);
+    if (lane == 0) lse[r] = l == 0.f ? -INFINITY : m + logf(l);
+}
+
+// A warp per entry of gbias: its parts of every image and block, in a fixed order.
+template <typename T>
+__global__ void __launch_bounds__(256) bias_sum_kernel(BandArgs a, const float* __restrict__ bpart, int blocks, int heads,
+                                                       T* __restrict__ gbias) {
+    const int e = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (e >= a.nb * a.Hq) return;
+    const int b = e / a.Hq, h = e - b * a.Hq, grp = h / heads, in = h - grp * heads, groups = a.Hq / heads;
+    float s = 0.f;
+    const long long count = static_cast<long long>(a.N) * blocks;
+    for (long long c = lane; c < count; c += 32) {
+        const long long n = c / blocks, blk = c - n * blocks;
+        s += bpart[(((n * groups + grp) * blocks + blk) * a.nb + b) * heads + in];
+    }
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) gbias[e] = from_f32<T>(s);
+}
+
+__global__ void __launch_bounds__(256) no_keys_kernel(float* __restrict__ lse, long long rows) {
+    const long long r = blockIdx.x * 256ll + threadIdx.x;
+    if (r < rows) lse[r] = -INFINITY;
+}
+
+size_t round256(size_t b) { return (b + 255) / 256 * 256; }
+
+size_t delta_bytes(const BandArgs& a) { return round256(static_cast<size_t>(band_rows(a)) * sizeof(float)); }
+
+}  // namespace
+
+cudaError_t launch_band_join(const BandArgs& a, int splits, BandPart part, void* out, float* lse, cudaStream_t stream) {
+    const long long rows = band_rows(a);
+    const unsigned grid = static_cast<unsigned>((rows + 7) / 8);
+    switch (a.dtype) {
+        case 0: join_kernel<float><<<grid, 256, 0, stream>>>(a, splits, part, static_cast<float*>(out), lse, rows); break;
+        case 1: join_kernel<__half><<<grid, 256, 0, stream>>>(a, splits, part, static_cast<__half*>(out), lse, rows); break;
+        case 2: join_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(a, splits, part, static_cast<__nv_bfloat16*>(out), lse, rows); break;
+        default: return cudaErrorInvalidValue;
+    }
+    return cudaGetLastError();
+}
+
+cudaError_t launch_band_bias_sum(const BandArgs& a, const float* bpart, int blocks, int heads, void* gbias,
+                                 cudaStream_t stream) {
+    const unsigned grid = static_cast<unsigned>((a.nb * a.Hq + 7) / 8);
+    switch (a.dtype) {
+        case 0: bias_sum_kernel<float><<<grid, 256, 0, stream>>>(a, bpart, blocks, heads, static_cast<float*>(gbias)); break;
+        case 1: bias_sum_kernel<__half><<<grid, 256, 0, stream>>>(a, bpart, blocks, heads, static_cast<__half*>(gbias)); break;
+        case 2: bias_sum_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(a, bpart, blocks, heads, static_cast<__nv_bfloat16*>(gbias)); break;
+        default: return cudaErrorInvalidValue;
+    }
+    return cudaGetLastError();
+}
+
+cudaError_t launch_band_empty(const BandArgs& a, void* out, float* lse, cudaStream_t stream) {
+    const long long rows = band_rows(a);
+    const cudaError_t e = cudaMemsetAsync(out, 0, static_cast<size_t>(rows) * a.D * (a.dtype == 0 ? 4 : 2), stream);
+    if (e != cudaSuccess) return e;
+    no_keys_kernel<<<static_cast<unsigned>((rows + 255) / 256), 256, 0, stream>>>(lse, rows);
+    return cudaGetLastError();
+}
+
+size_t band_forward_workspace_bytes(const BandArgs& a) { return round256(band_part_bytes(a, simt_splits(a))); }
+
+size_t band_backward_workspace_bytes(const BandArgs& a) {
+    const size_t parts = static_cast<size_t>(a.N) * a.Hk * simt_row_blocks(a) * a.nb * a.G;
+    return delta_bytes(a) + round256(parts * sizeof(float));
+}
+
+cudaError_t launch_band_forward(const BandArgs& a, void* out, float* lse, void* ws, cudaStream_t stream) {
+    return launch_band_simt_forward(a, out, lse, ws, stream);
+}
+
+cudaError_t launch_band_backward(const BandArgs& a, const void* out, const float* lse, const void* gout, void* gq,
+                                 void* gk, void* gv, void* gbias, void* ws, cudaStream_t stream) {
+    float* delta = static_cast<float*>(ws);
+    float* bpart = reinterpret_cast<float*>(static_cast<char*>(ws) + delta_bytes(a));
+    return launch_band_simt_backward(a, out, lse, gout, gq, gk, gv, gbias, delta, bpart, stream);
+}
+
+}  // namespace dcn4

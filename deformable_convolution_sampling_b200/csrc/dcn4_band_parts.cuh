@@ -1,0 +1,53 @@
+// dcn4_band_parts.cuh — the band attention's partial results (a long key axis
+// split over CTAs, the bias gradient's part of every CTA), the kernels that join
+// them, and the launchers of its forms.  Internal to the band attention.
+#pragma once
+
+#include <algorithm>
+
+#include "dcn4_band.cuh"
+
+namespace dcn4 {
+
+// Partial forwards over ranges of the keys: of row r = (n Hq + h) Lq + i and
+// range s, the unnormalised output o[r splits + s][D] with its running maximum
+// and sum ml[r splits + s].
+struct BandPart {
+    float* o;
+    float2* ml;
+};
+inline long long band_rows(const BandArgs& a) { return static_cast<long long>(a.N) * a.Hq * a.Lq; }
+inline size_t band_part_bytes(const BandArgs& a, int splits) {
+    return splits > 1 ? static_cast<size_t>(band_rows(a)) * splits * (a.D * sizeof(float) + sizeof(float2)) : 0;
+}
+inline BandPart band_part(const BandArgs& a, int splits, void* ws) {
+    BandPart p;
+    p.ml = static_cast<float2*>(ws);
+    p.o = reinterpret_cast<float*>(p.ml + band_rows(a) * splits);
+    return p;
+}
+
+// Ranges of the keys for `ctas` CTAs whose `queries` neighbouring queries visit
+// tiles of `bn` keys: enough to put `per_sm` CTAs on every SM, none shorter than
+// four tiles (the join reads a row of fp32 a range back).
+inline int band_splits(const BandArgs& a, long long ctas, int queries, int bn, int per_sm) {
+    const long long span = std::min<long long>(a.Lk, static_cast<long long>(std::min(a.left, kBandMaxLen)) +
+                                                         std::min(a.right, kBandMaxLen) + queries + a.sinks);
+    const long long tiles = (span + bn - 1) / bn;
+    const long long want = (static_cast<long long>(per_sm) * kBandSms + ctas - 1) / std::max<long long>(ctas, 1);
+    return static_cast<int>(std::max<long long>(1, std::min<long long>(std::min<long long>(want, tiles / 4), 256)));
+}
+
+// out and lse of every row from its parts.
+cudaError_t launch_band_join(const BandArgs& a, int splits, BandPart part, void* out, float* lse, cudaStream_t stream);
+// gbias[b][h] from parts bpart[(n Hq / heads + group) blocks + block][nb][heads].
+cudaError_t launch_band_bias_sum(const BandArgs& a, const float* bpart, int blocks, int heads, void* gbias,
+                                 cudaStream_t stream);
+
+int simt_row_blocks(const BandArgs& a);
+int simt_splits(const BandArgs& a);
+cudaError_t launch_band_simt_forward(const BandArgs& a, void* out, float* lse, void* ws, cudaStream_t stream);
+cudaError_t launch_band_simt_backward(const BandArgs& a, const void* out, const float* lse, const void* gout, void* gq,
+                                      void* gk, void* gv, void* gbias, float* delta, float* bpart, cudaStream_t stream);
+
+}  // namespace dcn4

@@ -414,6 +414,156 @@ int dcn4_attn_backward(const dcn4_attn_params* p, const void* value, const float
                        const void* offset_logits, const void* grad_out, void* grad_value,
                        void* grad_offset_logits, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Dense attention over a band of keys, with sinks and a relative position bias.
+ *
+ * What stands beside the deformable attention in a layer: the queries of a
+ * decoder attending to one another, the tokens of a map (in raster order)
+ * attending to the rows around them and to a few register tokens, one new
+ * token attending to a cache.  For image n, query i of head h stands at position
+ * p = q_start[n] + i, and sees key j iff
+ *     j < k_len[n],   j - p <= right,   and   p - j <= left or j < sinks
+ * (left, right = -1: no limit; the first `sinks` keys stay visible behind the
+ * window, not ahead of it).  Over the keys it sees,
+ *     s_j = scale * <q_i, k_j> + bias[buckets[clamp(j - p, -M, M) + M], h]
+ *     out_i = sum_j e^{s_j - lse_i} v_j,      lse_i = log sum_j e^{s_j}.
+ * A query that sees nothing, and every query i >= q_len[n], gives out = 0 and
+ * lse = -infinity.  Query head h reads key head h / (Hq / Hk).
+ *
+ * Layouts (a head's D entries and a token's heads contiguous):
+ *   q                [N, Lq, Hq, D]  dtype, images q_batch and tokens q_row elements apart
+ *   k, v             [N, Lk, Hk, D]  dtype, likewise (a cache: Lk of its tokens, k_batch its whole length)
+ *   bias             [nb, Hq]        dtype; NULL iff nb == 0
+ *   buckets          [2 M + 1]       int32, the bucket of relative position -M .. M; an entry
+ *                                    outside [0, nb) means no bias there; NULL iff nb == 0
+ *   q_start, q_len, k_len  [N]       int32, or NULL: Lk - Lq (the last queries stand on the last
+ *                                    keys), Lq, Lk.  Lengths are clamped to [0, Lq] and [0, Lk],
+ *                                    q_start to +-2^28.
+ *   out, grad_out    [N, Lq, Hq, D]  dtype, dense
+ *   lse              [N, Hq, Lq]     fp32
+ *   grad_q, grad_k, grad_v           dtype, dense [N, Lq, Hq, D], [N, Lk, Hk, D], [N, Lk, Hk, D];
+ *                                    rows i >= q_len[n] and keys j >= k_len[n] are written as 0
+ *   grad_bias        [nb, Hq]        dtype
+ *
+ * Keys and values at j >= k_len[n] and queries (and grad_out) at i >= q_len[n]
+ * may hold anything, infinities and NaN too.  A non-finite key or value at j <
+ * k_len[n] reaches the queries that see it, and may reach any that share a tile
+ * of 128 with one that does.
+ *
+ * Precision: products accumulate in fp32, the softmax statistics are fp32.  For
+ * fp16 / bf16 the products run on the tensor cores, whose second operands (the
+ * probabilities e^{s - m} against a running maximum m, and in the backward the
+ * probabilities and their gradients) are rounded to dtype; each output is then
+ * rounded once.  fp32 stays fp32 throughout.  No atomics on sums: results are
+ * the same from call to call.
+ *
+ * Preconditions beyond those of every call (16-byte aligned pointers, q_start,
+ * q_len, k_len 4-byte aligned): Hq a multiple of Hk, Hq / Hk <= 128, D *
+ * sizeof(dtype) a multiple of 16 and D <= 128, strides multiples of 16 bytes,
+ * lengths below 2^28, N * Hq, N * Lq * Hq and N * Lk * Hk at most 2^30, nb <= 1024 and
+ * 1 <= M <= 1024 with a bias.  Empty sizes are fine: Lk == 0 gives out = 0.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    int N, Lq, Lk;        /* images, queries and keys per image                      */
+    int Hq, Hk, D;        /* query heads, key heads, entries of a head               */
+    int left, right;      /* keys seen behind and ahead of a query; -1: all          */
+    int sinks;            /* first keys that stay visible behind the window          */
+    float scale;          /* of the products q.k                                     */
+    int nb, M;            /* buckets and reach of the relative bias; nb = 0: none    */
+    int dtype;            /* dcn4_dtype                                              */
+    long long q_batch, q_row, k_batch, k_row, v_batch, v_row;  /* in elements; 0: dense */
+} dcn4_band_params;
+
+/* Host-only validation of p; returns DCN4_OK or the status a call would return. */
+int dcn4_band_check_params(const dcn4_band_params* p);
+
+/* Fills table[0 .. 2 M] with the buckets of relative positions -M .. M (key minus
+ * query): distances below half of a side's buckets one by one, larger ones by
+ * their logarithm, the last bucket from M on.  both != 0: keys ahead of the query
+ * have the upper nb / 2 buckets (nb even); otherwise all nb are for keys behind it
+ * and every key ahead shares bucket 0.  Host memory; touches no GPU. */
+int dcn4_rel_buckets(int nb, int M, int both, int* table);
+
+/* Bytes of device workspace dcn4_band_forward needs (fp32 partial results of key
+ * ranges where few queries face many keys); 0 if none, or if p is invalid. */
+size_t dcn4_band_forward_workspace_size(const dcn4_band_params* p);
+
+/* Forward: out and lse.  One kernel on `stream`, or two where the keys are split. */
+int dcn4_band_forward(const dcn4_band_params* p, const void* q, const void* k, const void* v, const void* bias,
+                      const int* buckets, const int* q_start, const int* q_len, const int* k_len, void* out, float* lse,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace dcn4_band_backward needs (fp32: one number per query
+ * and head, and with a bias the parts of its gradient); 0 if p is invalid. */
+size_t dcn4_band_backward_workspace_size(const dcn4_band_params* p);
+
+/* Backward for grad_out, from the out and lse of the forward: with D_i = <grad_out_i, out_i>,
+ * p_ij = e^{s_ij - lse_i} and d_ij = p_ij (<grad_out_i, v_j> - D_i),
+ *     grad_q_i = scale sum_j d_ij k_j,   grad_k_j = scale sum_i d_ij q_i,   grad_v_j = sum_i p_ij grad_out_i,
+ *     grad_bias[b, h] = sum of d_ij over the pairs of bucket b and head h
+ * (sums over the images too; grad_k and grad_v also over the query heads of a key
+ * head).  All are overwritten.  grad_bias may be NULL (not wanted).  Launches on
+ * `stream`: a kernel for grad_q, one for grad_k and grad_v, one for grad_bias. */
+int dcn4_band_backward(const dcn4_band_params* p, const void* q, const void* k, const void* v, const void* bias,
+                       const int* buckets, const int* q_start, const int* q_len, const int* k_len, const void* out,
+                       const float* lse, const void* grad_out, void* grad_q, void* grad_k, void* grad_v,
+                       void* grad_bias, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * RMS norm of every query and key head and the position rotation, in one pass.
+ *
+ * For each token and head x (D entries; w = wq for queries, wk for keys):
+ *     y = w * x / sqrt(mean(x^2) + eps)
+ * then the first R entries of y are rotated in R / 2 pairs by the token's position:
+ * pair i is (y_i, y_{i + R/2}), or (y_2i, y_2i+1) with `interleaved`, and
+ *     (a, b) -> (a cos f - b sin f, a sin f + b cos f),   f = pos[axis] * inv_freq[i],
+ * axis 0, or with axes == 2 (positions (x, y), as ref_points have them) axis 0 for
+ * the first half of the pairs and axis 1 for the second.  f is formed and reduced
+ * in 64 bits, the rest is fp32, rounded once.
+ *
+ * Layouts (a head's D entries and a token's heads contiguous):
+ *   q, k           [N, L, Hq, D], [N, L, Hk, D]  dtype, images q_batch / k_batch and tokens
+ *                  q_row / k_row elements apart (parts of one packed projection)
+ *   wq, wk         [D]         dtype, or NULL: ones
+ *   pos            [N, L, axes] fp32; NULL iff R == 0
+ *   inv_freq       [R / 2]     fp32; NULL iff R == 0
+ *   q_out, k_out and every gradient: dense, dtype
+ * Hq or Hk may be 0 (its pointers are then not read).  Preconditions beyond those
+ * of every call: D * sizeof(dtype) a multiple of 16 and D <= 256, R <= D a
+ * multiple of 2 * axes, eps > 0, strides multiples of 16 bytes, heads at most
+ * 65536 in all.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    int N, L;             /* images, tokens per image                                */
+    int Hq, Hk, D;        /* query heads, key heads, entries of a head               */
+    int R;                /* entries of a head that are rotated; 0: none             */
+    int axes;             /* numbers of a position: 1 or 2                           */
+    int interleaved;      /* 0: pairs (i, i + R/2), 1: pairs (2i, 2i + 1)            */
+    float eps;
+    int dtype;            /* dcn4_dtype                                              */
+    long long q_batch, q_row, k_batch, k_row;  /* in elements; 0: dense              */
+} dcn4_qknorm_params;
+
+/* Host-only validation of p; returns DCN4_OK or the status a call would return. */
+int dcn4_qknorm_check_params(const dcn4_qknorm_params* p);
+
+/* Forward: q_out and k_out.  One kernel on `stream`. */
+int dcn4_qknorm_forward(const dcn4_qknorm_params* p, const void* q, const void* k, const void* wq, const void* wk,
+                        const float* pos, const float* inv_freq, void* q_out, void* k_out, void* stream);
+
+/* Bytes of device workspace dcn4_qknorm_backward needs when a weight's gradient is
+ * wanted (fp32 sums of each CTA); 0 if p is invalid. */
+size_t dcn4_qknorm_backward_workspace_size(const dcn4_qknorm_params* p);
+
+/* Backward: grad_q and grad_k from the gradients of q_out and k_out (the inputs are
+ * read again, nothing of the forward is kept), and the sums over all tokens and heads
+ * grad_wq and grad_wk, each of which may be NULL (not wanted; both NULL need no
+ * workspace).  Sums are taken in a fixed order.  One kernel, and one for the weights. */
+int dcn4_qknorm_backward(const dcn4_qknorm_params* p, const void* q, const void* k, const void* wq, const void* wk,
+                         const float* pos, const float* inv_freq, const void* grad_q_out, const void* grad_k_out,
+                         void* grad_q, void* grad_k, void* grad_wq, void* grad_wk, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
 /* Name of a dcn4_status. */
 const char* dcn4_status_string(int status);
 
