@@ -179,6 +179,7 @@ def _load() -> ctypes.CDLL:
         "dcn4_band_forward": ([BP] + [vp] * 11 + [ctypes.c_size_t, vp], ctypes.c_int),
         "dcn4_band_backward_workspace_size": ([BP], ctypes.c_size_t),
         "dcn4_band_backward": ([BP] + [vp] * 16 + [ctypes.c_size_t, vp], ctypes.c_int),
+        "dcn4_band_status": ([ctypes.c_int], ctypes.c_int),
         "dcn4_qknorm_check_params": ([QP], ctypes.c_int),
         "dcn4_qknorm_forward": ([QP] + [vp] * 9, ctypes.c_int),
         "dcn4_qknorm_backward_workspace_size": ([QP], ctypes.c_size_t),
@@ -337,6 +338,10 @@ def dcn4_band_backward(p: dcn4_band_params, q, k, v, bias, buckets, q_start, q_l
                        grad_k, grad_v, grad_bias, workspace, workspace_bytes: int, stream=None) -> int:
     return lib.dcn4_band_backward(ctypes.byref(p), q, k, v, bias, buckets, q_start, q_len, k_len, out, lse, grad_out,
                                   grad_q, grad_k, grad_v, grad_bias, workspace, workspace_bytes, stream)
+
+
+def dcn4_band_status(reset: bool = False) -> int:
+    return lib.dcn4_band_status(1 if reset else 0)
 
 
 def dcn4_qknorm_check_params(p: dcn4_qknorm_params) -> int:

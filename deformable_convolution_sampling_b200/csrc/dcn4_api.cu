@@ -903,6 +903,13 @@ int dcn4_band_backward(const dcn4_band_params* p, const void* q, const void* k, 
     return DCN4_OK;
 }
 
+int dcn4_band_status(int reset) {
+    unsigned v = 0u;
+    const cudaError_t e = dcn4::band_status(&v, reset != 0);
+    if (e != cudaSuccess) return fail(DCN4_ERR_LAUNCH, "reading the band attention's status word: %s", cudaGetErrorString(e));
+    return static_cast<int>(v & 0x7fffffffu);
+}
+
 int dcn4_qknorm_check_params(const dcn4_qknorm_params* p) {
     dcn4::QkNormArgs a;
     return make_qknorm(p, &a);

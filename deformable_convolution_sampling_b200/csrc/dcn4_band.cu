@@ -101,7 +101,11 @@ cudaError_t launch_band_empty(const BandArgs& a, void* out, float* lse, cudaStre
     return cudaGetLastError();
 }
 
-size_t band_forward_workspace_bytes(const BandArgs& a) { return round256(band_part_bytes(a, simt_splits(a))); }
+size_t band_forward_workspace_bytes(const BandArgs& a) {
+    return round256(a.dtype == 0 ? band_part_bytes(a, simt_splits(a)) : band_fwd_tc_part_bytes(a));
+}
+
+cudaError_t band_status(unsigned* status, bool reset) { return band_fwd_status(status, reset); }
 
 size_t band_backward_workspace_bytes(const BandArgs& a) {
     const size_t parts = static_cast<size_t>(a.N) * a.Hk * simt_row_blocks(a) * a.nb * a.G;
@@ -109,7 +113,7 @@ size_t band_backward_workspace_bytes(const BandArgs& a) {
 }
 
 cudaError_t launch_band_forward(const BandArgs& a, void* out, float* lse, void* ws, cudaStream_t stream) {
-    return launch_band_simt_forward(a, out, lse, ws, stream);
+    return a.dtype == 0 ? launch_band_simt_forward(a, out, lse, ws, stream) : launch_band_fwd_tc(a, out, lse, ws, stream);
 }
 
 cudaError_t launch_band_backward(const BandArgs& a, const void* out, const float* lse, const void* gout, void* gq,

@@ -22,8 +22,8 @@ inline size_t band_part_bytes(const BandArgs& a, int splits) {
 }
 inline BandPart band_part(const BandArgs& a, int splits, void* ws) {
     BandPart p;
-    p.ml = static_cast<float2*>(ws);
-    p.o = reinterpret_cast<float*>(p.ml + band_rows(a) * splits);
+    p.o = static_cast<float*>(ws);  // rows of D floats: 16-byte aligned
+    p.ml = reinterpret_cast<float2*>(p.o + band_rows(a) * splits * a.D);
     return p;
 }
 
@@ -44,6 +44,12 @@ cudaError_t launch_band_join(const BandArgs& a, int splits, BandPart part, void*
 cudaError_t launch_band_bias_sum(const BandArgs& a, const float* bpart, int blocks, int heads, void* gbias,
                                  cudaStream_t stream);
 
+// 16-bit types on the tensor cores (dcn4_band_fwd_tc.cu).
+size_t band_fwd_tc_part_bytes(const BandArgs& a);
+cudaError_t launch_band_fwd_tc(const BandArgs& a, void* out, float* lse, void* ws, cudaStream_t stream);
+cudaError_t band_fwd_status(unsigned* status, bool reset);
+
+// Every type on the fp32 pipes (dcn4_band_simt.cu).
 int simt_row_blocks(const BandArgs& a);
 int simt_splits(const BandArgs& a);
 cudaError_t launch_band_simt_forward(const BandArgs& a, void* out, float* lse, void* ws, cudaStream_t stream);

@@ -8,7 +8,9 @@ Band forward: a score is a sum of D products and a bias in fp32, so it is off by
 at most ds = (D + 4) e (scale |q|.|k| + |b|); with |s - m| up to a few hundred,
 e^(s - m) adds (4 + |s - m|) e of itself.  The probabilities that meet the values
 are rounded to the type once (16-bit types), relative to a running maximum that
-may lag (no effect: a rounding is relative).  Sums of Lk terms in fp32: Lk e in
+may lag (no effect: a rounding is relative, but for fp16's steps of 2^-24 below 2^-14:
+half of one off each probability relative to the row's largest, low = 2^-25 e^(max - lse)
+sum |V| on out).  Sums of Lk terms in fp32: Lk e in
 the worst case.  So each p is off by at most rp p with
     rp = u + 2 max_row(ds) + (Lk + 16 + spread) e,
 out by rp (P |V|) + u |out| and lse by rp (without u) plus e |lse|.
@@ -83,7 +85,11 @@ def reference(q, k, v, g=None, *, left=-1, right=-1, sinks=0, scale=None, bias=N
     pv = torch.einsum("nhij,njhd->nhid", p, vv.abs())
     out = torch.einsum("nhij,njhd->nihd", p, vv)
     r = {"out": out, "lse": lse}
-    e_out = (rp * pv).transpose(1, 2) + u * out.abs() * 1.01 + tiny
+    low = 0.0
+    if dtype == "f16" and Lk:
+        top = torch.where(some, s.amax(-1) - torch.where(some, lse, torch.zeros(()).double()), torch.zeros(()).double()).exp()
+        low = 2.0 ** -25 * (top[..., None] * torch.einsum("nhij,njhd->nhid", see.double(), vv.abs())).transpose(1, 2)
+    e_out = (rp * pv).transpose(1, 2) + low + u * out.abs() * 1.01 + tiny
     r["out_tol"] = e_out
     r["lse_tol"] = rp32[..., 0] * 1.01 + 4 * E32 * torch.where(some, lse.abs(), torch.zeros(()).double())
     if g is None:

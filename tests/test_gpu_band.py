@@ -61,7 +61,7 @@ def run(dcn, c, t, backward=True):
                             sinks=c.get("sinks", 0), scale=c.get("scale"), **more)
     out, lse = dcn.band_forward(p, cu["q"], cu["k"], cu["v"], **more)
     grads = dcn.band_backward(p, cu["q"], cu["k"], cu["v"], out, lse, cu["g"], **more) if backward else ()
-    torch.cuda.synchronize()
+    assert dcn.dcn4_band_status() == 0
     return (out, lse) + tuple(grads)
 
 
