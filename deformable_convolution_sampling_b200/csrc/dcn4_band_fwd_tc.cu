@@ -10,11 +10,11 @@
 // second product's operand; its sum is taken in fp32 before the rounding.
 //
 // A CTA holds two tiles of 128 rows (a row is a query of one of the heads that
-// share a key head) and streams tiles of 128 keys past both, or, where a head has
+// share a key head) and streams tiles of keys past both, or, where a head has
 // no more than one tile of rows, lets its two halves take the key tiles in turn.
-// Warps 0-3 and 4-7 each own a tile's softmax (thread = row = TMEM lane), warps
-// 8-11 fill operand tiles, one thread of warp 12 issues the MMAs:
-//     S = Q K^T  (both operands in shared memory, 128 x 128 into tensor memory)
+// Warps 0-3 and 4-7 each own a tile's softmax (thread = row = TMEM lane), warp 8
+// loads tiles with TMA, the warps from 9 on issue the MMAs:
+//     S = Q K^T  (both operands in shared memory, into tensor memory)
 //     O += P V   (P written over S in tensor memory as 16-bit pairs)
 // so that one tile's exponentials run under the other's products.  Of a key tile
 // only the 32-column chunks that some row may see are computed; only chunks on the
@@ -26,17 +26,26 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 416, kProducer = 8, kMma = 12;
-constexpr int kSlots = 4;             // ring of operand tiles: K, V, K, V
-constexpr int kLag = 2;               // tiles of cp.async in flight behind the one being issued
+constexpr int kProducer = 8, kMma = 9;
 constexpr float kRescale = 8.f;
-constexpr int kTableExtra = 256;      // the bias table reaches this far past M: no clamp in a chunk that touches [-M, M]
-constexpr int kTableBytes = 28 << 10;
+constexpr int kTableExtra = 160;      // the bias table reaches past M by a tile's rows and a chunk: no clamp in a chunk that touches [-M, M]
 
-// A bounded wait by a whole warp: all of its lanes go on, or none.
-__device__ __forceinline__ bool warp_wait(uint64_t* mbar, uint32_t parity, volatile int* abort) {
-    return __all_sync(0xffffffffu, mbar_wait_or(smem_u32(mbar), parity, abort));
-}
+// Tiles of 64 keys.  Heads up to 128: the scores of two tiles a half in tensor
+// memory, so that the product for tile t + 1 runs under the exponentials of tile t.
+// Heads of up to 64: one, in 256 columns of tensor memory, and two CTAs an SM.
+constexpr int kKeys = 64, kChunks = kKeys / kTcChunk;
+constexpr int kKeyBlock = kKeys * 128;                   // bytes of 64 columns of a key tile
+template <int NB>
+struct Cfg {
+    static constexpr int ahead = NB == 1 ? 1 : 2;        // tiles whose scores are held
+    static constexpr int mma = NB == 1 ? 1 : 2;          // warps that issue: one for both halves, or one for each
+    static constexpr int threads = (kMma + mma) * 32;
+    static constexpr int slots = 4;                      // ring of V of a tile with K of the tile `ahead` on
+    static constexpr int scores = ahead * kKeys;         // columns of a half's scores
+    static constexpr int tmem = NB == 1 ? 256 : 512;
+    static constexpr int ctas = NB == 1 ? 2 : 1;
+    static constexpr int table_bytes = NB == 1 ? 12 << 10 : 28 << 10;
+};
 
 __device__ unsigned g_band_status;    // nonzero once a bounded wait gave up
 
@@ -70,38 +79,33 @@ __device__ __forceinline__ RowBand row_band(const BandArgs& a, int start, int i0
     return b;
 }
 __device__ __forceinline__ bool chunks_of(const RowBand& b, int j0, int& ca, int& cb) {
-    int lo = max(b.lo, j0), hi = min(b.hi, j0 + kTcRows);
-    const int sink = min(b.sink, j0 + kTcRows);
+    int lo = max(b.lo, j0), hi = min(b.hi, j0 + kKeys);
+    const int sink = min(b.sink, j0 + kKeys);
     if (sink > j0) {
         if (lo >= hi) hi = sink;
         lo = j0;
     }
-    ca = (lo - j0) / kTcChunk;
-    cb = (hi - j0 + kTcChunk - 1) / kTcChunk;
+    ca = (lo - j0) >> 5;
+    cb = (hi - j0 + kTcChunk - 1) >> 5;
     return b.any && lo < hi;
 }
 
-struct Row {           // a softmax thread's row
-    int pos;           // position of its query
-    int jlo, jhi;      // keys of its window
-    float m, l;        // reference (log2 units without a bias, natural with one) and sum
-};
-
-// The scores of one chunk: raw products in x; masked ones become -infinity * sign.
-__device__ __forceinline__ bool sees(const Row& r, int sinks, int j) { return j < r.jhi && (j >= r.jlo || j < sinks); }
-
 template <typename T, int NB, bool BIAS>
-__global__ void __launch_bounds__(kThreads, 1)
-    fwd_kernel(BandArgs a, FwdShape sh, T* __restrict__ out, float* __restrict__ lse, BandPart part) {
+__global__ void __launch_bounds__(Cfg<NB>::threads, Cfg<NB>::ctas)
+    fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+               const __grid_constant__ CUtensorMap map_v, BandArgs a, FwdShape sh, T* __restrict__ out,
+               float* __restrict__ lse, BandPart part) {
+    using C = Cfg<NB>;
+    constexpr int kSlots = C::slots, kAhead = C::ahead;
     extern __shared__ __align__(1024) unsigned char band_smem[];
-    __shared__ __align__(8) uint64_t full[kSlots], empty[kSlots], q_full, s_full[2], p_full[2], o_done[2];
+    __shared__ __align__(8) uint64_t full[kSlots], empty[kSlots], raw, q_full, s_full[2][2], p_full[2][2], o_done[2][2], drained[2];
     __shared__ uint32_t taddr_s;
     __shared__ int s_abort;
     __shared__ float2 s_ml[kTcRows];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = static_cast<int>(uniform(tid >> 5)), lane = tid & 31;
     const uint32_t base = (smem_u32(band_smem) + 1023u) & ~1023u;
     const uint32_t qs = base, ring = base + (sh.alt ? 1 : 2) * NB * kTcBlock;
-    float* table = reinterpret_cast<float*>(band_smem + (ring - smem_u32(band_smem)) + kSlots * NB * kTcBlock);
+    float* table = reinterpret_cast<float*>(band_smem + (ring - smem_u32(band_smem)) + kSlots * 2 * NB * kKeyBlock);
 
     int b = blockIdx.x;
     const int sp = b % sh.splits;
@@ -109,30 +113,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int blk = sh.blocks - 1 - b % sh.blocks;  // the longest rows of a causal band first
     b /= sh.blocks;
     const int groups = a.Hq / sh.pack, n = b / groups, grp = b - n * groups, h0 = grp * sh.pack, hk = h0 / a.G;
-    const int klen = band_klen(a, n), qlen = band_qlen(a, n), start = band_start(a, n);
+    const int klen = static_cast<int>(uniform(band_klen(a, n))), qlen = static_cast<int>(uniform(band_qlen(a, n))),
+              start = static_cast<int>(uniform(band_start(a, n)));
     const int tiles = sh.alt ? 1 : 2;
     const int i0 = blk * tiles * sh.tq, i1 = min(i0 + tiles * sh.tq, qlen) - 1;
 
     if (tid == 0) {
         for (int s = 0; s < kSlots; ++s) {
-            mbar_init(smem_u32(&full[s]), 4);
-            mbar_init(smem_u32(&empty[s]), 1);
+            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&empty[s]), C::mma);
         }
-        mbar_init(smem_u32(&q_full), 4);
-        for (int w = 0; w < 2; ++w) {
-            mbar_init(smem_u32(&s_full[w]), 1);
-            mbar_init(smem_u32(&p_full[w]), 4);
-            mbar_init(smem_u32(&o_done[w]), 1);
+        mbar_init(smem_u32(&drained[0]), 1);
+        mbar_init(smem_u32(&drained[1]), 1);
+        mbar_init(smem_u32(&raw), 1);
+        mbar_init(smem_u32(&q_full), 1);
+        for (int w = 0; w < 4; ++w) {
+            mbar_init(smem_u32(&s_full[w >> 1][w & 1]), 1);
+            mbar_init(smem_u32(&p_full[w >> 1][w & 1]), 4);
+            mbar_init(smem_u32(&o_done[w >> 1][w & 1]), 1);
         }
         s_abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    if (warp == kProducer && elect_one()) {
+        prefetch_map(&map_q);
+        prefetch_map(&map_k);
+        prefetch_map(&map_v);
+    }
     if (warp == kMma) {  // S and O of both halves
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&taddr_s)), "r"(512));
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&taddr_s)), "r"(C::tmem));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     if (BIAS) {  // the bias of every head of the tile by relative position
-        for (int e = tid; e < sh.pack * sh.table; e += kThreads) {
+        for (int e = tid; e < sh.pack * sh.table; e += C::threads) {
             const int g = e / sh.table, rel = e - g * sh.table - a.M - kTableExtra;
             const int bk = __ldg(a.buckets + max(-a.M, min(rel, a.M)) + a.M);
             table[e] = static_cast<unsigned>(bk) < static_cast<unsigned>(a.nb)
@@ -142,13 +155,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = taddr_s;
+    const uint32_t tmem = uniform(taddr_s);
     volatile int* abort = &s_abort;
 
     int t0 = 0, t1 = 0;
     BandTiles bt{0, 0, 0};
     if (i0 <= i1) {
-        bt = band_tiles(a, start + i0, start + i1, klen, kTcRows);
+        bt = band_tiles(a, start + i0, start + i1, klen, kKeys);
         const long long cnt = bt.count();
         t0 = static_cast<int>(cnt * sp / sh.splits);
         t1 = static_cast<int>(cnt * (sp + 1) / sh.splits);
@@ -161,260 +174,267 @@ __global__ void __launch_bounds__(kThreads, 1)
     const RowBand rb0 = band_of(0), rb1 = sh.alt ? rb0 : band_of(1);
     auto active = [&](int w, int t, int& ca, int& cb) {
         if (t >= t1 || (sh.alt && ((t - t0) & 1) != w)) return false;
-        return chunks_of(w ? rb1 : rb0, bt.tile(t) * kTcRows, ca, cb);
+        return chunks_of(w ? rb1 : rb0, bt.tile(t) * kKeys, ca, cb);
     };
 
-    if (warp >= kProducer && warp < kMma) {
-        const int pt = tid - kProducer * 32;
-        const T* q = static_cast<const T*>(a.q) + n * a.q_batch + static_cast<long long>(h0) * a.D;
-        const T* k = static_cast<const T*>(a.k) + n * a.k_batch + static_cast<long long>(hk) * a.D;
-        const T* v = static_cast<const T*>(a.v) + n * a.v_batch + static_cast<long long>(hk) * a.D;
-        for (int w = 0; w < tiles && t0 < t1; ++w)
-            load_operand<T, NB>(qs + w * NB * kTcBlock, a.D, kTcRows, q, [&](int r) -> const T* {
-                const int ql = r / sh.pack, i = i0 + w * sh.tq + ql;
-                return ql < sh.tq && i < qlen ? q + i * a.q_row + static_cast<long long>(r - ql * sh.pack) * a.D : nullptr;
-            }, pt);
-        cp_commit();
-        const int items = 2 * (t1 - t0);
-        for (int it = 0; it < items + kLag; ++it) {
-            if (it < items) {
-                const int s = it % kSlots, j0 = bt.tile(t0 + (it >> 1)) * kTcRows;
-                if (!warp_wait(&empty[s], ((it / kSlots) & 1) ^ 1u, abort)) break;
-                const T* src = it & 1 ? v : k;
-                const long long row = it & 1 ? a.v_row : a.k_row;
-                load_operand<T, NB>(ring + s * NB * kTcBlock, a.D, kTcRows, src,
-                                    [&](int r) -> const T* { return j0 + r < klen ? src + (j0 + r) * row : nullptr; }, pt);
-            }
-            cp_commit();
-            if (it >= kLag) {
-                cp_wait<kLag>();
-                fence_async_smem();  // the tensor cores read through the async proxy
-                __syncwarp();
-                if (lane == 0) {
-                    if (it == kLag) mbar_arrive(smem_u32(&q_full));
-                    mbar_arrive(smem_u32(&full[(it - kLag) % kSlots]));
+    if (warp == kProducer) {
+        if (t0 < t1 && elect_one()) {
+            const int bytes = sh.pack * sh.tq * 128;
+            mbar_expect_tx(smem_u32(&q_full), tiles * NB * bytes);
+            for (int w = 0; w < tiles; ++w)
+                for (int c = 0; c < NB; ++c)
+                    tma_load_rows(qs + (w * NB + c) * kTcBlock, &map_q, c * 64, h0, i0 + w * sh.tq, n, smem_u32(&q_full));
+        }
+        // stage i: K of tile i and V of tile i - kAhead
+        int raws = 0;
+        const int cnt = t1 - t0;
+        for (int i = 0; cnt && i < cnt + kAhead; ++i) {
+            const int s = i % kSlots;
+            if (!warp_wait(&empty[s], ((i / kSlots) & 1) ^ 1u, abort)) break;
+            const uint32_t at_k = ring + s * 2 * NB * kKeyBlock, at_v = at_k + NB * kKeyBlock;
+            const bool with_k = i < cnt, with_v = i >= kAhead;
+            const int jv = with_v ? bt.tile(t0 + i - kAhead) * kKeys : 0;
+            // values past the sequence but inside the tensor meet probabilities of 0: clear them (scores are masked)
+            const bool clear = with_v && jv + kKeys > klen && klen < a.Lk;
+            if (elect_one()) {
+                const uint32_t bar = smem_u32(clear ? &raw : &full[s]);
+                mbar_expect_tx(bar, (with_k + with_v) * NB * kKeyBlock);
+                const int jk = with_k ? bt.tile(t0 + i) * kKeys : 0;
+                for (int c = 0; c < NB; ++c) {
+                    if (with_k) tma_load_rows(at_k + c * kKeyBlock, &map_k, c * 64, hk, jk, n, bar);
+                    if (with_v) tma_load_rows(at_v + c * kKeyBlock, &map_v, c * 64, hk, jv, n, bar);
                 }
+            }
+            if (clear) {
+                if (!warp_wait(&raw, raws++ & 1, abort)) break;
+                zero_rows<NB>(at_v, kKeyBlock, max(klen - jv, 0), kKeys, lane);
+                if (elect_one()) mbar_arrive(smem_u32(&full[s]));
             }
         }
-        cp_wait<0>();
-    } else if (warp == kMma) {
-        if (lane == 0 && t0 < t1) {
+    } else if (warp >= kMma) {
+        if (t0 < t1) {
             const int steps = (a.D + 15) / 16;
-            const uint32_t id_o = umma_idesc<T>(kTcRows, steps * 16, 0, 1);
-            bool ok = mbar_wait_or(smem_u32(&q_full), 0u, abort);
-            auto slot = [&](int it) { return ring + (it % kSlots) * NB * kTcBlock; };
-            auto wait_tile = [&](int it) {
-                ok = ok && mbar_wait_or(smem_u32(&full[it % kSlots]), (it / kSlots) & 1, abort);
-                tc_fence_after();
+            // a negative scale turns the products' sign, so that the largest score is the largest product
+            const uint32_t id_s = umma_idesc<T>(kTcRows, 0, 0, 0) | (a.scale < 0.f ? kNegateA : 0u),
+                           id_o = umma_idesc<T>(kTcRows, steps * 16, 0, 1);
+            const uint64_t q_desc = umma_desc_sw128(qs, 16, 1024), k_desc = umma_desc_sw128(ring, 16, 1024),
+                           v_desc = umma_desc_sw128(ring + NB * kKeyBlock, kKeyBlock, 1024);
+            const int w_lo = C::mma == 2 ? warp - kMma : 0, w_hi = C::mma == 2 ? w_lo + 1 : 2;
+            bool ok = warp_wait(&q_full, 0u, abort);
+            uint32_t counts = 0;  // scores (bits 0-1) and sums (2-3) issued by each half, mod 2; whether it has an O (4-5)
+            int now0 = -1, now1 = -1, ahead0 = -1, ahead1 = -1;  // chunks of each half's tile, ca | cb << 8 (-1: none), and of the next with kAhead 2
+            uint32_t phases = 0;  // of p_full[w][buf], bit 2 w + buf
+            auto span_of = [&](int w, int t) {
+                int ca, cb;
+                return active(w, t, ca, cb) ? ca | cb << 8 : -1;
             };
-            auto scores = [&](int w, int t, int ca, int cb) {
-                const int it = 2 * (t - t0);
-                wait_tile(it);
-                if (!ok) return;
-                issue_rows(tmem + w * 128 + ca * kTcChunk, qs + (sh.alt ? 0 : w) * NB * kTcBlock, slot(it) + ca * kTcChunk * 128,
-                           umma_idesc<T>(kTcRows, (cb - ca) * kTcChunk, 0, 0), steps);
-                umma_commit(smem_u32(&s_full[w]));
-            };
-            int nw[2] = {0, 0};
-            int ca, cb;
-            for (int w = 0; w < 2; ++w)
-                if (ok && active(w, t0, ca, cb)) scores(w, t0, ca, cb);
-            umma_commit(smem_u32(&empty[0]));
-            for (int t = t0; t < t1 && ok; ++t) {
-                bool now[2], next[2];
-                int na[2], nb_[2], xa[2], xb[2];
-#pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    now[w] = active(w, t, na[w], nb_[w]);
-                    next[w] = active(w, t + 1, xa[w], xb[w]);
+            auto scores = [&](int w, int s, int span) {
+                const int buf = kAhead == 2 ? (counts >> w) & 1 : 0, ca = span & 255, cb = span >> 8;
+                counts ^= 1u << w;
+                if (elect_one()) {
+                    issue_rows<NB>(tmem + w * C::scores + buf * kKeys + ca * kTcChunk, step_desc(q_desc, sh.alt ? 0 : w * NB * kTcBlock), kTcBlock,
+                                   step_desc(k_desc, s * 2 * NB * kKeyBlock + ca * kTcChunk * 128), kKeyBlock,
+                                   id_s | (static_cast<uint32_t>((cb - ca) * (kTcChunk / 8)) << 17), steps);
+                    umma_commit(smem_u32(&s_full[w][buf]));
                 }
-#pragma unroll
-                for (int w = 0; w < 2; ++w)  // a half that rests on this tile starts on the next one
-                    if (ok && !now[w] && next[w]) scores(w, t + 1, xa[w], xb[w]);
-                const int iv = 2 * (t - t0) + 1;
-#pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    if (!now[w] || !ok) continue;
-                    wait_tile(iv);
-                    ok = ok && mbar_wait_or(smem_u32(&p_full[w]), nw[w] & 1, abort);
-                    tc_fence_after();
-                    if (!ok) break;
-                    issue_sum(tmem + 256 + w * 64 * NB, tmem + w * 128, slot(iv), id_o, na[w] * 2, nb_[w] * 2, nw[w] > 0);
-                    umma_commit(smem_u32(&o_done[w]));
-                    ++nw[w];
-                    if (next[w]) scores(w, t + 1, xa[w], xb[w]);  // its S takes P's place, after the product that reads P
+                __syncwarp();
+            };
+#pragma unroll 1
+            for (int i = 0; i < kAhead && ok; ++i) {
+                if (t0 + i >= t1) break;
+                if (!(ok = warp_wait(&full[i], 0u, abort))) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int w = w_lo; w < w_hi; ++w) {
+                    const int span = span_of(w, t0 + i);
+                    if (i == 0) (w ? now1 : now0) = span; else (w ? ahead1 : ahead0) = span;
+                    if (span >= 0) scores(w, i, span);
+                }
+                if (elect_one()) umma_commit(smem_u32(&empty[i]));
+                __syncwarp();
+            }
+            int s = kAhead;
+            uint32_t ph = 0;
+#pragma unroll 1
+            for (int t = t0; t < t1 && ok; ++t) {
+                const int next0 = w_lo == 0 ? span_of(0, t + kAhead) : -1, next1 = w_hi == 2 ? span_of(1, t + kAhead) : -1;
+                if (!(ok = warp_wait(&full[s], ph, abort))) break;
+                tc_fence_after();
+                // first the halves that rest on this tile: they start on the next one at once
+#pragma unroll 1
+                for (int u = 2 * w_lo; u < 2 * w_hi; ++u) {
+                    const int w = C::mma == 2 ? w_lo : u & 1, now = w ? now1 : now0, next = w ? next1 : next0;
+                    if ((C::mma == 2 ? !(u & 1) : u < 2) != (now < 0)) continue;
+                    if (now >= 0) {
+                        const int buf = kAhead == 2 ? (counts >> (2 + w)) & 1 : 0;
+                        ok = warp_wait(&p_full[w][buf], (phases >> (2 * w + buf)) & 1u, abort);
+                        if (!ok) break;
+                        tc_fence_after();
+                        phases ^= 1u << (2 * w + buf);
+                        if (elect_one()) {
+                            issue_sum<kKeys / 16>(tmem + 2 * C::scores + w * 64 * NB, tmem + w * C::scores + buf * kKeys,
+                                                  step_desc(v_desc, s * 2 * NB * kKeyBlock), id_o, (now & 255) * 2, (now >> 8) * 2,
+                                                  (counts >> (4 + w)) & 1);
+                            umma_commit(smem_u32(&o_done[w][buf]));
+                        }
+                        __syncwarp();
+                        counts ^= 4u << w;
+                        counts |= 16u << w;
+                    }
+                    if (next >= 0) scores(w, s, next);  // after the product that reads P, whose place its S takes
                 }
                 if (!ok) break;
-                if (!now[0] && !now[1]) wait_tile(iv);  // nobody reads this tile's values
-                umma_commit(smem_u32(&empty[iv % kSlots]));
-                if (t + 1 < t1) {
-                    if (!next[0] && !next[1]) wait_tile(iv + 1);
-                    umma_commit(smem_u32(&empty[(iv + 1) % kSlots]));
+                if (elect_one()) umma_commit(smem_u32(&empty[s]));
+                __syncwarp();
+                s = s + 1 == kSlots ? 0 : s + 1;
+                ph ^= s == 0;
+                if (kAhead == 2) {
+                    now0 = ahead0;
+                    now1 = ahead1;
+                    ahead0 = next0;
+                    ahead1 = next1;
+                } else {
+                    now0 = next0;
+                    now1 = next1;
                 }
             }
-            if (*abort) {  // the MMAs already issued must end before the memory goes
-                umma_commit(smem_u32(&q_full));
+            if (!ok && lane == 0) {  // the MMAs already issued must end before the memory goes
+                umma_commit(smem_u32(&drained[warp - kMma]));
                 int never = 0;
-                mbar_wait_or(smem_u32(&q_full), 1u, &never);
+                mbar_wait_or(smem_u32(&drained[warp - kMma]), 0u, &never);
             }
         }
         __syncwarp();
     } else if (warp < kProducer) {
         const int w = warp >> 2, row = tid & 127;
         const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        const uint32_t s_at = lane_base + w * 128, o_at = lane_base + 256 + w * 64 * NB;
+        const uint32_t s_first = lane_base + w * C::scores, o_at = lane_base + 2 * C::scores + w * 64 * NB;
         const int ql = row / sh.pack, g = row - ql * sh.pack, i = i0 + (sh.alt ? 0 : w) * sh.tq + ql;
         const bool live = ql < sh.tq && i < qlen;
         const bool warp_live = __any_sync(0xffffffffu, live);
         const RowBand& rb = w ? rb1 : rb0;
-        Row r;
-        r.pos = start + i;
-        r.jlo = max(0, r.pos - a.left);
-        r.jhi = min(klen, r.pos + a.right + 1);
-        r.m = -INFINITY;
-        r.l = 0.f;
-        const int sinks = a.sinks;
-        const float sc = BIAS ? a.scale : a.scale * kLog2e;
-        const bool neg = sc < 0.f;
-        const float* tab = table + g * sh.table + a.M + kTableExtra - r.pos;
+        const int pos = start + i;
+        const int jlo = max(0, pos - a.left), jhi = min(klen, pos + a.right + 1), jsink = min(a.sinks, jhi);
+        // keys that every row of the tile sees; relative positions at which a chunk has one bias
+        const int all_lo = rb.phi - a.left, all_hi = min(klen, rb.plo + a.right + 1) - kTcChunk;
+        float rm = -INFINITY, rl = 0.f;  // reference (log2 units without a bias, natural with one) and sum
+        // a scale of 0 is held at 1e-30, so that 0 times a mask's infinity does not arise (products below
+        // 1e20 still vanish next to any score)
+        const float scale = a.scale == 0.f ? 1e-30f : fabsf(a.scale);
+        const float sc = BIAS ? scale : scale * kLog2e;
+        constexpr float unit = BIAS ? kLog2e : 1.f;  // of the reference, to log2
+        const float* tab = table + g * sh.table + a.M + kTableExtra - pos;
         int nw = 0, ca, cb;
         bool ok = true;
         for (int t = t0; t < t1; ++t) {
             if (!active(w, t, ca, cb)) continue;
-            const int j0 = bt.tile(t) * kTcRows;
-            ok = warp_wait(&s_full[w], nw & 1, abort);
+            const int j0 = bt.tile(t) * kKeys, buf = nw & (kAhead - 1);
+            const uint32_t s_at = s_first + buf * kKeys;
+            ok = warp_wait(&s_full[w][buf], (nw / kAhead) & 1, abort);
             if (!ok) break;
             tc_fence_after();
             if (warp_live) {
-                // every row sees every key of these chunks
-                auto clear = [&](int c) { const int j = j0 + c * kTcChunk; return j + kTcChunk <= min(klen, rb.plo + a.right + 1) && j >= rb.phi - a.left; };
-                // 0: each pair has its own bias; 1, -1: all are beyond M, ahead or behind
-                auto side = [&](int c) { const int j = j0 + c * kTcChunk; return j - rb.phi >= a.M ? 1 : j + kTcChunk - 1 - rb.plo <= -a.M ? -1 : 0; };
-                auto scored = [&](uint32_t (&x)[32], int c) {  // natural scores with their bias
-                    const int j = j0 + c * kTcChunk, sd = side(c);
-                    if (sd == 0) {
+                float mx[2] = {-INFINITY, -INFINITY};
+                uint32_t x[kChunks][32];
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(fmaf(__uint_as_float(x[e]), sc, tab[j + e]));
-                    } else {
-                        const float bb = table[g * sh.table + (sd > 0 ? sh.table - 1 : 0)];
+                for (int c = 0; c < kChunks; ++c)
+                    if (c >= ca && c < cb) tmem_ld32_async(s_at + c * kTcChunk, x[c]);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(fmaf(__uint_as_float(x[e]), sc, bb));
-                    }
-                };
-                // the tile's maximum (of raw products without a bias: their minimum under a negative scale)
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                auto fold = [&](uint32_t (&x)[32], int c) {
-                    if (BIAS) scored(x, c);
-                    if (!clear(c)) {
+                for (int c = 0; c < kChunks; ++c)
+                    if (c >= ca && c < cb) {
                         const int j = j0 + c * kTcChunk;
+                        tmem_ld_wait(x[c]);
+                        if (BIAS) {  // natural scores with their bias: each pair's own, or that of all pairs beyond M
+                            const int side = j - rb.phi >= a.M ? sh.table - 1 : 0;
+                            if (side || j + kTcChunk - 1 - rb.plo <= -a.M) {
+                                const float bb = table[g * sh.table + side];
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!sees(r, sinks, j + e)) x[e] = __float_as_uint(!BIAS && neg ? INFINITY : -INFINITY);
-                    }
-                    if (!BIAS && neg) {
+                                for (int e = 0; e < 32; e += 2) fma2(x[c][e], x[c][e + 1], sc, bb);
+                            } else {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], -__uint_as_float(x[e]));
-                    } else {
+                                for (int e = 0; e < 32; ++e) x[c][e] = __float_as_uint(fmaf(__uint_as_float(x[c][e]), sc, tab[j + e]));
+                            }
+                        }
+                        if (j < all_lo || j > all_hi) {
+                            const uint32_t see = (low_bits(jhi - j) & ~low_bits(jlo - j)) | low_bits(jsink - j);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(x[e]));
+                            for (int e = 0; e < 32; ++e)
+                                if (!(see & (1u << e))) x[c][e] = __float_as_uint(-INFINITY);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2)
+                            mx[(e >> 1) & 1] = max3(mx[(e >> 1) & 1], __uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
                     }
-                };
-                uint32_t x[32], y[32];
-                for (int c = ca; c < cb; c += 2) {
-                    tmem_ld32_async(s_at + c * kTcChunk, x);
-                    if (c + 1 < cb) tmem_ld32_async(s_at + (c + 1) * kTcChunk, y);
-                    tmem_ld_wait(x);
-                    fold(x, c);
-                    if (c + 1 < cb) {
-                        tmem_ld_wait(y);
-                        fold(y, c + 1);
-                    }
-                }
-                float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                if (!BIAS && top != -INFINITY) top *= fabsf(sc);
-                constexpr float unit = BIAS ? kLog2e : 1.f;  // of m, to log2
+                float top = fmaxf(mx[0], mx[1]);
+                if (!BIAS) top *= sc;
                 if (nw == 0) {
-                    r.m = top;
-                } else if (__any_sync(0xffffffffu, (top - r.m) * unit > kRescale)) {
+                    rm = top;
+                } else if (__any_sync(0xffffffffu, live && (top - rm) * unit > kRescale)) {
                     // a maximum outgrew its reference (or a row sees its first key): move the references
-                    const float to = fmaxf(top, r.m);
-                    const float f = to == -INFINITY ? 1.f : ex2((r.m - to) * unit);
-                    r.m = to;
-                    r.l *= f;
-                    ok = warp_wait(&o_done[w], (nw - 1) & 1, abort);
+                    const float to = fmaxf(top, rm);
+                    const float f = to == -INFINITY ? 1.f : ex2((rm - to) * unit);
+                    rm = to;
+                    rl *= f;
+                    ok = warp_wait(&o_done[w][(nw - 1) & (kAhead - 1)], ((nw - 1) / kAhead) & 1, abort);
                     if (!ok) break;
                     tc_fence_after();
-                    for (int d = 0; d < a.D; d += 32) {
-                        tmem_ld32_async(o_at + d, x);
-                        tmem_ld_wait(x);
+                    for (int d = 0; d < a.D; d += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(o_at + d, o);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
-                        tmem_st32(o_at + d, x);
+                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tmem_st16(o_at + d, o);
                     }
                 }
-                const float ref = r.m == -INFINITY ? 0.f : r.m;
-                float sum[4] = {};
-                auto probs = [&](uint32_t (&x)[32], int c) {
-                    if (BIAS) {
-                        scored(x, c);
+                const float ref = rm == -INFINITY ? 0.f : rm;
+                float2 sum[2] = {};
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(ex2((__uint_as_float(x[e]) - ref) * kLog2e));
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(ex2(fmaf(__uint_as_float(x[e]), sc, -ref)));
-                    }
-                    if (!clear(c)) {
-                        const int j = j0 + c * kTcChunk;
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!sees(r, sinks, j + e)) x[e] = 0u;
-                    }
+                for (int c = 0; c < kChunks; ++c) {
+                    if (c < ca || c >= cb) continue;
                     uint32_t p[16];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float lo = __uint_as_float(x[2 * e]), hi = __uint_as_float(x[2 * e + 1]);
-                        sum[(2 * e) & 3] += lo;
-                        sum[(2 * e + 1) & 3] += hi;
-                        p[e] = pack2<T>(lo, hi);
+                    for (int e = 0; e < 32; e += 2) {
+                        uint32_t &lo = x[c][e], &hi = x[c][e + 1];
+                        if (BIAS) {  // the difference first: scores may be of the type's lowest value
+                            lo = __float_as_uint(ex2((__uint_as_float(lo) - ref) * kLog2e));
+                            hi = __float_as_uint(ex2((__uint_as_float(hi) - ref) * kLog2e));
+                        } else {
+                            fma2(lo, hi, sc, -ref);
+                            lo = __float_as_uint(ex2(__uint_as_float(lo)));
+                            hi = __float_as_uint(ex2(__uint_as_float(hi)));
+                        }
+                        add2(sum[(e >> 1) & 1], lo, hi);
+                        p[e >> 1] = pack2<T>(__uint_as_float(lo), __uint_as_float(hi));
                     }
-                    tmem_st16(s_at + c * 16, p);  // over columns whose scores have been read
-                };
-                for (int c = ca; c < cb; c += 2) {
-                    tmem_ld32_async(s_at + c * kTcChunk, x);
-                    if (c + 1 < cb) tmem_ld32_async(s_at + (c + 1) * kTcChunk, y);
-                    tmem_ld_wait(x);
-                    if (c + 1 < cb) tmem_ld_wait(y);
-                    probs(x, c);
-                    if (c + 1 < cb) probs(y, c + 1);
+                    tmem_st16(s_at + c * 16, p);  // the scores are in registers: P takes their place
                 }
-                r.l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                rl += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 tmem_st_wait();
             }
             ++nw;
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&p_full[w]));
+            if (lane == 0) mbar_arrive(smem_u32(&p_full[w][buf]));
         }
-        if (ok && nw > 0) ok = warp_wait(&o_done[w], (nw - 1) & 1, abort);
+        if (ok && nw > 0) ok = warp_wait(&o_done[w][(nw - 1) & (kAhead - 1)], ((nw - 1) / kAhead) & 1, abort);
         tc_fence_after();
         if (sh.alt) {
             // the second half's rows are the first's: join them (its O is in the same lanes)
-            if (w == 1) s_ml[row] = make_float2(r.m, nw > 0 && warp_live ? r.l : 0.f);
+            if (w == 1) s_ml[row] = make_float2(rm, nw > 0 && warp_live ? rl : 0.f);
             tc_fence_before();
             asm volatile("bar.sync 1, 256;" ::: "memory");
             tc_fence_after();
         }
         const bool rows_here = ql < sh.tq && i < a.Lq;
         if (ok && !(sh.alt && w == 1) && __any_sync(0xffffffffu, rows_here)) {
-            constexpr float unit = BIAS ? kLog2e : 1.f;
-            float f0 = 1.f, f1 = 0.f, m = r.m, l = live ? r.l : 0.f;
+            float f0 = 1.f, f1 = 0.f, m = rm, l = live ? rl : 0.f;
             bool first = nw > 0, second = false;
             if (sh.alt) {
                 const float2 other = s_ml[row];
                 const float l1 = live ? other.y : 0.f;
-                m = fmaxf(r.m, l1 > 0.f ? other.x : -INFINITY);
+                m = fmaxf(rm, l1 > 0.f ? other.x : -INFINITY);
                 const float ref = m == -INFINITY ? 0.f : m;
-                f0 = l > 0.f ? ex2((r.m - ref) * unit) : 0.f;
+                f0 = l > 0.f ? ex2((rm - ref) * unit) : 0.f;
                 f1 = l1 > 0.f ? ex2((other.x - ref) * unit) : 0.f;
                 l = l * f0 + l1 * f1;
                 second = t1 - t0 > 1 && __any_sync(0xffffffffu, l1 > 0.f);
@@ -470,30 +490,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     if (tid == 0 && *abort) atomicOr(&g_band_status, 1u);
-    if (warp == kMma) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+    if (warp == kMma) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::tmem));
 }
 
 FwdShape shape_of(const BandArgs& a) {
     FwdShape s;
+    const int table_bytes = a.D > 64 ? Cfg<2>::table_bytes : Cfg<1>::table_bytes;
     s.table = a.nb ? table_floats(a.M) : 0;
     s.pack = a.G;
-    if (s.pack * s.table * static_cast<int>(sizeof(float)) > kTableBytes) s.pack = 1;
+    if (s.pack * s.table * static_cast<int>(sizeof(float)) > table_bytes) s.pack = 1;
     s.tq = kTcRows / s.pack;
     s.alt = a.Lq <= s.tq;
     s.blocks = s.alt ? 1 : (a.Lq + 2 * s.tq - 1) / (2 * s.tq);
     const long long ctas = static_cast<long long>(a.N) * (a.Hq / s.pack) * s.blocks;
-    s.splits = band_splits(a, ctas, std::min(a.Lq, 2 * s.tq), kTcRows, 1);
+    s.splits = band_splits(a, ctas, std::min(a.Lq, 2 * s.tq), kKeys, a.D > 64 ? Cfg<2>::ctas : Cfg<1>::ctas);
     return s;
 }
 
 template <typename T, int NB, bool BIAS>
 cudaError_t launch(const BandArgs& a, const FwdShape& s, void* out, float* lse, void* ws, cudaStream_t stream) {
-    const size_t smem = 1024 + static_cast<size_t>((s.alt ? 1 : 2) + kSlots) * NB * kTcBlock + s.pack * s.table * sizeof(float);
+    using C = Cfg<NB>;
+    const size_t smem = 1024 + static_cast<size_t>(s.alt ? 1 : 2) * NB * kTcBlock + static_cast<size_t>(C::slots) * 2 * NB * kKeyBlock +
+                        s.pack * s.table * sizeof(float);
     cudaError_t e = cudaFuncSetAttribute(fwd_kernel<T, NB, BIAS>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
+    CUtensorMap mq, mk, mv;
+    if (!make_map(&mq, a.dtype, a.q, a.N, a.Lq, a.Hq, a.D, a.q_batch, a.q_row, s.pack, s.tq) ||
+        !make_map(&mk, a.dtype, a.k, a.N, a.Lk, a.Hk, a.D, a.k_batch, a.k_row, 1, kKeys) ||
+        !make_map(&mv, a.dtype, a.v, a.N, a.Lk, a.Hk, a.D, a.v_batch, a.v_row, 1, kKeys))
+        return cudaErrorInvalidValue;
     const BandPart part = band_part(a, s.splits, ws);
     const long long ctas = static_cast<long long>(a.N) * (a.Hq / s.pack) * s.blocks * s.splits;
-    fwd_kernel<T, NB, BIAS><<<static_cast<unsigned>(ctas), kThreads, smem, stream>>>(a, s, static_cast<T*>(out), lse, part);
+    fwd_kernel<T, NB, BIAS><<<static_cast<unsigned>(ctas), C::threads, smem, stream>>>(mq, mk, mv, a, s, static_cast<T*>(out), lse, part);
     e = cudaGetLastError();
     if (e != cudaSuccess || s.splits == 1) return e;
     return launch_band_join(a, s.splits, part, out, lse, stream);

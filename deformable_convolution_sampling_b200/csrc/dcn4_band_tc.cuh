@@ -2,13 +2,14 @@
 // tiles of 128 rows in the 128-byte swizzled layout, products whose first operand
 // is in tensor memory, and tensor-memory loads and stores by a thread per row.
 //
-// Operand tile: 128 rows (queries or keys) of D entries in blocks of 64 columns;
-// row r of a block is 128 bytes at r * 128, its 16-byte pieces permuted by r mod 8.
-// As a K-major operand (contraction over D) a step of 16 entries moves 32 bytes,
-// as an M/N-major one (contraction over the rows) a step of 16 rows moves 2048
-// bytes and the blocks are kTcBlock apart.  Rows past a sequence and entries past
-// D are zeros: a TMA box would bring what lies there, and 0 times an infinity is
-// not 0, so the tiles are filled with 16-byte cp.async, which write zeros instead.
+// Operand tile: rows (queries or keys) of D entries in blocks of 64 columns; row r
+// of a block is 128 bytes at r * 128, its 16-byte pieces permuted by r mod 8 (what
+// TMA's 128-byte swizzle writes).  As a K-major operand (contraction over D) a step
+// of 16 entries moves 32 bytes, as an M/N-major one (contraction over the rows) a
+// step of 16 rows moves 2048 bytes and the blocks are one block's bytes apart.
+// Entries past D and rows past the tensor arrive as zeros; rows between a
+// sequence's own length and the tensor's end may hold anything, and 0 times an
+// infinity is not 0, so the one tile they can share is cleared there after it lands.
 #pragma once
 
 #include <type_traits>
@@ -21,7 +22,7 @@ namespace dcn4 {
 namespace tc {
 
 constexpr int kTcRows = 128;                 // rows of a tile: the MMA's M, TMEM's lanes
-constexpr int kTcBlock = kTcRows * 128;      // bytes of a block of 64 columns
+constexpr int kTcBlock = kTcRows * 128;      // bytes of 64 columns of a tile of 128 rows
 constexpr int kTcChunk = 32;                 // columns of scores handled at a time
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -71,6 +72,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -90,45 +96,131 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return u;
 }
 
-// 16 bytes from global to shared memory, or zeros.
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool on) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// One tile of `rows` (a multiple of 8) rows by 128 threads: row(r) gives a row's address, or NULL for
-// zeros; `safe` is any valid address of the tensor.  A warp reads 256 (D > 64) or
-// 128 bytes of neighbouring pieces of a row.
-template <typename T, int NB, typename Row>
-__device__ __forceinline__ void load_operand(uint32_t dst, int D, int rows, const T* safe, Row row, int tid) {
-    constexpr int P = 8 * NB;  // pieces of a padded row
-    const int piece = tid % P, col = piece * 8;
-    const bool in = col < D;
-    if (col >= (D + 15) / 16 * 16) return;  // no product reads these
-    const uint32_t at = dst + (piece / 8) * kTcBlock;
-    for (int r = tid / P; r < rows; r += 128 / P) {
-        const T* src = row(r);
-        const bool on = in && src;
-        cp16(at + r * 128 + (((piece & 7) ^ (r & 7)) << 4), on ? src + col : safe, on);
-    }
+// A box of rows of an operand's tensor map (make_map): 64 columns from `col`, heads
+// from `head`, tokens from `row` of image n.
+__device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* map, int col, int head, int row, int n, uint32_t mbar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(col), "r"(head), "r"(row), "r"(n), "r"(mbar)
+        : "memory");
 }
 
-// Products of 128 x N tiles over D: D rounded up to steps of 16.
-__device__ __forceinline__ void issue_rows(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, int steps) {
-    for (int q = 0; q < steps; ++q) {
-        const uint32_t off = (q >> 2) * kTcBlock + (q & 3) * 32;
-        umma_f16(d, umma_desc_sw128(a + off, 16, 1024), umma_desc_sw128(b + off, 16, 1024), idesc, q > 0);
-    }
+// One warp writes zeros to rows [from, to) of a tile whose loads have landed.
+template <int NB>
+__device__ __forceinline__ void zero_rows(uint32_t tile, int block, int from, int to, int lane) {
+    for (int e = from * 8 + lane; e < to * 8; e += 32)
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + b * block + e * 16), "r"(0) : "memory");
+    fence_async_smem();
+    __syncwarp();
 }
-// d (+)= a (tensor memory, K steps of 16 rows [s0, s1)) times the tile b of those rows.
-__device__ __forceinline__ void issue_sum(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, int s0, int s1, bool accum) {
-    for (int s = s0; s < s1; ++s)
-        umma_f16_ts(d, a + s * 8, umma_desc_sw128(b + s * 2048, kTcBlock, 1024), idesc, accum || s > s0);
+
+// A bounded wait by a whole warp: all of its lanes go on, or none.  The loop ends
+// on a vote, so the warp never diverges (one lane polling for the rest took 300
+// cycles on a phase long complete, this 90).
+__device__ __forceinline__ bool warp_wait(uint64_t* mbar, uint32_t parity, volatile int* abort) {
+    const uint32_t at = smem_u32(mbar);
+    for (int i = 0; i < kTWaitSpins; ++i) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred P1;\n\tmbarrier.try_wait.parity.shared::cta.b64 P1, [%1], %2;\n\t"
+            "selp.b32 %0, 1, 0, P1;\n\t}"
+            : "=r"(done)
+            : "r"(at), "r"(parity)
+            : "memory");
+        if (__all_sync(0xffffffffu, done)) return true;
+        if ((i & 63) == 63 && __any_sync(0xffffffffu, *abort)) return false;
+    }
+    *abort = 1;
+    return false;
+}
+
+// x * m + c of two values at once.
+__device__ __forceinline__ void fma2(uint32_t& x, uint32_t& y, float m, float c) {
+    asm("{\n\t.reg .b64 v, w, z;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 w, {%2, %2};\n\tmov.b64 z, {%3, %3};\n\t"
+        "fma.rn.f32x2 v, v, w, z;\n\tmov.b64 {%0, %1}, v;\n\t}"
+        : "+r"(x), "+r"(y)
+        : "f"(m), "f"(c));
+}
+__device__ __forceinline__ void add2(float2& s, uint32_t x, uint32_t y) {
+    asm("{\n\t.reg .b64 v, w;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 w, {%2, %3};\n\tadd.rn.f32x2 v, v, w;\n\tmov.b64 {%0, %1}, v;\n\t}"
+        : "+f"(s.x), "+f"(s.y)
+        : "r"(x), "r"(y));
+}
+
+// MMA operands are warp-uniform registers.  The issuing warp therefore runs as a
+// whole, on values the compiler knows to be uniform (parameters, block indexes,
+// broadcasts from a fixed lane), and only the instruction itself is one lane's: with
+// the whole loop inside one lane's branch every MMA took 97 cycles to issue, its
+// descriptors moved to uniform registers one by one, instead of the 64 it runs for.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t on;
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b32 r;\n\telect.sync r|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(on));
+    return on;
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+constexpr uint32_t kNegateA = 1u << 13;  // instruction descriptor: D = -A B
+// The lowest n of 32 bits (n <= 0: none, n >= 32: all).
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+__device__ __forceinline__ uint64_t step_desc(uint64_t d, uint32_t bytes) {
+    return d + (bytes >> 4);  // no carry out of the address field: shared memory ends below 2^18
+}
+// Products of 128 x N tiles over D: `steps` steps of 16 of at most 4 NB.
+template <int NB>
+__device__ __forceinline__ void issue_rows(uint32_t d, uint64_t a, int ablock, uint64_t b, int bblock, uint32_t idesc, int steps) {
+#pragma unroll
+    for (int q = 0; q < 4 * NB; ++q)
+        if (q < steps)
+            umma_f16(d, step_desc(a, (q >> 2) * ablock + (q & 3) * 32), step_desc(b, (q >> 2) * bblock + (q & 3) * 32), idesc, q > 0);
+}
+// d (+)= a (tensor memory, steps [s0, s1) of 16 of its rows) times the tile b of those rows.
+template <int STEPS>
+__device__ __forceinline__ void issue_sum(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, int s0, int s1, bool accum) {
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s)
+        if (s >= s0 && s < s1) {
+            umma_f16_ts(d, a + s * 8, step_desc(b, s * 2048), idesc, accum);
+            accum = true;
+        }
+}
+
+// cuTensorMapEncodeTiled from the driver (resolved once through the runtime).
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+inline EncodeTiledFn band_encode_tiled() {
+    static EncodeTiledFn fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return static_cast<EncodeTiledFn>(nullptr);
+        return reinterpret_cast<EncodeTiledFn>(p);
+    }();
+    return fn;
+}
+
+// [N][L][H][D] of 16-bit elements (strides in elements, 0 batch stride for one image) with boxes of
+// 64 columns, `heads` heads and `rows` tokens, 128-byte swizzle, zeros outside.
+inline bool make_map(CUtensorMap* map, int dtype, const void* base, int N, int L, int H, int D, long long batch, long long row,
+                     int heads, int rows) {
+    const EncodeTiledFn fn = band_encode_tiled();
+    if (!fn) return false;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(L),
+                                static_cast<cuuint64_t>(N)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(row) * 2,
+                                   static_cast<cuuint64_t>(batch ? batch : row) * 2};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(heads), static_cast<cuuint32_t>(rows), 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(map, dtype == 1 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+              const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace tc
