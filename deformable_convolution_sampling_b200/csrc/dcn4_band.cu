@@ -105,9 +105,16 @@ size_t band_forward_workspace_bytes(const BandArgs& a) {
     return round256(a.dtype == 0 ? band_part_bytes(a, simt_splits(a)) : band_fwd_tc_part_bytes(a));
 }
 
-cudaError_t band_status(unsigned* status, bool reset) { return band_fwd_status(status, reset); }
+cudaError_t band_status(unsigned* status, bool reset) {
+    unsigned fwd = 0, bwd = 0;
+    cudaError_t e = band_fwd_status(&fwd, reset);
+    if (e == cudaSuccess) e = band_bwd_status(&bwd, reset);
+    *status = fwd | bwd;
+    return e;
+}
 
 size_t band_backward_workspace_bytes(const BandArgs& a) {
+    if (band_bwd_tc_fits(a)) return band_bwd_tc_workspace(a);
     const size_t parts = static_cast<size_t>(a.N) * a.Hk * simt_row_blocks(a) * a.nb * a.G;
     return delta_bytes(a) + round256(parts * sizeof(float));
 }
@@ -118,6 +125,7 @@ cudaError_t launch_band_forward(const BandArgs& a, void* out, float* lse, void* 
 
 cudaError_t launch_band_backward(const BandArgs& a, const void* out, const float* lse, const void* gout, void* gq,
                                  void* gk, void* gv, void* gbias, void* ws, cudaStream_t stream) {
+    if (band_bwd_tc_fits(a)) return launch_band_bwd_tc(a, out, lse, gout, gq, gk, gv, gbias, ws, stream);
     float* delta = static_cast<float*>(ws);
     float* bpart = reinterpret_cast<float*>(static_cast<char*>(ws) + delta_bytes(a));
     return launch_band_simt_backward(a, out, lse, gout, gq, gk, gv, gbias, delta, bpart, stream);

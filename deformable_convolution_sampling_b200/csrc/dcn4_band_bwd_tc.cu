@@ -1,0 +1,895 @@
+// dcn4_band_bwd_tc.cu — the band attention's backward for 16-bit types on the
+// fifth-generation tensor cores: three kernels, no atomics.
+//
+//   stats     delta_i = <g_i, out_i> beside lse_i (+infinity for rows that see
+//             nothing: their probabilities are then 0 without a mask).
+//   grad_q    a CTA holds two tiles of 128 rows and streams tiles of 64 keys:
+//             S = Q K^T, E = G V^T, d = p (E - delta), p = e^(S - lse), gq += d K.
+//             With a bias it also sums d along the diagonals (see diagonal sums).
+//   grad_kv   a CTA holds 128 keys and streams tiles of 64 queries of every head
+//             that shares them: S^T = K Q^T, E^T = V G^T, gv += p^T G, gk += d^T Q.
+// Scores are recomputed by both kernels (7 products instead of 5): one kernel would
+// have to add every gq from many CTAs, in an order that changes.
+//
+// p and d go to the tensor cores as the I/O type, over the scores they came from in
+// tensor memory; the sums stay there in fp32 until they are rounded once.
+#include "dcn4_band_tc.cuh"
+
+namespace dcn4 {
+namespace {
+
+using namespace tc;
+
+constexpr int kProducer = 8, kMma = 9;
+constexpr int kTile = 64, kChunks = kTile / kTcChunk;  // keys or queries of a streamed tile
+constexpr int kTileBlock = kTile * 128;                // bytes of 64 of its columns
+constexpr int kTableExtra = 160;                       // as in the forward: a chunk and a tile's rows past M
+constexpr int kTableBytes = 28 << 10;
+constexpr int kTmem = 512;
+
+__device__ unsigned g_band_bwd_status;
+
+__host__ __device__ inline int table_floats(int M) { return 2 * (M + kTableExtra) + 1; }
+__host__ __device__ inline int padded_queries(int Lq) { return (Lq + kTile - 1) / kTile * kTile; }
+
+// Bias of `heads` heads from h0 on by relative position, clamped.
+template <typename T>
+__device__ __forceinline__ void fill_table(const BandArgs& a, float* table, int floats, int h0, int heads, int threads) {
+    for (int e = threadIdx.x; e < heads * floats; e += threads) {
+        const int g = e / floats, rel = e - g * floats - a.M - kTableExtra;
+        const int bk = __ldg(a.buckets + max(-a.M, min(rel, a.M)) + a.M);
+        table[e] = static_cast<unsigned>(bk) < static_cast<unsigned>(a.nb)
+                       ? to_f32(static_cast<const T*>(a.bias)[static_cast<long long>(bk) * a.Hq + h0 + g]) : 0.f;
+    }
+}
+
+// (lse, delta) of every row, [N][Hq][padded Lq]; 16 lanes a row.  Without a bias lse is
+// in log2 units, as the scores are formed there.
+template <typename T>
+__global__ void __launch_bounds__(256) stats_kernel(BandArgs a, const T* __restrict__ out, const float* __restrict__ lse,
+                                                    const T* __restrict__ gout, float2* __restrict__ stats) {
+    const int LP = padded_queries(a.Lq);
+    const long long r = blockIdx.x * 16ll + (threadIdx.x >> 4), rows = static_cast<long long>(a.N) * LP * a.Hq;
+    const int piece = threadIdx.x & 15;
+    const bool on = r < rows;
+    const int h = on ? static_cast<int>(r % a.Hq) : 0;
+    const long long ni = on ? r / a.Hq : 0;
+    const int n = static_cast<int>(ni / LP), i = static_cast<int>(ni - static_cast<long long>(n) * LP);
+    const bool live = on && i < band_qlen(a, n);
+    float d = 0.f;
+    if (live && piece * 8 < a.D) {
+        const long long at = ((static_cast<long long>(n) * a.Lq + i) * a.Hq + h) * a.D + piece * 8;
+        float2 x[4], y[4];
+        unpack(__ldg(reinterpret_cast<const uint4*>(out + at)), x, T());
+        unpack(__ldg(reinterpret_cast<const uint4*>(gout + at)), y, T());
+#pragma unroll
+        for (int e = 0; e < 4; ++e) d = fmaf(x[e].x, y[e].x, fmaf(x[e].y, y[e].y, d));
+    }
+    for (int o = 8; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+    if (on && piece == 0) {
+        const long long nh = static_cast<long long>(n) * a.Hq + h;
+        const float l = live ? band_lse_ref(lse[nh * a.Lq + i]) : INFINITY;
+        stats[nh * LP + i] = make_float2(a.nb ? l : l * kLog2e, d);
+    }
+}
+
+
+// ---------------------------------------------------------------------------
+// grad_q
+// ---------------------------------------------------------------------------
+template <int NB>
+struct QCfg {
+    static constexpr int slots = NB == 1 ? 4 : 2;
+    static constexpr int threads = 352;              // 8 softmax warps, the loads, an issuing warp a half
+    static constexpr size_t smem = 1024 + 4 * NB * kTcBlock + slots * 2 * NB * kTileBlock;
+};
+
+// Diagonal sums.  All pairs of a diagonal of the score matrix share a relative
+// position, so the bias gradient is the sum of d along diagonals, then over the
+// diagonals of a bucket.  A lane holds a row; as the columns go by, a partial sum
+// moves from lane to lane: after column j, lane i holds the sum over rows 0..i of
+// the diagonal through (i, j).  Lane 31's is complete, and is handed to lane j mod 32,
+// so that 32 columns end in one store of 32 neighbouring relative positions: two
+// shuffles a column, no shared memory, no atomics, one order.
+struct Diagonals {
+    float* mine;    // this warp's sums, of relative position -M .. M (the ends: and beyond)
+    int M, pos31;   // position of lane 31's query
+    int next;       // key the run goes on with; -1: no run
+    bool again;     // a run has been stored already: add
+    float s, below, above;
+    __device__ __forceinline__ void store(int j, int lane, float v) {
+        const int rel = j + lane - pos31;
+        if (rel <= -M) below += v;
+        else if (rel >= M) above += v;
+        else {
+            float* to = mine + rel + M;
+            *to = again ? *to + v : v;
+        }
+    }
+    __device__ __forceinline__ void flush(int lane) {
+        if (next < 0) return;
+        float got = 0.f;
+        for (int e = 0; e < 31; ++e) {
+            s = __shfl_up_sync(0xffffffffu, s, 1);
+            if (lane == 0) s = 0.f;
+            const float o = __shfl_sync(0xffffffffu, s, 31);
+            if (lane == e) got = o;
+        }
+        store(next, lane, got);  // lane 31 adds a 0
+        __syncwarp();
+        again = true;
+        next = -1;
+        s = 0.f;
+    }
+    __device__ __forceinline__ void chunk(int j, int lane, const uint32_t (&d)[32]) {
+        if (j != next) flush(lane);
+        float got = 0.f;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+            s = __shfl_up_sync(0xffffffffu, s, 1);
+            s = (lane == 0 ? 0.f : s) + __uint_as_float(d[e]);
+            const float o = __shfl_sync(0xffffffffu, s, 31);
+            if (lane == e) got = o;
+        }
+        store(j, lane, got);
+        next = j + 32;
+    }
+};
+
+template <typename T, int NB, bool BIAS>
+__global__ void __launch_bounds__(QCfg<NB>::threads, 1)
+    grad_q_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_g,
+                  const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, BandArgs a, int pack,
+                  int tq, int blocks, int floats, const float2* __restrict__ stats, T* __restrict__ gq, float* __restrict__ diag) {
+    constexpr int kSlots = QCfg<NB>::slots;
+    extern __shared__ __align__(1024) unsigned char band_smem[];
+    __shared__ __align__(8) uint64_t full[kSlots], empty[kSlots], raw, rows_full, s_full[2], p_full[2], o_done[2];
+    __shared__ uint32_t taddr_s;
+    __shared__ int s_abort;
+    const int tid = threadIdx.x, warp = static_cast<int>(uniform(tid >> 5)), lane = tid & 31;
+    const uint32_t base = (smem_u32(band_smem) + 1023u) & ~1023u;
+    const uint32_t qs = base, ring = base + 4 * NB * kTcBlock;  // Q, G of the first half, then of the second
+    float* table = reinterpret_cast<float*>(band_smem + (ring - smem_u32(band_smem)) + kSlots * 2 * NB * kTileBlock);
+
+    int b = blockIdx.x;
+    const int blk = blocks - 1 - b % blocks;
+    b /= blocks;
+    const int groups = a.Hq / pack, n = b / groups, h0 = (b - n * groups) * pack, hk = h0 / a.G;
+    const int klen = static_cast<int>(uniform(band_klen(a, n))), qlen = static_cast<int>(uniform(band_qlen(a, n))),
+              start = static_cast<int>(uniform(band_start(a, n)));
+    const int i0 = blk * 2 * tq, i1 = min(i0 + 2 * tq, qlen) - 1;
+
+    if (tid == 0) {
+        for (int s = 0; s < kSlots; ++s) {
+            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&empty[s]), 2);
+        }
+        mbar_init(smem_u32(&raw), 1);
+        mbar_init(smem_u32(&rows_full), 1);
+        for (int w = 0; w < 2; ++w) {
+            mbar_init(smem_u32(&s_full[w]), 1);
+            mbar_init(smem_u32(&p_full[w]), 4);
+            mbar_init(smem_u32(&o_done[w]), 1);
+        }
+        s_abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kMma) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&taddr_s)), "r"(kTmem));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    if (BIAS) fill_table<T>(a, table, floats, h0, 1, QCfg<NB>::threads);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = uniform(taddr_s);
+    volatile int* abort = &s_abort;
+
+    BandTiles bt{0, 0, 0};
+    if (i0 <= i1) bt = band_tiles(a, start + i0, start + i1, klen, kTile);
+    const int cnt = bt.count();
+    // what a half's rows see of key tile t: chunks [ca, cb)
+    auto band_of = [&](int w, int& plo, int& phi) {
+        plo = start + i0 + w * tq;
+        phi = min(plo + tq, start + qlen) - 1;
+    };
+    auto active = [&](int w, int t, int& ca, int& cb) {
+        int plo, phi;
+        band_of(w, plo, phi);
+        const int j0 = bt.tile(t) * kTile, end = min(klen, phi + a.right + 1), sink = min(min(a.sinks, end), j0 + kTile);
+        int lo = max(max(0, plo - a.left), j0), hi = min(end, j0 + kTile);
+        if (sink > j0) {
+            if (lo >= hi) hi = sink;
+            lo = j0;
+        }
+        ca = (lo - j0) >> 5;
+        cb = (hi - j0 + kTcChunk - 1) >> 5;
+        return plo <= phi && lo < hi;
+    };
+
+    if (warp == kProducer) {
+        if (cnt && elect_one()) {
+            mbar_expect_tx(smem_u32(&rows_full), 4 * NB * pack * tq * 128);
+            for (int w = 0; w < 2; ++w)
+                for (int c = 0; c < NB; ++c) {
+                    tma_load_rows(qs + (2 * w * NB + c) * kTcBlock, &map_q, c * 64, h0, i0 + w * tq, n, smem_u32(&rows_full));
+                    tma_load_rows(qs + ((2 * w + 1) * NB + c) * kTcBlock, &map_g, c * 64, h0, i0 + w * tq, n, smem_u32(&rows_full));
+                }
+        }
+        int raws = 0;
+        for (int t = 0; t < cnt; ++t) {
+            const int s = t % kSlots, j0 = bt.tile(t) * kTile;
+            if (!warp_wait(&empty[s], ((t / kSlots) & 1) ^ 1u, abort)) break;
+            const uint32_t at_k = ring + s * 2 * NB * kTileBlock, at_v = at_k + NB * kTileBlock;
+            const bool clear = j0 + kTile > klen && klen < a.Lk;  // keys past the sequence meet d of 0
+            if (elect_one()) {
+                const uint32_t bar = smem_u32(clear ? &raw : &full[s]);
+                mbar_expect_tx(bar, 2 * NB * kTileBlock);
+                for (int c = 0; c < NB; ++c) {
+                    tma_load_rows(at_k + c * kTileBlock, &map_k, c * 64, hk, j0, n, bar);
+                    tma_load_rows(at_v + c * kTileBlock, &map_v, c * 64, hk, j0, n, bar);
+                }
+            }
+            if (clear) {
+                if (!warp_wait(&raw, raws++ & 1, abort)) break;
+                zero_rows<2 * NB>(at_k, kTileBlock, max(klen - j0, 0), kTile, lane);
+                if (elect_one()) mbar_arrive(smem_u32(&full[s]));
+            }
+        }
+    } else if (warp >= kMma) {
+        const int w = warp - kMma;
+        if (cnt) {
+            const int steps = (a.D + 15) / 16;
+            const uint32_t id_s = umma_idesc<T>(kTcRows, 0, 0, 0), id_o = umma_idesc<T>(kTcRows, steps * 16, 0, 1);
+            const uint64_t q_desc = umma_desc_sw128(qs + 2 * w * NB * kTcBlock, 16, 1024), g_desc = step_desc(q_desc, NB * kTcBlock),
+                           k_desc = umma_desc_sw128(ring, 16, 1024), v_desc = step_desc(k_desc, NB * kTileBlock),
+                           k_sum = umma_desc_sw128(ring, kTileBlock, 1024);
+            const uint32_t at_s = tmem + w * 256, at_o = at_s + 128;
+            bool ok = warp_wait(&rows_full, 0u, abort), some = false;
+            uint32_t p_phase = 0;
+            int s = 0;
+            uint32_t ph = 0;
+#pragma unroll 1
+            for (int t = 0; t < cnt && ok; ++t) {
+                int ca, cb;
+                const bool on = active(w, t, ca, cb);
+                if (!(ok = warp_wait(&full[s], ph, abort))) break;
+                tc_fence_after();
+                const uint32_t off = s * 2 * NB * kTileBlock, row = off + ca * kTcChunk * 128;
+                if (on) {
+                    if (elect_one()) {
+                        const uint32_t id = id_s | (static_cast<uint32_t>((cb - ca) * (kTcChunk / 8)) << 17);
+                        issue_rows<NB>(at_s + ca * kTcChunk, q_desc, kTcBlock, step_desc(k_desc, row), kTileBlock, id, steps);
+                        issue_rows<NB>(at_s + 64 + ca * kTcChunk, g_desc, kTcBlock, step_desc(v_desc, row), kTileBlock, id, steps);
+                        umma_commit(smem_u32(&s_full[w]));
+                    }
+                    __syncwarp();
+                    if (!(ok = warp_wait(&p_full[w], p_phase, abort))) break;
+                    tc_fence_after();
+                    p_phase ^= 1u;
+                    if (elect_one()) issue_sum<kTile / 16>(at_o, at_s, step_desc(k_sum, off), id_o, ca * 2, cb * 2, some);
+                    __syncwarp();
+                    some = true;
+                }
+                if (elect_one()) umma_commit(smem_u32(&empty[s]));
+                __syncwarp();
+                s = s + 1 == kSlots ? 0 : s + 1;
+                ph ^= s == 0;
+            }
+            if (elect_one()) umma_commit(smem_u32(&o_done[w]));
+            __syncwarp();
+            int never = 0;
+            if (!ok && lane == 0) mbar_wait_or(smem_u32(&o_done[w]), 0u, &never);  // the MMAs must end before the memory goes
+        }
+        __syncwarp();
+    } else if (warp < kProducer) {
+        const int w = warp >> 2, row = tid & 127;
+        const uint32_t at_s = tmem + w * 256 + (static_cast<uint32_t>((warp & 3) * 32) << 16), at_o = at_s + 128;
+        const int ql = row / pack, g = row - ql * pack, i = i0 + w * tq + ql;
+        const bool live = ql < tq && i < qlen;
+        const bool warp_live = __any_sync(0xffffffffu, live);
+        int plo, phi;
+        band_of(w, plo, phi);
+        const int pos = start + i;
+        const int jlo = max(0, pos - a.left), jhi = live ? min(klen, pos + a.right + 1) : 0, jsink = min(a.sinks, jhi);
+        // keys that all rows of the tile see (with a bias a dead row's d must be 0, so its tile is masked)
+        const int all_lo = BIAS && phi - plo + 1 < tq ? kBandFar : phi - a.left, all_hi = min(klen, plo + a.right + 1) - kTcChunk;
+        const float2 st = live ? stats[(static_cast<long long>(n) * a.Hq + h0 + g) * padded_queries(a.Lq) + i] : make_float2(INFINITY, 0.f);
+        const float sc = BIAS ? a.scale : a.scale * kLog2e;
+        const float* tab = table + a.M + kTableExtra - pos;
+        Diagonals dg;
+        if (BIAS) {
+            const int rowwarps = (a.Lq + 31) / 32, first = (i0 + w * tq) / 32 + (warp & 3);  // pack is 1: 32 queries a warp
+            dg.mine = diag + ((static_cast<long long>(n) * a.Hq + h0) * rowwarps + min(first, rowwarps - 1)) * (2 * a.M + 1);
+            dg.M = a.M;
+            dg.pos31 = start + i0 + w * tq + (warp & 3) * 32 + 31;
+            dg.next = -1;
+            dg.again = false;
+            dg.s = dg.below = dg.above = 0.f;
+        }
+        int nw = 0, ca, cb;
+        bool ok = true;
+        for (int t = 0; t < cnt; ++t) {
+            if (!active(w, t, ca, cb)) continue;
+            const int j0 = bt.tile(t) * kTile;
+            if (!(ok = warp_wait(&s_full[w], nw & 1, abort))) break;
+            tc_fence_after();
+            if (warp_live) {
+                uint32_t x[kChunks][32], y[kChunks][32];
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c)
+                    if (c >= ca && c < cb) {
+                        tmem_ld32_async(at_s + c * kTcChunk, x[c]);
+                        tmem_ld32_async(at_s + 64 + c * kTcChunk, y[c]);
+                    }
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) {
+                    if (c < ca || c >= cb) continue;
+                    const int j = j0 + c * kTcChunk;
+                    tmem_ld_wait(x[c]);
+                    tmem_ld_wait(y[c]);
+                    const int side = j - phi >= a.M ? 1 : j + kTcChunk - 1 - plo <= -a.M ? -1 : 0;
+                    if (BIAS) {
+                        const float bb = table[side > 0 ? floats - 1 : 0];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            x[c][e] = __float_as_uint((fmaf(__uint_as_float(x[c][e]), sc, side ? bb : tab[j + e]) - st.x) * kLog2e);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) fma2(x[c][e], x[c][e + 1], sc, -st.x);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        x[c][e] = __float_as_uint(ex2(__uint_as_float(x[c][e])) * (__uint_as_float(y[c][e]) - st.y));
+                    if (j < all_lo || j > all_hi) {
+                        const uint32_t see = (low_bits(jhi - j) & ~low_bits(jlo - j)) | low_bits(jsink - j);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!(see & (1u << e))) x[c][e] = 0u;
+                    }
+                    uint32_t p[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) p[e >> 1] = pack2<T>(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
+                    tmem_st16(at_s + c * 16, p);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&p_full[w]));
+                if (BIAS) {  // under the product of this tile
+#pragma unroll
+                    for (int c = 0; c < kChunks; ++c) {
+                        if (c < ca || c >= cb) continue;
+                        const int j = j0 + c * kTcChunk;
+                        // the warp's own rows: 32 queries up to pos31
+                        const bool above = j - dg.pos31 >= a.M, below = j + kTcChunk - 1 - (dg.pos31 - 31) <= -a.M;
+                        if (above || below) {
+                            float s = 0.f;
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) s += __uint_as_float(x[c][e]);
+                            (above ? dg.above : dg.below) += s;
+                        } else {
+                            dg.chunk(j, lane, x[c]);
+                        }
+                    }
+                }
+            } else {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&p_full[w]));
+            }
+            ++nw;
+        }
+        if (BIAS && warp_live) {
+            dg.flush(lane);
+            float lo = dg.below, hi = dg.above;
+            for (int o = 16; o; o >>= 1) {
+                lo += __shfl_xor_sync(0xffffffffu, lo, o);
+                hi += __shfl_xor_sync(0xffffffffu, hi, o);
+            }
+            if (lane == 0) {
+                dg.mine[0] = lo;
+                dg.mine[2 * a.M] = hi;
+            }
+        }
+        if (ok && cnt) ok = warp_wait(&o_done[w], 0u, abort);
+        tc_fence_after();
+        const bool rows_here = ql < tq && i < a.Lq;
+        if (ok && __any_sync(0xffffffffu, rows_here)) {
+            T* to = gq + ((static_cast<long long>(n) * a.Lq + i) * a.Hq + h0 + g) * a.D;
+            for (int d = 0; d < a.D; d += 32) {
+                uint32_t x[32];
+                if (nw) {
+                    tmem_ld32_async(at_o + d, x);
+                    tmem_ld_wait(x);
+                }
+                if (!rows_here) continue;
+                const bool zero = !nw || !live;
+#pragma unroll
+                for (int e = 0; e < 32; e += 8)
+                    if (d + e < a.D) {
+                        uint32_t u[4];
+#pragma unroll
+                        for (int f = 0; f < 4; ++f)
+                            u[f] = zero ? 0u : pack2<T>(__uint_as_float(x[e + 2 * f]) * a.scale, __uint_as_float(x[e + 2 * f + 1]) * a.scale);
+                        *reinterpret_cast<uint4*>(to + d + e) = make_uint4(u[0], u[1], u[2], u[3]);
+                    }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (tid == 0 && *abort) atomicOr(&g_band_bwd_status, 1u);
+    if (warp == kMma) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmem));
+}
+
+// ---------------------------------------------------------------------------
+// grad_k and grad_v
+// ---------------------------------------------------------------------------
+// Items of an image and key head: every tile of 128 keys in `others` parts along the
+// queries, those of the sinks (which see far more queries than the window) in `sinks`.
+struct KvShape {
+    int tiles, sink_tiles;
+    int sink_parts, other_parts;
+    int floats;             // of a head's bias table
+    __host__ __device__ int items() const { return sink_tiles * sink_parts + (tiles - sink_tiles) * other_parts; }
+    __host__ __device__ bool split() const { return sink_parts > 1 || other_parts > 1; }
+};
+
+template <int NB>
+struct KvCfg {
+    static constexpr int slots = NB == 1 ? 6 : 4;
+    static constexpr int threads = 320;
+    static constexpr int stage = 2 * NB * kTileBlock;      // Q, G
+    static constexpr int stat = kTile * sizeof(float2);
+    static constexpr size_t smem = 1024 + 2 * NB * kTcBlock + slots * (stage + stat);
+};
+
+template <typename T, int NB, bool BIAS>
+__global__ void __launch_bounds__(KvCfg<NB>::threads, 1)
+    grad_kv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_g,
+                   const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, BandArgs a, KvShape sh,
+                   const float2* __restrict__ stats, T* __restrict__ gk, T* __restrict__ gv, float* __restrict__ part) {
+    using C = KvCfg<NB>;
+    constexpr int kSlots = C::slots;
+    extern __shared__ __align__(1024) unsigned char band_smem[];
+    __shared__ __align__(8) uint64_t full[kSlots], empty[kSlots], raw, keys_full, s_full[2], p_full[2], done;
+    __shared__ uint32_t taddr_s;
+    __shared__ int s_abort;
+    const int tid = threadIdx.x, warp = static_cast<int>(uniform(tid >> 5)), lane = tid & 31;
+    const uint32_t base = (smem_u32(band_smem) + 1023u) & ~1023u;
+    const uint32_t ks = base, ring = base + 2 * NB * kTcBlock, stat_at = ring + kSlots * C::stage;
+    const float4* stat_s = reinterpret_cast<const float4*>(band_smem + (stat_at - smem_u32(band_smem)));
+    float* table = reinterpret_cast<float*>(band_smem + (stat_at - smem_u32(band_smem)) + kSlots * C::stat);
+
+    const int items = sh.items(), nh = blockIdx.x / items, item = blockIdx.x - nh * items;
+    const int n = nh / a.Hk, hk = nh - n * a.Hk;
+    const int sink_items = sh.sink_tiles * sh.sink_parts;
+    const bool is_sink = item < sink_items;
+    const int parts = is_sink ? sh.sink_parts : sh.other_parts;
+    const int rest = is_sink ? item : item - sink_items, kt = (is_sink ? 0 : sh.sink_tiles) + rest / parts, prt = rest % parts;
+    const int k0 = kt * kTcRows;
+    const int klen = static_cast<int>(uniform(band_klen(a, n))), qlen = static_cast<int>(uniform(band_qlen(a, n))),
+              start = static_cast<int>(uniform(band_start(a, n)));
+    const int k1 = min(k0 + kTcRows, klen);
+    int ilo = 0, ihi = 0;
+    if (k0 < klen) band_queries(a, start, qlen, k0, k1, ilo, ihi);
+    const int q0 = ilo / kTile, nq = ilo < ihi ? (ihi - 1) / kTile - q0 + 1 : 0;
+    const long long total = static_cast<long long>(nq) * a.G;
+    const int t0 = static_cast<int>(total * prt / parts), cnt = static_cast<int>(total * (prt + 1) / parts) - t0;
+
+    if (tid == 0) {
+        for (int s = 0; s < kSlots; ++s) {
+            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&empty[s]), 1);
+        }
+        mbar_init(smem_u32(&raw), 1);
+        mbar_init(smem_u32(&keys_full), 1);
+        mbar_init(smem_u32(&done), 1);
+        for (int w = 0; w < 2; ++w) {
+            mbar_init(smem_u32(&s_full[w]), 1);
+            mbar_init(smem_u32(&p_full[w]), 4);
+        }
+        s_abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kMma) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&taddr_s)), "r"(kTmem));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    if (BIAS) fill_table<T>(a, table, sh.floats, hk * a.G, a.G, C::threads);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = uniform(taddr_s);
+    volatile int* abort = &s_abort;
+    // step t: queries [tile * 64, + 64) of head hk G + g, of which the chunks [ca, cb) are in [ilo, ihi)
+    auto step_of = [&](int t, int& g, int& i) {
+        g = (t0 + t) / nq;
+        i = (q0 + (t0 + t) - g * nq) * kTile;
+    };
+    auto chunks = [&](int i, int& ca, int& cb) {
+        ca = (max(ilo, i) - i) >> 5;
+        cb = (min(ihi, i + kTile) - i + kTcChunk - 1) >> 5;
+    };
+
+    if (warp == kProducer) {
+        if (cnt && elect_one()) {
+            mbar_expect_tx(smem_u32(&keys_full), 2 * NB * kTcBlock);
+            for (int c = 0; c < NB; ++c) {
+                tma_load_rows(ks + c * kTcBlock, &map_k, c * 64, hk, k0, n, smem_u32(&keys_full));
+                tma_load_rows(ks + (NB + c) * kTcBlock, &map_v, c * 64, hk, k0, n, smem_u32(&keys_full));
+            }
+        }
+        int raws = 0;
+        const int LP = padded_queries(a.Lq);
+        for (int t = 0; t < cnt; ++t) {
+            const int s = t % kSlots;
+            int g, i;
+            step_of(t, g, i);
+            if (!warp_wait(&empty[s], ((t / kSlots) & 1) ^ 1u, abort)) break;
+            const uint32_t at_q = ring + s * C::stage, at_g = at_q + NB * kTileBlock;
+            const bool clear = i + kTile > qlen && qlen < a.Lq;  // queries past the sequence meet p and d of 0
+            if (elect_one()) {
+                const uint32_t bar = smem_u32(clear ? &raw : &full[s]);
+                mbar_expect_tx(bar, C::stage + C::stat);
+                for (int c = 0; c < NB; ++c) {
+                    tma_load_rows(at_q + c * kTileBlock, &map_q, c * 64, hk * a.G + g, i, n, bar);
+                    tma_load_rows(at_g + c * kTileBlock, &map_g, c * 64, hk * a.G + g, i, n, bar);
+                }
+                const float2* src = stats + (static_cast<long long>(n) * a.Hq + hk * a.G + g) * LP + i;
+                asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                                 stat_at + s * C::stat), "l"(src), "r"(C::stat), "r"(bar) : "memory");
+            }
+            if (clear) {
+                if (!warp_wait(&raw, raws++ & 1, abort)) break;
+                zero_rows<2 * NB>(at_q, kTileBlock, max(qlen - i, 0), kTile, lane);
+                if (elect_one()) mbar_arrive(smem_u32(&full[s]));
+            }
+        }
+    } else if (warp == kMma) {
+        if (cnt) {
+            const int steps = (a.D + 15) / 16;
+            const uint32_t id_s = umma_idesc<T>(kTcRows, 0, 0, 0), id_o = umma_idesc<T>(kTcRows, steps * 16, 0, 1);
+            const uint64_t k_desc = umma_desc_sw128(ks, 16, 1024), v_desc = step_desc(k_desc, NB * kTcBlock),
+                           q_desc = umma_desc_sw128(ring, 16, 1024), g_desc = step_desc(q_desc, NB * kTileBlock),
+                           q_sum = umma_desc_sw128(ring, kTileBlock, 1024), g_sum = step_desc(q_sum, NB * kTileBlock);
+            bool ok = warp_wait(&keys_full, 0u, abort);
+            int s = 0;          // slot of step t + 2 as the loop goes on
+            uint32_t ph = 0;
+            auto scores = [&](int t) {
+                int g, i, ca, cb;
+                step_of(t, g, i);
+                chunks(i, ca, cb);
+                ok = ok && warp_wait(&full[s], ph, abort);
+                if (!ok) return;
+                tc_fence_after();
+                const uint32_t off = s * C::stage + ca * kTcChunk * 128, at = tmem + (t & 1) * 128 + ca * kTcChunk;
+                if (elect_one()) {
+                    const uint32_t id = id_s | (static_cast<uint32_t>((cb - ca) * (kTcChunk / 8)) << 17);
+                    issue_rows<NB>(at, k_desc, kTcBlock, step_desc(q_desc, off), kTileBlock, id, steps);
+                    issue_rows<NB>(at + 64, v_desc, kTcBlock, step_desc(g_desc, off), kTileBlock, id, steps);
+                    umma_commit(smem_u32(&s_full[t & 1]));
+                }
+                __syncwarp();
+                s = s + 1 == kSlots ? 0 : s + 1;
+                ph ^= s == 0;
+            };
+            int sum_slot = 0;
+#pragma unroll 1
+            for (int t = -2; t < cnt && ok; ++t) {
+                if (t >= 0) {
+                    int g, i, ca, cb;
+                    step_of(t, g, i);
+                    chunks(i, ca, cb);
+                    if (!(ok = warp_wait(&p_full[t & 1], (t >> 1) & 1, abort))) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint32_t off = sum_slot * C::stage, at = tmem + (t & 1) * 128;
+                        issue_sum<kTile / 16>(tmem + 256, at, step_desc(g_sum, off), id_o, ca * 2, cb * 2, t > 0);
+                        issue_sum<kTile / 16>(tmem + 256 + 64 * NB, at + 64, step_desc(q_sum, off), id_o, ca * 2, cb * 2, t > 0);
+                        umma_commit(smem_u32(&empty[sum_slot]));
+                    }
+                    __syncwarp();
+                    sum_slot = sum_slot + 1 == kSlots ? 0 : sum_slot + 1;
+                }
+                if (t + 2 < cnt) scores(t + 2);  // over the place of p and d of step t
+            }
+            if (elect_one()) umma_commit(smem_u32(&done));
+            __syncwarp();
+            int never = 0;
+            if (!ok && lane == 0) mbar_wait_or(smem_u32(&done), 0u, &never);
+        }
+        __syncwarp();
+    } else if (warp < kProducer) {
+        const int w = warp >> 2, row = tid & 127, j = k0 + row;
+        const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const uint32_t at_s = lane_base + w * 128;
+        const bool warp_live = k0 + (warp & 3) * 32 < klen;
+        // queries that see this key
+        const int vlo = j - a.right - start, vhi = j >= klen ? 0 : j < a.sinks ? qlen : min(qlen, j + a.left - start + 1);
+        // queries that see every key of the tile
+        const int all_lo = k1 - 1 - a.right - start, all_hi = (k1 <= a.sinks ? qlen : min(qlen, k0 + a.left - start + 1)) - kTcChunk;
+        const float sc = BIAS ? a.scale : a.scale * kLog2e;
+        bool ok = true;
+        int s = w;
+        for (int t = w; t < cnt; t += 2) {
+            int g, i, ca, cb;
+            step_of(t, g, i);
+            chunks(i, ca, cb);
+            // the scores, and (the loads' own barrier) the queries' stats
+            ok = warp_wait(&full[s], (t / kSlots) & 1, abort) && warp_wait(&s_full[w], (t >> 1) & 1, abort);
+            if (!ok) break;
+            tc_fence_after();
+            if (warp_live) {
+                const float4* st = stat_s + s * (C::stat / 16);
+                const float* tab = table + g * sh.floats + a.M + kTableExtra + j - start;
+                uint32_t x[32], y[32];
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) {
+                    if (c < ca || c >= cb) continue;
+                    const int ic = i + c * kTcChunk;
+                    tmem_ld32_async(at_s + c * kTcChunk, x);
+                    tmem_ld32_async(at_s + 64 + c * kTcChunk, y);
+                    tmem_ld_wait(x);
+                    tmem_ld_wait(y);
+                    // relative positions k0 - (start + ic + 31) ... k1 - 1 - (start + ic)
+                    const int side = k0 - (start + ic + kTcChunk - 1) >= a.M ? 1 : k1 - 1 - (start + ic) <= -a.M ? -1 : 0;
+                    const float bb = BIAS ? table[g * sh.floats + (side > 0 ? sh.floats - 1 : 0)] : 0.f;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const float4 u = st[(c * kTcChunk + e) >> 1];  // lse, delta of two queries
+                        float p0, p1;
+                        if (BIAS) {
+                            p0 = ex2((fmaf(__uint_as_float(x[e]), sc, side ? bb : tab[-(ic + e)]) - u.x) * kLog2e);
+                            p1 = ex2((fmaf(__uint_as_float(x[e + 1]), sc, side ? bb : tab[-(ic + e + 1)]) - u.z) * kLog2e);
+                        } else {
+                            p0 = ex2(fmaf(__uint_as_float(x[e]), sc, -u.x));
+                            p1 = ex2(fmaf(__uint_as_float(x[e + 1]), sc, -u.z));
+                        }
+                        x[e] = __float_as_uint(p0);
+                        x[e + 1] = __float_as_uint(p1);
+                        y[e] = __float_as_uint(p0 * (__uint_as_float(y[e]) - u.y));
+                        y[e + 1] = __float_as_uint(p1 * (__uint_as_float(y[e + 1]) - u.w));
+                    }
+                    if (ic < all_lo || ic > all_hi) {
+                        const uint32_t see = low_bits(vhi - ic) & ~low_bits(vlo - ic);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!(see & (1u << e))) x[e] = y[e] = 0u;
+                    }
+                    uint32_t p[16], d[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        p[e] = pack2<T>(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+                        d[e] = pack2<T>(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1]));
+                    }
+                    tmem_st16(at_s + c * 16, p);
+                    tmem_st16(at_s + 64 + c * 16, d);
+                }
+                tmem_st_wait();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&p_full[w]));
+            s += 2;
+            if (s >= kSlots) s -= kSlots;
+        }
+        if (ok && cnt) ok = warp_wait(&done, 0u, abort);
+        tc_fence_after();
+        // the first four warps store gv, the others gk
+        const bool row_here = parts > 1 || j < a.Lk;
+        const uint32_t at_o = lane_base + 256 + w * 64 * NB;
+        const float f = w ? a.scale : 1.f;
+        const bool zero = !cnt || j >= klen;
+        T* to = (w ? gk : gv) + ((static_cast<long long>(n) * a.Lk + j) * a.Hk + hk) * a.D;
+        float* po = part + ((static_cast<long long>(blockIdx.x) * 2 + w) * kTcRows + row) * a.D;
+        for (int d = 0; d < a.D && ok; d += 32) {
+            uint32_t x[32];
+            if (cnt) {
+                tmem_ld32_async(at_o + d, x);
+                tmem_ld_wait(x);
+            }
+            if (!row_here) continue;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] = zero ? 0u : __float_as_uint(__uint_as_float(x[e]) * f);
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+                if (d + e >= a.D) continue;
+                if (parts > 1) {
+                    *reinterpret_cast<uint4*>(po + d + e) = make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+                    *reinterpret_cast<uint4*>(po + d + e + 4) = make_uint4(x[e + 4], x[e + 5], x[e + 6], x[e + 7]);
+                } else {
+                    uint32_t u[4];
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) u[v] = pack2<T>(__uint_as_float(x[e + 2 * v]), __uint_as_float(x[e + 2 * v + 1]));
+                    *reinterpret_cast<uint4*>(to + d + e) = make_uint4(u[0], u[1], u[2], u[3]);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (tid == 0 && *abort) atomicOr(&g_band_bwd_status, 1u);
+    if (warp == kMma) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmem));
+}
+
+// Sums the parts of tiles that were split, in order: a thread per four entries.
+template <typename T>
+__global__ void __launch_bounds__(256) kv_join_kernel(BandArgs a, KvShape sh, int tiles, const float* __restrict__ part,
+                                                      T* __restrict__ gk, T* __restrict__ gv) {
+    const int D4 = a.D / 4;
+    const long long per = static_cast<long long>(tiles) * kTcRows * D4 * 2, e = blockIdx.x * 256ll + threadIdx.x;
+    if (e >= per * a.N * a.Hk) return;
+    const long long nh = e / per;
+    long long r = e - nh * per;
+    const int d = static_cast<int>(r % D4) * 4;
+    r /= D4;
+    const int row = static_cast<int>(r % kTcRows);
+    r /= kTcRows;
+    const int side = static_cast<int>(r & 1), kt = static_cast<int>(r >> 1), j = kt * kTcRows + row;
+    if (j >= a.Lk) return;
+    const bool sink = kt < sh.sink_tiles;
+    const int parts = sink ? sh.sink_parts : sh.other_parts;
+    if (parts == 1) return;
+    const int first = sink ? kt * parts : sh.sink_tiles * sh.sink_parts + (kt - sh.sink_tiles) * parts;
+    const float* p = part + (((nh * sh.items() + first) * 2 + side) * kTcRows + row) * a.D + d;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = 0; i < parts; ++i) {
+        const float4 v = *reinterpret_cast<const float4*>(p + static_cast<long long>(i) * 2 * kTcRows * a.D);
+        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+    const long long n = nh / a.Hk, hk = nh - n * a.Hk;
+    T* to = (side ? gk : gv) + ((n * a.Lk + j) * a.Hk + hk) * a.D + d;
+    *reinterpret_cast<uint2*>(to) = make_uint2(pack2<T>(s.x, s.y), pack2<T>(s.z, s.w));
+}
+
+// sums[h][rel] = the warps' diagonal sums of head h over images and rows, in a fixed order.
+__global__ void __launch_bounds__(256) diag_sum_kernel(BandArgs a, int rowwarps, const float* __restrict__ diag, float* __restrict__ sums) {
+    __shared__ float s_part[8][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.y, len = 2 * a.M + 1, rel = blockIdx.x * 32 + lane;
+    const long long rows = static_cast<long long>(a.N) * rowwarps;
+    float s = 0.f;
+    if (rel < len) {
+#pragma unroll 8
+        for (long long r = warp; r < rows; r += 8) {
+            const long long n = r / rowwarps;
+            s += diag[((n * a.Hq + h) * rowwarps + r - n * rowwarps) * len + rel];
+        }
+    }
+    s_part[warp][lane] = s;
+    __syncthreads();
+    if (warp || rel >= len) return;
+    for (int w = 1; w < 8; ++w) s += s_part[w][lane];
+    sums[static_cast<long long>(h) * len + rel] = s;
+}
+
+// gbias[b][h]: a warp sums the relative positions of its bucket.
+template <typename T>
+__global__ void __launch_bounds__(256) bucket_sum_kernel(BandArgs a, const float* __restrict__ sums, T* __restrict__ gbias) {
+    const int e = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31, len = 2 * a.M + 1;
+    if (e >= a.nb * a.Hq) return;
+    const int b = e / a.Hq, h = e - b * a.Hq;
+    float s = 0.f;
+    for (int r = lane; r < len; r += 32)
+        if (__ldg(a.buckets + r) == b) s += sums[static_cast<long long>(h) * len + r];
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) gbias[e] = from_f32<T>(s);
+}
+
+KvShape kv_shape(const BandArgs& a) {
+    KvShape s;
+    s.floats = a.nb ? table_floats(a.M) : 0;
+    s.tiles = (a.Lk + kTcRows - 1) / kTcRows;
+    // the tiles a window leaves behind see about `left + right` queries, those of the sinks all that follow
+    const long long reach = std::min<long long>(a.Lq, static_cast<long long>(std::min(a.left, kBandMaxLen)) + std::min(a.right, kBandMaxLen) + kTcRows);
+    s.sink_tiles = a.left < kBandFar ? std::min((a.sinks + kTcRows - 1) / kTcRows, s.tiles) : 0;
+    const int wide = (a.Lq + kTile - 1) / kTile, narrow = static_cast<int>((reach + kTile - 1) / kTile) + 1;
+    // parts until every SM has a CTA, none shorter than four steps
+    const long long ctas = static_cast<long long>(a.N) * a.Hk * s.tiles;
+    const long long want = std::max<long long>(1, kBandSms / ctas);
+    s.other_parts = static_cast<int>(std::min<long long>(want, std::max<long long>(1, static_cast<long long>(narrow) * a.G / 4)));
+    s.sink_parts = s.other_parts;
+    if (s.sink_tiles) {  // parts about as long as a window, while that keeps the parts' memory small
+        const long long each = static_cast<long long>(a.N) * a.Hk * s.sink_tiles, most = (4 * kBandSms + each - 1) / each;
+        s.sink_parts = static_cast<int>(std::max<long long>(s.other_parts, std::min<long long>(static_cast<long long>(s.other_parts) * ((wide + narrow - 1) / narrow), most)));
+    }
+    return s;
+}
+
+size_t up256(size_t b) { return (b + 255) / 256 * 256; }
+size_t stats_bytes(const BandArgs& a) { return up256(static_cast<size_t>(a.N) * a.Hq * padded_queries(a.Lq) * sizeof(float2)); }
+size_t part_bytes(const BandArgs& a, const KvShape& s) {
+    return s.split() ? up256(static_cast<size_t>(a.N) * a.Hk * s.items() * 2 * kTcRows * a.D * sizeof(float)) : 0;
+}
+size_t diag_rows(const BandArgs& a) { return static_cast<size_t>(a.N) * a.Hq * ((a.Lq + 31) / 32); }
+size_t diag_bytes(const BandArgs& a) { return a.nb ? up256(diag_rows(a) * (2 * a.M + 1) * sizeof(float)) : 0; }
+size_t sums_bytes(const BandArgs& a) { return a.nb ? up256(static_cast<size_t>(a.Hq) * (2 * a.M + 1) * sizeof(float)) : 0; }
+
+template <typename K>
+cudaError_t allow_smem(K kernel, size_t bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+}
+
+template <typename T, int NB, bool BIAS>
+cudaError_t launch(const BandArgs& a, const void* out, const float* lse, const void* gout, void* gq, void* gk, void* gv, void* gbias,
+                   void* ws, cudaStream_t stream) {
+    char* at = static_cast<char*>(ws);
+    const KvShape kv = kv_shape(a);
+    float2* stats = reinterpret_cast<float2*>(at);
+    float* part = reinterpret_cast<float*>(at += stats_bytes(a));
+    float* diag = reinterpret_cast<float*>(at += part_bytes(a, kv));
+    float* sums = reinterpret_cast<float*>(at += diag_bytes(a));
+    const int pack = BIAS ? 1 : a.G, tq = kTcRows / pack, blocks = (a.Lq + 2 * tq - 1) / (2 * tq);
+    const long long dense = static_cast<long long>(a.Hq) * a.D;
+    const size_t smem_q = QCfg<NB>::smem + (BIAS ? table_floats(a.M) * sizeof(float) : 0),
+                 smem_kv = KvCfg<NB>::smem + (BIAS ? static_cast<size_t>(a.G) * kv.floats * sizeof(float) : 0);
+    // (first, for the context: another thread may run the backward, and the maps' encoder asks for one)
+    cudaError_t e = allow_smem(grad_q_kernel<T, NB, BIAS>, smem_q);
+    if (e == cudaSuccess) e = allow_smem(grad_kv_kernel<T, NB, BIAS>, smem_kv);
+    if (e == cudaSuccess && BIAS) e = cudaMemsetAsync(diag, 0, diag_bytes(a), stream);
+    if (e != cudaSuccess) return e;
+    CUtensorMap mq, mg, mk, mv, mq1, mg1, mk1, mv1;
+    if (!make_map(&mq, a.dtype, a.q, a.N, a.Lq, a.Hq, a.D, a.q_batch, a.q_row, pack, tq) ||
+        !make_map(&mg, a.dtype, gout, a.N, a.Lq, a.Hq, a.D, dense * a.Lq, dense, pack, tq) ||
+        !make_map(&mk, a.dtype, a.k, a.N, a.Lk, a.Hk, a.D, a.k_batch, a.k_row, 1, kTile) ||
+        !make_map(&mv, a.dtype, a.v, a.N, a.Lk, a.Hk, a.D, a.v_batch, a.v_row, 1, kTile) ||
+        !make_map(&mq1, a.dtype, a.q, a.N, a.Lq, a.Hq, a.D, a.q_batch, a.q_row, 1, kTile) ||
+        !make_map(&mg1, a.dtype, gout, a.N, a.Lq, a.Hq, a.D, dense * a.Lq, dense, 1, kTile) ||
+        !make_map(&mk1, a.dtype, a.k, a.N, a.Lk, a.Hk, a.D, a.k_batch, a.k_row, 1, kTcRows) ||
+        !make_map(&mv1, a.dtype, a.v, a.N, a.Lk, a.Hk, a.D, a.v_batch, a.v_row, 1, kTcRows))
+        return cudaErrorInvalidValue;
+    const long long rows = static_cast<long long>(a.N) * padded_queries(a.Lq) * a.Hq;
+    stats_kernel<T><<<static_cast<unsigned>((rows + 15) / 16), 256, 0, stream>>>(a, static_cast<const T*>(out), lse,
+                                                                              static_cast<const T*>(gout), stats);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    grad_q_kernel<T, NB, BIAS><<<static_cast<unsigned>(static_cast<long long>(a.N) * (a.Hq / pack) * blocks), QCfg<NB>::threads, smem_q, stream>>>(
+        mq, mg, mk, mv, a, pack, tq, blocks, BIAS ? table_floats(a.M) : 0, stats, static_cast<T*>(gq), diag);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    grad_kv_kernel<T, NB, BIAS><<<static_cast<unsigned>(static_cast<long long>(a.N) * a.Hk * kv.items()), KvCfg<NB>::threads, smem_kv, stream>>>(
+        mq1, mg1, mk1, mv1, a, kv, stats, static_cast<T*>(gk), static_cast<T*>(gv), part);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (kv.split()) {
+        const int tiles = kv.other_parts > 1 ? kv.tiles : kv.sink_tiles;
+        const long long n4 = static_cast<long long>(a.N) * a.Hk * tiles * kTcRows * (a.D / 4) * 2;
+        kv_join_kernel<T><<<static_cast<unsigned>((n4 + 255) / 256), 256, 0, stream>>>(a, kv, tiles, part, static_cast<T*>(gk), static_cast<T*>(gv));
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    if (!BIAS || !gbias) return cudaSuccess;
+    diag_sum_kernel<<<dim3((2 * a.M + 32) / 32, a.Hq), 256, 0, stream>>>(a, (a.Lq + 31) / 32, diag, sums);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    bucket_sum_kernel<T><<<(a.nb * a.Hq + 7) / 8, 256, 0, stream>>>(a, sums, static_cast<T*>(gbias));
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+// The bias tables of all heads that share a key head have to fit shared memory.
+bool band_bwd_tc_fits(const BandArgs& a) {
+    return a.dtype != 0 && (!a.nb || static_cast<size_t>(a.G) * table_floats(a.M) * sizeof(float) <= kTableBytes);
+}
+
+size_t band_bwd_tc_workspace(const BandArgs& a) {
+    return stats_bytes(a) + part_bytes(a, kv_shape(a)) + diag_bytes(a) + sums_bytes(a);
+}
+
+cudaError_t launch_band_bwd_tc(const BandArgs& a, const void* out, const float* lse, const void* gout, void* gq, void* gk, void* gv,
+                               void* gbias, void* ws, cudaStream_t stream) {
+#define DCN4_BAND_BWD(T, NB)                                                                              \
+    (a.nb ? launch<T, NB, true>(a, out, lse, gout, gq, gk, gv, gbias, ws, stream)                         \
+          : launch<T, NB, false>(a, out, lse, gout, gq, gk, gv, gbias, ws, stream))
+    if (a.dtype == 1) return a.D > 64 ? DCN4_BAND_BWD(__half, 2) : DCN4_BAND_BWD(__half, 1);
+    return a.D > 64 ? DCN4_BAND_BWD(__nv_bfloat16, 2) : DCN4_BAND_BWD(__nv_bfloat16, 1);
+#undef DCN4_BAND_BWD
+}
+
+cudaError_t band_bwd_status(unsigned* status, bool reset) {
+    cudaError_t e = cudaMemcpyFromSymbol(status, g_band_bwd_status, sizeof(unsigned));
+    if (e == cudaSuccess && reset) {
+        const unsigned zero = 0;
+        e = cudaMemcpyToSymbol(g_band_bwd_status, &zero, sizeof(unsigned));
+    }
+    return e;
+}
+
+}  // namespace dcn4

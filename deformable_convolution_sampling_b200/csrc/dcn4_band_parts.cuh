@@ -49,6 +49,13 @@ size_t band_fwd_tc_part_bytes(const BandArgs& a);
 cudaError_t launch_band_fwd_tc(const BandArgs& a, void* out, float* lse, void* ws, cudaStream_t stream);
 cudaError_t band_fwd_status(unsigned* status, bool reset);
 
+// 16-bit backward on the tensor cores (dcn4_band_bwd_tc.cu), where it fits.
+bool band_bwd_tc_fits(const BandArgs& a);
+size_t band_bwd_tc_workspace(const BandArgs& a);
+cudaError_t launch_band_bwd_tc(const BandArgs& a, const void* out, const float* lse, const void* gout, void* gq, void* gk, void* gv,
+                               void* gbias, void* ws, cudaStream_t stream);
+cudaError_t band_bwd_status(unsigned* status, bool reset);
+
 // Every type on the fp32 pipes (dcn4_band_simt.cu).
 int simt_row_blocks(const BandArgs& a);
 int simt_splits(const BandArgs& a);
