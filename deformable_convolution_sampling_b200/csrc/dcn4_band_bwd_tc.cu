@@ -5,11 +5,18 @@
 //             nothing: their probabilities are then 0 without a mask).
 //   grad_q    a CTA holds two tiles of 128 rows and streams tiles of 64 keys:
 //             S = Q K^T, E = G V^T, d = p (E - delta), p = e^(S - lse), gq += d K.
-//             With a bias it also sums d along the diagonals (see diagonal sums).
 //   grad_kv   a CTA holds 128 keys and streams tiles of 64 queries of every head
-//             that shares them: S^T = K Q^T, E^T = V G^T, gv += p^T G, gk += d^T Q.
+//             that shares them: S^T = K Q^T, E^T = V G^T, gv += p^T G, gk += d^T Q;
+//             with a bias it also sums d along the diagonals (see there).
 // Scores are recomputed by both kernels (7 products instead of 5): one kernel would
 // have to add every gq from many CTAs, in an order that changes.
+//
+// out is rounded, so delta is off, by the same amount for all of a row's d.  The
+// sum of a row's d is that error (it is 0 otherwise), so grad_q corrects delta by it
+// for grad_kv, where it would add up: over the pairs of a bucket most of all.  For
+// gq the error weighs as the mean of a row's keys, that is with the root of their
+// number: where rows see at most kFewKeys, grad_q goes over the keys twice and takes
+// delta = sum p E from the first pass (one more pass of two of its three products).
 //
 // p and d go to the tensor cores as the I/O type, over the scores they came from in
 // tensor memory; the sums stay there in fp32 until they are rounded once.
@@ -26,6 +33,7 @@ constexpr int kTileBlock = kTile * 128;                // bytes of 64 of its col
 constexpr int kTableExtra = 160;                       // as in the forward: a chunk and a tile's rows past M
 constexpr int kTableBytes = 28 << 10;
 constexpr int kTmem = 512;
+constexpr int kFewKeys = 512;
 
 __device__ unsigned g_band_bwd_status;
 
@@ -84,63 +92,11 @@ struct QCfg {
     static constexpr size_t smem = 1024 + 4 * NB * kTcBlock + slots * 2 * NB * kTileBlock;
 };
 
-// Diagonal sums.  All pairs of a diagonal of the score matrix share a relative
-// position, so the bias gradient is the sum of d along diagonals, then over the
-// diagonals of a bucket.  A lane holds a row; as the columns go by, a partial sum
-// moves from lane to lane: after column j, lane i holds the sum over rows 0..i of
-// the diagonal through (i, j).  Lane 31's is complete, and is handed to lane j mod 32,
-// so that 32 columns end in one store of 32 neighbouring relative positions: two
-// shuffles a column, no shared memory, no atomics, one order.
-struct Diagonals {
-    float* mine;    // this warp's sums, of relative position -M .. M (the ends: and beyond)
-    int M, pos31;   // position of lane 31's query
-    int next;       // key the run goes on with; -1: no run
-    bool again;     // a run has been stored already: add
-    float s, below, above;
-    __device__ __forceinline__ void store(int j, int lane, float v) {
-        const int rel = j + lane - pos31;
-        if (rel <= -M) below += v;
-        else if (rel >= M) above += v;
-        else {
-            float* to = mine + rel + M;
-            *to = again ? *to + v : v;
-        }
-    }
-    __device__ __forceinline__ void flush(int lane) {
-        if (next < 0) return;
-        float got = 0.f;
-        for (int e = 0; e < 31; ++e) {
-            s = __shfl_up_sync(0xffffffffu, s, 1);
-            if (lane == 0) s = 0.f;
-            const float o = __shfl_sync(0xffffffffu, s, 31);
-            if (lane == e) got = o;
-        }
-        store(next, lane, got);  // lane 31 adds a 0
-        __syncwarp();
-        again = true;
-        next = -1;
-        s = 0.f;
-    }
-    __device__ __forceinline__ void chunk(int j, int lane, const uint32_t (&d)[32]) {
-        if (j != next) flush(lane);
-        float got = 0.f;
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-            s = __shfl_up_sync(0xffffffffu, s, 1);
-            s = (lane == 0 ? 0.f : s) + __uint_as_float(d[e]);
-            const float o = __shfl_sync(0xffffffffu, s, 31);
-            if (lane == e) got = o;
-        }
-        store(j, lane, got);
-        next = j + 32;
-    }
-};
-
 template <typename T, int NB, bool BIAS>
 __global__ void __launch_bounds__(QCfg<NB>::threads, 1)
     grad_q_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_g,
                   const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, BandArgs a, int pack,
-                  int tq, int blocks, int floats, const float2* __restrict__ stats, T* __restrict__ gq, float* __restrict__ diag) {
+                  int tq, int blocks, int floats, int twice, float2* __restrict__ stats, T* __restrict__ gq) {
     constexpr int kSlots = QCfg<NB>::slots;
     extern __shared__ __align__(1024) unsigned char band_smem[];
     __shared__ __align__(8) uint64_t full[kSlots], empty[kSlots], raw, rows_full, s_full[2], p_full[2], o_done[2];
@@ -178,7 +134,7 @@ __global__ void __launch_bounds__(QCfg<NB>::threads, 1)
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&taddr_s)), "r"(kTmem));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
-    if (BIAS) fill_table<T>(a, table, floats, h0, 1, QCfg<NB>::threads);
+    if (BIAS) fill_table<T>(a, table, floats, h0, pack, QCfg<NB>::threads);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -187,7 +143,9 @@ __global__ void __launch_bounds__(QCfg<NB>::threads, 1)
 
     BandTiles bt{0, 0, 0};
     if (i0 <= i1) bt = band_tiles(a, start + i0, start + i1, klen, kTile);
-    const int cnt = bt.count();
+    // tiles to go over: with `twice`, first for delta alone
+    const int tiles = bt.count(), first = twice ? tiles : 0, cnt = first + tiles;
+    auto tile_at = [&](int t) { return bt.tile(t < first ? t : t - first) * kTile; };
     // what a half's rows see of key tile t: chunks [ca, cb)
     auto band_of = [&](int w, int& plo, int& phi) {
         plo = start + i0 + w * tq;
@@ -196,7 +154,7 @@ __global__ void __launch_bounds__(QCfg<NB>::threads, 1)
     auto active = [&](int w, int t, int& ca, int& cb) {
         int plo, phi;
         band_of(w, plo, phi);
-        const int j0 = bt.tile(t) * kTile, end = min(klen, phi + a.right + 1), sink = min(min(a.sinks, end), j0 + kTile);
+        const int j0 = tile_at(t), end = min(klen, phi + a.right + 1), sink = min(min(a.sinks, end), j0 + kTile);
         int lo = max(max(0, plo - a.left), j0), hi = min(end, j0 + kTile);
         if (sink > j0) {
             if (lo >= hi) hi = sink;
@@ -218,7 +176,7 @@ __global__ void __launch_bounds__(QCfg<NB>::threads, 1)
         }
         int raws = 0;
         for (int t = 0; t < cnt; ++t) {
-            const int s = t % kSlots, j0 = bt.tile(t) * kTile;
+            const int s = t % kSlots, j0 = tile_at(t);
             if (!warp_wait(&empty[s], ((t / kSlots) & 1) ^ 1u, abort)) break;
             const uint32_t at_k = ring + s * 2 * NB * kTileBlock, at_v = at_k + NB * kTileBlock;
             const bool clear = j0 + kTile > klen && klen < a.Lk;  // keys past the sequence meet d of 0
@@ -267,9 +225,11 @@ __global__ void __launch_bounds__(QCfg<NB>::threads, 1)
                     if (!(ok = warp_wait(&p_full[w], p_phase, abort))) break;
                     tc_fence_after();
                     p_phase ^= 1u;
-                    if (elect_one()) issue_sum<kTile / 16>(at_o, at_s, step_desc(k_sum, off), id_o, ca * 2, cb * 2, some);
-                    __syncwarp();
-                    some = true;
+                    if (t >= first) {
+                        if (elect_one()) issue_sum<kTile / 16>(at_o, at_s, step_desc(k_sum, off), id_o, ca * 2, cb * 2, some);
+                        __syncwarp();
+                        some = true;
+                    }
                 }
                 if (elect_one()) umma_commit(smem_u32(&empty[s]));
                 __syncwarp();
@@ -291,27 +251,22 @@ __global__ void __launch_bounds__(QCfg<NB>::threads, 1)
         int plo, phi;
         band_of(w, plo, phi);
         const int pos = start + i;
-        const int jlo = max(0, pos - a.left), jhi = live ? min(klen, pos + a.right + 1) : 0, jsink = min(a.sinks, jhi);
-        // keys that all rows of the tile see (with a bias a dead row's d must be 0, so its tile is masked)
-        const int all_lo = BIAS && phi - plo + 1 < tq ? kBandFar : phi - a.left, all_hi = min(klen, plo + a.right + 1) - kTcChunk;
-        const float2 st = live ? stats[(static_cast<long long>(n) * a.Hq + h0 + g) * padded_queries(a.Lq) + i] : make_float2(INFINITY, 0.f);
+        const int jlo = max(0, pos - a.left), jhi = min(klen, pos + a.right + 1), jsink = min(a.sinks, jhi);
+        const int all_lo = phi - a.left, all_hi = min(klen, plo + a.right + 1) - kTcChunk;  // keys that all rows of the tile see
+        float2* stat = stats + (static_cast<long long>(n) * a.Hq + h0 + g) * padded_queries(a.Lq) + i;
+        const float2 st = live ? *stat : make_float2(INFINITY, 0.f);
+        float delta = twice ? 0.f : st.y, off = 0.f;  // off: the sum of the row's d, or in the first pass of p E
         const float sc = BIAS ? a.scale : a.scale * kLog2e;
-        const float* tab = table + a.M + kTableExtra - pos;
-        Diagonals dg;
-        if (BIAS) {
-            const int rowwarps = (a.Lq + 31) / 32, first = (i0 + w * tq) / 32 + (warp & 3);  // pack is 1: 32 queries a warp
-            dg.mine = diag + ((static_cast<long long>(n) * a.Hq + h0) * rowwarps + min(first, rowwarps - 1)) * (2 * a.M + 1);
-            dg.M = a.M;
-            dg.pos31 = start + i0 + w * tq + (warp & 3) * 32 + 31;
-            dg.next = -1;
-            dg.again = false;
-            dg.s = dg.below = dg.above = 0.f;
-        }
+        const float* tab = table + g * floats + a.M + kTableExtra - pos;
         int nw = 0, ca, cb;
         bool ok = true;
         for (int t = 0; t < cnt; ++t) {
+            if (t == first && twice) {
+                delta = off;
+                off = 0.f;
+            }
             if (!active(w, t, ca, cb)) continue;
-            const int j0 = bt.tile(t) * kTile;
+            const int j0 = tile_at(t);
             if (!(ok = warp_wait(&s_full[w], nw & 1, abort))) break;
             tc_fence_after();
             if (warp_live) {
@@ -330,7 +285,7 @@ __global__ void __launch_bounds__(QCfg<NB>::threads, 1)
                     tmem_ld_wait(y[c]);
                     const int side = j - phi >= a.M ? 1 : j + kTcChunk - 1 - plo <= -a.M ? -1 : 0;
                     if (BIAS) {
-                        const float bb = table[side > 0 ? floats - 1 : 0];
+                        const float bb = table[g * floats + (side > 0 ? floats - 1 : 0)];
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
                             x[c][e] = __float_as_uint((fmaf(__uint_as_float(x[c][e]), sc, side ? bb : tab[j + e]) - st.x) * kLog2e);
@@ -340,57 +295,31 @@ __global__ void __launch_bounds__(QCfg<NB>::threads, 1)
                     }
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
-                        x[c][e] = __float_as_uint(ex2(__uint_as_float(x[c][e])) * (__uint_as_float(y[c][e]) - st.y));
+                        x[c][e] = __float_as_uint(ex2(__uint_as_float(x[c][e])) * (__uint_as_float(y[c][e]) - delta));
                     if (j < all_lo || j > all_hi) {
                         const uint32_t see = (low_bits(jhi - j) & ~low_bits(jlo - j)) | low_bits(jsink - j);
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
                             if (!(see & (1u << e))) x[c][e] = 0u;
                     }
+                    float2 sum[2] = {};
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) add2(sum[(e >> 1) & 1], x[c][e], x[c][e + 1]);
+                    off += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                    if (t < first) continue;
                     uint32_t p[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) p[e >> 1] = pack2<T>(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
                     tmem_st16(at_s + c * 16, p);
                 }
                 tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&p_full[w]));
-                if (BIAS) {  // under the product of this tile
-#pragma unroll
-                    for (int c = 0; c < kChunks; ++c) {
-                        if (c < ca || c >= cb) continue;
-                        const int j = j0 + c * kTcChunk;
-                        // the warp's own rows: 32 queries up to pos31
-                        const bool above = j - dg.pos31 >= a.M, below = j + kTcChunk - 1 - (dg.pos31 - 31) <= -a.M;
-                        if (above || below) {
-                            float s = 0.f;
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) s += __uint_as_float(x[c][e]);
-                            (above ? dg.above : dg.below) += s;
-                        } else {
-                            dg.chunk(j, lane, x[c]);
-                        }
-                    }
-                }
-            } else {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&p_full[w]));
             }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&p_full[w]));
             ++nw;
         }
-        if (BIAS && warp_live) {
-            dg.flush(lane);
-            float lo = dg.below, hi = dg.above;
-            for (int o = 16; o; o >>= 1) {
-                lo += __shfl_xor_sync(0xffffffffu, lo, o);
-                hi += __shfl_xor_sync(0xffffffffu, hi, o);
-            }
-            if (lane == 0) {
-                dg.mine[0] = lo;
-                dg.mine[2 * a.M] = hi;
-            }
-        }
+        if (ok && live) stat->y = delta + off;
         if (ok && cnt) ok = warp_wait(&o_done[w], 0u, abort);
         tc_fence_after();
         const bool rows_here = ql < tq && i < a.Lq;
@@ -435,6 +364,75 @@ struct KvShape {
     __host__ __device__ bool split() const { return sink_parts > 1 || other_parts > 1; }
 };
 
+// Diagonal sums.  All pairs of a diagonal of the score matrix share a relative
+// position, so the bias gradient is the sum of d along diagonals, then over the
+// diagonals of a bucket.  A lane holds a key; as the queries go by, a partial sum
+// moves from lane to lane: after query i, lane j holds the sum over the warp's keys
+// up to its own of the diagonal through (i, j).  Lane 31's is complete, and is handed
+// to lane i mod 32, so that 32 queries end in one store of 32 neighbouring relative
+// positions: two shuffles a query, no shared memory, no atomics, one order.
+struct Diagonals {
+    float* mine;    // this warp's sums, of relative position -M .. M (the ends: and beyond)
+    int M, rel31;   // relative position of lane 31's key and query 0
+    int next;       // query the run goes on with; -1: no run
+    bool again;     // a run of this head has been stored already: add
+    float s, below, above;
+    __device__ __forceinline__ void start(float* to) {
+        mine = to;
+        next = -1;
+        again = false;
+        s = below = above = 0.f;
+    }
+    __device__ __forceinline__ void store(int i, int lane, float v) {
+        const int rel = rel31 - i - lane;
+        if (rel <= -M) below += v;
+        else if (rel >= M) above += v;
+        else {
+            float* to = mine + rel + M;
+            *to = again ? *to + v : v;
+        }
+    }
+    __device__ __forceinline__ void flush(int lane) {
+        if (next < 0) return;
+        float got = 0.f;
+        for (int e = 0; e < 31; ++e) {
+            s = __shfl_up_sync(0xffffffffu, s, 1);
+            if (lane == 0) s = 0.f;
+            const float o = __shfl_sync(0xffffffffu, s, 31);
+            if (lane == e) got = o;
+        }
+        store(next, lane, got);  // lane 31 adds a 0
+        __syncwarp();
+        again = true;
+        next = -1;
+        s = 0.f;
+    }
+    __device__ __forceinline__ void chunk(int i, int lane, const uint32_t (&d)[32]) {
+        if (i != next) flush(lane);
+        float got = 0.f;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+            s = __shfl_up_sync(0xffffffffu, s, 1);
+            s = (lane == 0 ? 0.f : s) + __uint_as_float(d[e]);
+            const float o = __shfl_sync(0xffffffffu, s, 31);
+            if (lane == e) got = o;
+        }
+        store(i, lane, got);
+        next = i + 32;
+    }
+    __device__ __forceinline__ void finish(int lane) {
+        flush(lane);
+        for (int o = 16; o; o >>= 1) {
+            below += __shfl_xor_sync(0xffffffffu, below, o);
+            above += __shfl_xor_sync(0xffffffffu, above, o);
+        }
+        if (lane == 0) {
+            mine[0] = below;
+            mine[2 * M] = above;
+        }
+    }
+};
+
 template <int NB>
 struct KvCfg {
     static constexpr int slots = NB == 1 ? 6 : 4;
@@ -448,7 +446,8 @@ template <typename T, int NB, bool BIAS>
 __global__ void __launch_bounds__(KvCfg<NB>::threads, 1)
     grad_kv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_g,
                    const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, BandArgs a, KvShape sh,
-                   const float2* __restrict__ stats, T* __restrict__ gk, T* __restrict__ gv, float* __restrict__ part) {
+                   const float2* __restrict__ stats, T* __restrict__ gk, T* __restrict__ gv, float* __restrict__ part,
+                   float* __restrict__ diag) {
     using C = KvCfg<NB>;
     constexpr int kSlots = C::slots;
     extern __shared__ __align__(1024) unsigned char band_smem[];
@@ -503,9 +502,13 @@ __global__ void __launch_bounds__(KvCfg<NB>::threads, 1)
     const uint32_t tmem = uniform(taddr_s);
     volatile int* abort = &s_abort;
     // step t: queries [tile * 64, + 64) of head hk G + g, of which the chunks [ca, cb) are in [ilo, ihi)
+    // (even steps go through the first half of them, odd ones through the second: each softmax
+    // half then meets neighbouring tiles)
+    const int half = (cnt + 1) >> 1;
     auto step_of = [&](int t, int& g, int& i) {
-        g = (t0 + t) / nq;
-        i = (q0 + (t0 + t) - g * nq) * kTile;
+        const int u = t0 + (t >> 1) + (t & 1 ? half : 0);
+        g = u / nq;
+        i = (q0 + u - g * nq) * kTile;
     };
     auto chunks = [&](int i, int& ca, int& cb) {
         ca = (max(ilo, i) - i) >> 5;
@@ -607,14 +610,24 @@ __global__ void __launch_bounds__(KvCfg<NB>::threads, 1)
         const bool warp_live = k0 + (warp & 3) * 32 < klen;
         // queries that see this key
         const int vlo = j - a.right - start, vhi = j >= klen ? 0 : j < a.sinks ? qlen : min(qlen, j + a.left - start + 1);
-        // queries that see every key of the tile
-        const int all_lo = k1 - 1 - a.right - start, all_hi = (k1 <= a.sinks ? qlen : min(qlen, k0 + a.left - start + 1)) - kTcChunk;
+        // queries that see every key of the tile (with a bias a dead key's d must be 0, so its tile is masked)
+        const int all_lo = BIAS && k1 - k0 < kTcRows ? kBandFar : k1 - 1 - a.right - start, all_hi = (k1 <= a.sinks ? qlen : min(qlen, k0 + a.left - start + 1)) - kTcChunk;
         const float sc = BIAS ? a.scale : a.scale * kLog2e;
+        const int kw = k0 + (warp & 3) * 32;  // this warp's keys
+        Diagonals dg;
+        int dg_head = -1;
+        dg.M = a.M;
+        dg.rel31 = kw + 31 - start;
         bool ok = true;
         int s = w;
         for (int t = w; t < cnt; t += 2) {
             int g, i, ca, cb;
             step_of(t, g, i);
+            if (BIAS && warp_live && g != dg_head) {
+                if (dg_head >= 0) dg.finish(lane);
+                dg.start(diag + ((static_cast<long long>(blockIdx.x) * 8 + warp) * a.G + g) * (2 * a.M + 1));
+                dg_head = g;
+            }
             chunks(i, ca, cb);
             // the scores, and (the loads' own barrier) the queries' stats
             ok = warp_wait(&full[s], (t / kSlots) & 1, abort) && warp_wait(&s_full[w], (t >> 1) & 1, abort);
@@ -665,6 +678,17 @@ __global__ void __launch_bounds__(KvCfg<NB>::threads, 1)
                     }
                     tmem_st16(at_s + c * 16, p);
                     tmem_st16(at_s + 64 + c * 16, d);
+                    if (BIAS) {
+                        const bool above = kw - (start + ic + kTcChunk - 1) >= a.M, below = kw + 31 - (start + ic) <= -a.M;
+                        if (above || below) {
+                            float2 sum[2] = {};
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2) add2(sum[(e >> 1) & 1], y[e], y[e + 1]);
+                            (above ? dg.above : dg.below) += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                        } else {
+                            dg.chunk(ic, lane, y);
+                        }
+                    }
                 }
                 tmem_st_wait();
             }
@@ -674,6 +698,7 @@ __global__ void __launch_bounds__(KvCfg<NB>::threads, 1)
             s += 2;
             if (s >= kSlots) s -= kSlots;
         }
+        if (BIAS && dg_head >= 0) dg.finish(lane);
         if (ok && cnt) ok = warp_wait(&done, 0u, abort);
         tc_fence_after();
         // the first four warps store gv, the others gk
@@ -744,17 +769,18 @@ __global__ void __launch_bounds__(256) kv_join_kernel(BandArgs a, KvShape sh, in
     *reinterpret_cast<uint2*>(to) = make_uint2(pack2<T>(s.x, s.y), pack2<T>(s.z, s.w));
 }
 
-// sums[h][rel] = the warps' diagonal sums of head h over images and rows, in a fixed order.
-__global__ void __launch_bounds__(256) diag_sum_kernel(BandArgs a, int rowwarps, const float* __restrict__ diag, float* __restrict__ sums) {
+// sums[h][rel] = the warps' diagonal sums of head h, in a fixed order: 8 warps of `per` CTAs an image.
+__global__ void __launch_bounds__(256) diag_sum_kernel(BandArgs a, int per, const float* __restrict__ diag, float* __restrict__ sums) {
     __shared__ float s_part[8][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.y, len = 2 * a.M + 1, rel = blockIdx.x * 32 + lane;
-    const long long rows = static_cast<long long>(a.N) * rowwarps;
+    const int hk = h / a.G, g = h - hk * a.G;
+    const long long ctas = static_cast<long long>(a.N) * per;
     float s = 0.f;
     if (rel < len) {
-#pragma unroll 8
-        for (long long r = warp; r < rows; r += 8) {
-            const long long n = r / rowwarps;
-            s += diag[((n * a.Hq + h) * rowwarps + r - n * rowwarps) * len + rel];
+#pragma unroll 4
+        for (long long c = 0; c < ctas; ++c) {
+            const long long n = c / per, cta = (n * a.Hk + hk) * per + c - n * per;
+            s += diag[((cta * 8 + warp) * a.G + g) * len + rel];
         }
     }
     s_part[warp][lane] = s;
@@ -802,8 +828,9 @@ size_t stats_bytes(const BandArgs& a) { return up256(static_cast<size_t>(a.N) * 
 size_t part_bytes(const BandArgs& a, const KvShape& s) {
     return s.split() ? up256(static_cast<size_t>(a.N) * a.Hk * s.items() * 2 * kTcRows * a.D * sizeof(float)) : 0;
 }
-size_t diag_rows(const BandArgs& a) { return static_cast<size_t>(a.N) * a.Hq * ((a.Lq + 31) / 32); }
-size_t diag_bytes(const BandArgs& a) { return a.nb ? up256(diag_rows(a) * (2 * a.M + 1) * sizeof(float)) : 0; }
+size_t diag_bytes(const BandArgs& a, const KvShape& s) {
+    return a.nb ? up256(static_cast<size_t>(a.N) * a.Hq * s.items() * 8 * (2 * a.M + 1) * sizeof(float)) : 0;
+}
 size_t sums_bytes(const BandArgs& a) { return a.nb ? up256(static_cast<size_t>(a.Hq) * (2 * a.M + 1) * sizeof(float)) : 0; }
 
 template <typename K>
@@ -819,16 +846,18 @@ cudaError_t launch(const BandArgs& a, const void* out, const float* lse, const v
     float2* stats = reinterpret_cast<float2*>(at);
     float* part = reinterpret_cast<float*>(at += stats_bytes(a));
     float* diag = reinterpret_cast<float*>(at += part_bytes(a, kv));
-    float* sums = reinterpret_cast<float*>(at += diag_bytes(a));
-    const int pack = BIAS ? 1 : a.G, tq = kTcRows / pack, blocks = (a.Lq + 2 * tq - 1) / (2 * tq);
+    float* sums = reinterpret_cast<float*>(at += diag_bytes(a, kv));
+    const int pack = a.G, tq = kTcRows / pack, blocks = (a.Lq + 2 * tq - 1) / (2 * tq);
     const long long dense = static_cast<long long>(a.Hq) * a.D;
-    const size_t smem_q = QCfg<NB>::smem + (BIAS ? table_floats(a.M) * sizeof(float) : 0),
+    const size_t smem_q = QCfg<NB>::smem + (BIAS ? static_cast<size_t>(a.G) * kv.floats * sizeof(float) : 0),
                  smem_kv = KvCfg<NB>::smem + (BIAS ? static_cast<size_t>(a.G) * kv.floats * sizeof(float) : 0);
     // (first, for the context: another thread may run the backward, and the maps' encoder asks for one)
     cudaError_t e = allow_smem(grad_q_kernel<T, NB, BIAS>, smem_q);
     if (e == cudaSuccess) e = allow_smem(grad_kv_kernel<T, NB, BIAS>, smem_kv);
-    if (e == cudaSuccess && BIAS) e = cudaMemsetAsync(diag, 0, diag_bytes(a), stream);
+    if (e == cudaSuccess && BIAS) e = cudaMemsetAsync(diag, 0, diag_bytes(a, kv), stream);
     if (e != cudaSuccess) return e;
+    // most keys that a row sees
+    const long long most = std::min<long long>(a.Lk, static_cast<long long>(std::min(a.left, kBandMaxLen)) + std::min(a.right, kBandMaxLen) + 1 + a.sinks);
     CUtensorMap mq, mg, mk, mv, mq1, mg1, mk1, mv1;
     if (!make_map(&mq, a.dtype, a.q, a.N, a.Lq, a.Hq, a.D, a.q_batch, a.q_row, pack, tq) ||
         !make_map(&mg, a.dtype, gout, a.N, a.Lq, a.Hq, a.D, dense * a.Lq, dense, pack, tq) ||
@@ -844,10 +873,10 @@ cudaError_t launch(const BandArgs& a, const void* out, const float* lse, const v
                                                                               static_cast<const T*>(gout), stats);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     grad_q_kernel<T, NB, BIAS><<<static_cast<unsigned>(static_cast<long long>(a.N) * (a.Hq / pack) * blocks), QCfg<NB>::threads, smem_q, stream>>>(
-        mq, mg, mk, mv, a, pack, tq, blocks, BIAS ? table_floats(a.M) : 0, stats, static_cast<T*>(gq), diag);
+        mq, mg, mk, mv, a, pack, tq, blocks, kv.floats, most <= kFewKeys, stats, static_cast<T*>(gq));
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     grad_kv_kernel<T, NB, BIAS><<<static_cast<unsigned>(static_cast<long long>(a.N) * a.Hk * kv.items()), KvCfg<NB>::threads, smem_kv, stream>>>(
-        mq1, mg1, mk1, mv1, a, kv, stats, static_cast<T*>(gk), static_cast<T*>(gv), part);
+        mq1, mg1, mk1, mv1, a, kv, stats, static_cast<T*>(gk), static_cast<T*>(gv), part, diag);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (kv.split()) {
         const int tiles = kv.other_parts > 1 ? kv.tiles : kv.sink_tiles;
@@ -856,7 +885,7 @@ cudaError_t launch(const BandArgs& a, const void* out, const float* lse, const v
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     if (!BIAS || !gbias) return cudaSuccess;
-    diag_sum_kernel<<<dim3((2 * a.M + 32) / 32, a.Hq), 256, 0, stream>>>(a, (a.Lq + 31) / 32, diag, sums);
+    diag_sum_kernel<<<dim3((2 * a.M + 32) / 32, a.Hq), 256, 0, stream>>>(a, kv.items(), diag, sums);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     bucket_sum_kernel<T><<<(a.nb * a.Hq + 7) / 8, 256, 0, stream>>>(a, sums, static_cast<T*>(gbias));
     return cudaGetLastError();
@@ -870,7 +899,8 @@ bool band_bwd_tc_fits(const BandArgs& a) {
 }
 
 size_t band_bwd_tc_workspace(const BandArgs& a) {
-    return stats_bytes(a) + part_bytes(a, kv_shape(a)) + diag_bytes(a) + sums_bytes(a);
+    const KvShape kv = kv_shape(a);
+    return stats_bytes(a) + part_bytes(a, kv) + diag_bytes(a, kv) + sums_bytes(a);
 }
 
 cudaError_t launch_band_bwd_tc(const BandArgs& a, const void* out, const float* lse, const void* gout, void* gq, void* gk, void* gv,
