@@ -18,7 +18,8 @@
 // number: where rows see at most kFewKeys, grad_q goes over the keys twice and takes
 // delta = sum p E from the first pass (one more pass of two of its three products).
 //
-// p and d go to the tensor cores as the I/O type, over the scores they came from in
+// p and d go to the tensor cores as the I/O type (EXACT: as two numbers of it, see
+// kExactKeys), over the scores they came from in
 // tensor memory; the sums stay there in fp32 until they are rounded once.
 #include "dcn4_band_tc.cuh"
 
@@ -92,7 +93,7 @@ struct QCfg {
     static constexpr size_t smem = 1024 + 4 * NB * kTcBlock + slots * 2 * NB * kTileBlock;
 };
 
-template <typename T, int NB, bool BIAS>
+template <typename T, int NB, bool BIAS, bool EXACT>
 __global__ void __launch_bounds__(QCfg<NB>::threads, 1)
     grad_q_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_g,
                   const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, BandArgs a, int pack,
@@ -226,7 +227,10 @@ __global__ void __launch_bounds__(QCfg<NB>::threads, 1)
                     tc_fence_after();
                     p_phase ^= 1u;
                     if (t >= first) {
-                        if (elect_one()) issue_sum<kTile / 16>(at_o, at_s, step_desc(k_sum, off), id_o, ca * 2, cb * 2, some);
+                        if (elect_one()) {
+                            issue_sum<kTile / 16>(at_o, at_s, step_desc(k_sum, off), id_o, ca * 2, cb * 2, some);
+                            if (EXACT) issue_sum<kTile / 16>(at_o, at_s + kLow, step_desc(k_sum, off), id_o, ca * 2, cb * 2, true);
+                        }
                         __syncwarp();
                         some = true;
                     }
@@ -310,7 +314,12 @@ __global__ void __launch_bounds__(QCfg<NB>::threads, 1)
                     uint32_t p[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) p[e >> 1] = pack2<T>(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
-                    tmem_st16(at_s + c * 16, p);
+                    tmem_st16(at_s + c * kTcChunk, p);
+                    if (EXACT) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) p[e] = pack_low<T>(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1]), p[e]);
+                        tmem_st16(at_s + c * kTcChunk + kLow, p);
+                    }
                 }
                 tmem_st_wait();
             }
@@ -442,7 +451,7 @@ struct KvCfg {
     static constexpr size_t smem = 1024 + 2 * NB * kTcBlock + slots * (stage + stat);
 };
 
-template <typename T, int NB, bool BIAS>
+template <typename T, int NB, bool BIAS, bool EXACT>
 __global__ void __launch_bounds__(KvCfg<NB>::threads, 1)
     grad_kv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_g,
                    const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, BandArgs a, KvShape sh,
@@ -590,6 +599,10 @@ __global__ void __launch_bounds__(KvCfg<NB>::threads, 1)
                         const uint32_t off = sum_slot * C::stage, at = tmem + (t & 1) * 128;
                         issue_sum<kTile / 16>(tmem + 256, at, step_desc(g_sum, off), id_o, ca * 2, cb * 2, t > 0);
                         issue_sum<kTile / 16>(tmem + 256 + 64 * NB, at + 64, step_desc(q_sum, off), id_o, ca * 2, cb * 2, t > 0);
+                        if (EXACT) {
+                            issue_sum<kTile / 16>(tmem + 256, at + kLow, step_desc(g_sum, off), id_o, ca * 2, cb * 2, true);
+                            issue_sum<kTile / 16>(tmem + 256 + 64 * NB, at + 64 + kLow, step_desc(q_sum, off), id_o, ca * 2, cb * 2, true);
+                        }
                         umma_commit(smem_u32(&empty[sum_slot]));
                     }
                     __syncwarp();
@@ -676,8 +689,17 @@ __global__ void __launch_bounds__(KvCfg<NB>::threads, 1)
                         p[e] = pack2<T>(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
                         d[e] = pack2<T>(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1]));
                     }
-                    tmem_st16(at_s + c * 16, p);
-                    tmem_st16(at_s + 64 + c * 16, d);
+                    tmem_st16(at_s + c * kTcChunk, p);
+                    tmem_st16(at_s + 64 + c * kTcChunk, d);
+                    if (EXACT) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            p[e] = pack_low<T>(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]), p[e]);
+                            d[e] = pack_low<T>(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1]), d[e]);
+                        }
+                        tmem_st16(at_s + c * kTcChunk + kLow, p);
+                        tmem_st16(at_s + 64 + c * kTcChunk + kLow, d);
+                    }
                     if (BIAS) {
                         const bool above = kw - (start + ic + kTcChunk - 1) >= a.M, below = kw + 31 - (start + ic) <= -a.M;
                         if (above || below) {
@@ -838,7 +860,7 @@ cudaError_t allow_smem(K kernel, size_t bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
 }
 
-template <typename T, int NB, bool BIAS>
+template <typename T, int NB, bool BIAS, bool EXACT>
 cudaError_t launch(const BandArgs& a, const void* out, const float* lse, const void* gout, void* gq, void* gk, void* gv, void* gbias,
                    void* ws, cudaStream_t stream) {
     char* at = static_cast<char*>(ws);
@@ -852,12 +874,10 @@ cudaError_t launch(const BandArgs& a, const void* out, const float* lse, const v
     const size_t smem_q = QCfg<NB>::smem + (BIAS ? static_cast<size_t>(a.G) * kv.floats * sizeof(float) : 0),
                  smem_kv = KvCfg<NB>::smem + (BIAS ? static_cast<size_t>(a.G) * kv.floats * sizeof(float) : 0);
     // (first, for the context: another thread may run the backward, and the maps' encoder asks for one)
-    cudaError_t e = allow_smem(grad_q_kernel<T, NB, BIAS>, smem_q);
-    if (e == cudaSuccess) e = allow_smem(grad_kv_kernel<T, NB, BIAS>, smem_kv);
+    cudaError_t e = allow_smem(grad_q_kernel<T, NB, BIAS, EXACT>, smem_q);
+    if (e == cudaSuccess) e = allow_smem(grad_kv_kernel<T, NB, BIAS, EXACT>, smem_kv);
     if (e == cudaSuccess && BIAS) e = cudaMemsetAsync(diag, 0, diag_bytes(a, kv), stream);
     if (e != cudaSuccess) return e;
-    // most keys that a row sees
-    const long long most = std::min<long long>(a.Lk, static_cast<long long>(std::min(a.left, kBandMaxLen)) + std::min(a.right, kBandMaxLen) + 1 + a.sinks);
     CUtensorMap mq, mg, mk, mv, mq1, mg1, mk1, mv1;
     if (!make_map(&mq, a.dtype, a.q, a.N, a.Lq, a.Hq, a.D, a.q_batch, a.q_row, pack, tq) ||
         !make_map(&mg, a.dtype, gout, a.N, a.Lq, a.Hq, a.D, dense * a.Lq, dense, pack, tq) ||
@@ -872,10 +892,10 @@ cudaError_t launch(const BandArgs& a, const void* out, const float* lse, const v
     stats_kernel<T><<<static_cast<unsigned>((rows + 15) / 16), 256, 0, stream>>>(a, static_cast<const T*>(out), lse,
                                                                               static_cast<const T*>(gout), stats);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    grad_q_kernel<T, NB, BIAS><<<static_cast<unsigned>(static_cast<long long>(a.N) * (a.Hq / pack) * blocks), QCfg<NB>::threads, smem_q, stream>>>(
-        mq, mg, mk, mv, a, pack, tq, blocks, kv.floats, most <= kFewKeys, stats, static_cast<T*>(gq));
+    grad_q_kernel<T, NB, BIAS, EXACT><<<static_cast<unsigned>(static_cast<long long>(a.N) * (a.Hq / pack) * blocks), QCfg<NB>::threads, smem_q, stream>>>(
+        mq, mg, mk, mv, a, pack, tq, blocks, kv.floats, band_most_keys(a) <= kFewKeys, stats, static_cast<T*>(gq));
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    grad_kv_kernel<T, NB, BIAS><<<static_cast<unsigned>(static_cast<long long>(a.N) * a.Hk * kv.items()), KvCfg<NB>::threads, smem_kv, stream>>>(
+    grad_kv_kernel<T, NB, BIAS, EXACT><<<static_cast<unsigned>(static_cast<long long>(a.N) * a.Hk * kv.items()), KvCfg<NB>::threads, smem_kv, stream>>>(
         mq1, mg1, mk1, mv1, a, kv, stats, static_cast<T*>(gk), static_cast<T*>(gv), part, diag);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (kv.split()) {
@@ -905,11 +925,14 @@ size_t band_bwd_tc_workspace(const BandArgs& a) {
 
 cudaError_t launch_band_bwd_tc(const BandArgs& a, const void* out, const float* lse, const void* gout, void* gq, void* gk, void* gv,
                                void* gbias, void* ws, cudaStream_t stream) {
-#define DCN4_BAND_BWD(T, NB)                                                                              \
-    (a.nb ? launch<T, NB, true>(a, out, lse, gout, gq, gk, gv, gbias, ws, stream)                         \
-          : launch<T, NB, false>(a, out, lse, gout, gq, gk, gv, gbias, ws, stream))
-    if (a.dtype == 1) return a.D > 64 ? DCN4_BAND_BWD(__half, 2) : DCN4_BAND_BWD(__half, 1);
-    return a.D > 64 ? DCN4_BAND_BWD(__nv_bfloat16, 2) : DCN4_BAND_BWD(__nv_bfloat16, 1);
+#define DCN4_BAND_BWD(T, NB, BIAS)                                                                          \
+    (band_most_keys(a) <= kExactKeys ? launch<T, NB, BIAS, true>(a, out, lse, gout, gq, gk, gv, gbias, ws, stream) \
+                                     : launch<T, NB, BIAS, false>(a, out, lse, gout, gq, gk, gv, gbias, ws, stream))
+#define DCN4_BAND_BWD_T(T)                                                                    \
+    (a.D > 64 ? (a.nb ? DCN4_BAND_BWD(T, 2, true) : DCN4_BAND_BWD(T, 2, false))               \
+              : (a.nb ? DCN4_BAND_BWD(T, 1, true) : DCN4_BAND_BWD(T, 1, false)))
+    return a.dtype == 1 ? DCN4_BAND_BWD_T(__half) : DCN4_BAND_BWD_T(__nv_bfloat16);
+#undef DCN4_BAND_BWD_T
 #undef DCN4_BAND_BWD
 }
 

@@ -90,7 +90,8 @@ __device__ __forceinline__ bool chunks_of(const RowBand& b, int j0, int& ca, int
     return b.any && lo < hi;
 }
 
-template <typename T, int NB, bool BIAS>
+// EXACT: p as two numbers (kExactKeys)
+template <typename T, int NB, bool BIAS, bool EXACT>
 __global__ void __launch_bounds__(Cfg<NB>::threads, Cfg<NB>::ctas)
     fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                const __grid_constant__ CUtensorMap map_v, BandArgs a, FwdShape sh, T* __restrict__ out,
@@ -275,6 +276,9 @@ __global__ void __launch_bounds__(Cfg<NB>::threads, Cfg<NB>::ctas)
                             issue_sum<kKeys / 16>(tmem + 2 * C::scores + w * 64 * NB, tmem + w * C::scores + buf * kKeys,
                                                   step_desc(v_desc, s * 2 * NB * kKeyBlock), id_o, (now & 255) * 2, (now >> 8) * 2,
                                                   (counts >> (4 + w)) & 1);
+                            if (EXACT)
+                                issue_sum<kKeys / 16>(tmem + 2 * C::scores + w * 64 * NB, tmem + w * C::scores + buf * kKeys + kLow,
+                                                      step_desc(v_desc, s * 2 * NB * kKeyBlock), id_o, (now & 255) * 2, (now >> 8) * 2, true);
                             umma_commit(smem_u32(&o_done[w][buf]));
                         }
                         __syncwarp();
@@ -406,7 +410,12 @@ __global__ void __launch_bounds__(Cfg<NB>::threads, Cfg<NB>::ctas)
                         add2(sum[(e >> 1) & 1], lo, hi);
                         p[e >> 1] = pack2<T>(__uint_as_float(lo), __uint_as_float(hi));
                     }
-                    tmem_st16(s_at + c * 16, p);  // the scores are in registers: P takes their place
+                    tmem_st16(s_at + c * kTcChunk, p);  // the scores are in registers: P takes their place
+                    if (EXACT) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) p[e] = pack_low<T>(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1]), p[e]);
+                        tmem_st16(s_at + c * kTcChunk + kLow, p);
+                    }
                 }
                 rl += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 tmem_st_wait();
@@ -507,12 +516,12 @@ FwdShape shape_of(const BandArgs& a) {
     return s;
 }
 
-template <typename T, int NB, bool BIAS>
+template <typename T, int NB, bool BIAS, bool EXACT>
 cudaError_t launch(const BandArgs& a, const FwdShape& s, void* out, float* lse, void* ws, cudaStream_t stream) {
     using C = Cfg<NB>;
     const size_t smem = 1024 + static_cast<size_t>(s.alt ? 1 : 2) * NB * kTcBlock + static_cast<size_t>(C::slots) * 2 * NB * kKeyBlock +
                         s.pack * s.table * sizeof(float);
-    cudaError_t e = cudaFuncSetAttribute(fwd_kernel<T, NB, BIAS>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    cudaError_t e = cudaFuncSetAttribute(fwd_kernel<T, NB, BIAS, EXACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     CUtensorMap mq, mk, mv;
     if (!make_map(&mq, a.dtype, a.q, a.N, a.Lq, a.Hq, a.D, a.q_batch, a.q_row, s.pack, s.tq) ||
@@ -521,18 +530,23 @@ cudaError_t launch(const BandArgs& a, const FwdShape& s, void* out, float* lse, 
         return cudaErrorInvalidValue;
     const BandPart part = band_part(a, s.splits, ws);
     const long long ctas = static_cast<long long>(a.N) * (a.Hq / s.pack) * s.blocks * s.splits;
-    fwd_kernel<T, NB, BIAS><<<static_cast<unsigned>(ctas), C::threads, smem, stream>>>(mq, mk, mv, a, s, static_cast<T*>(out), lse, part);
+    fwd_kernel<T, NB, BIAS, EXACT><<<static_cast<unsigned>(ctas), C::threads, smem, stream>>>(mq, mk, mv, a, s, static_cast<T*>(out), lse, part);
     e = cudaGetLastError();
     if (e != cudaSuccess || s.splits == 1) return e;
     return launch_band_join(a, s.splits, part, out, lse, stream);
 }
 
+template <typename T, int NB>
+cudaError_t launch_heads(const BandArgs& a, const FwdShape& s, void* out, float* lse, void* ws, cudaStream_t stream) {
+    if (band_most_keys(a) <= kExactKeys)
+        return a.nb ? launch<T, NB, true, true>(a, s, out, lse, ws, stream) : launch<T, NB, false, true>(a, s, out, lse, ws, stream);
+    return a.nb ? launch<T, NB, true, false>(a, s, out, lse, ws, stream) : launch<T, NB, false, false>(a, s, out, lse, ws, stream);
+}
+
 template <typename T>
 cudaError_t launch_typed(const BandArgs& a, void* out, float* lse, void* ws, cudaStream_t stream) {
     const FwdShape s = shape_of(a);
-    if (a.D > 64)
-        return a.nb ? launch<T, 2, true>(a, s, out, lse, ws, stream) : launch<T, 2, false>(a, s, out, lse, ws, stream);
-    return a.nb ? launch<T, 1, true>(a, s, out, lse, ws, stream) : launch<T, 1, false>(a, s, out, lse, ws, stream);
+    return a.D > 64 ? launch_heads<T, 2>(a, s, out, lse, ws, stream) : launch_heads<T, 1>(a, s, out, lse, ws, stream);
 }
 
 }  // namespace

@@ -38,6 +38,11 @@ inline int band_splits(const BandArgs& a, long long ctas, int queries, int bn, i
     return static_cast<int>(std::max<long long>(1, std::min<long long>(std::min<long long>(want, tiles / 4), 256)));
 }
 
+// The most keys that a row can see.
+inline long long band_most_keys(const BandArgs& a) {
+    return std::min<long long>(a.Lk, static_cast<long long>(std::min(a.left, kBandMaxLen)) + std::min(a.right, kBandMaxLen) + 1 + a.sinks);
+}
+
 // out and lse of every row from its parts.
 cudaError_t launch_band_join(const BandArgs& a, int splits, BandPart part, void* out, float* lse, cudaStream_t stream);
 // gbias[b][h] from parts bpart[(n Hq / heads + group) blocks + block][nb][heads].

@@ -179,15 +179,35 @@ __device__ __forceinline__ void issue_rows(uint32_t d, uint64_t a, int ablock, u
         if (q < steps)
             umma_f16(d, step_desc(a, (q >> 2) * ablock + (q & 3) * 32), step_desc(b, (q >> 2) * bblock + (q & 3) * 32), idesc, q > 0);
 }
-// d (+)= a (tensor memory, steps [s0, s1) of 16 of its rows) times the tile b of those rows.
+// d (+)= a (tensor memory, steps [s0, s1) of 16 of its columns) times the tile b of those rows.  a's chunk
+// of 32 columns lies in the first 16 of the columns of the chunk of scores that it came from.
 template <int STEPS>
 __device__ __forceinline__ void issue_sum(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, int s0, int s1, bool accum) {
 #pragma unroll
     for (int s = 0; s < STEPS; ++s)
         if (s >= s0 && s < s1) {
-            umma_f16_ts(d, a + s * 8, step_desc(b, s * 2048), idesc, accum);
+            umma_f16_ts(d, a + (s >> 1) * kTcChunk + (s & 1) * 8, step_desc(b, s * 2048), idesc, accum);
             accum = true;
         }
+}
+
+// Where a row sees no more keys than this, what meets them (p, d) goes to the
+// tensor cores as two numbers of the I/O type, the second what the first leaves: few
+// roundings do not average out, and a small call's time is not in its products.
+constexpr int kExactKeys = 64;
+constexpr int kLow = 16;  // columns from the first numbers of a chunk to the second ones
+
+// Two floats as a pair of T, and what the pair leaves of them.
+template <typename T>
+__device__ __forceinline__ uint32_t pack_low(float lo, float hi, uint32_t pair) {
+    if constexpr (std::is_same<T, __half>::value) {
+        __half2 h;
+        memcpy(&h, &pair, 4);
+        const float2 f = __half22float2(h);
+        return pack2<T>(lo - f.x, hi - f.y);
+    } else {
+        return pack2<T>(lo - __uint_as_float(pair << 16), hi - __uint_as_float(pair & 0xffff0000u));
+    }
 }
 
 // cuTensorMapEncodeTiled from the driver (resolved once through the runtime).
