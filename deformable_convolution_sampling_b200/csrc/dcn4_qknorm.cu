@@ -49,31 +49,51 @@ __device__ __forceinline__ float group_sum(float v, int lph) {
     return v;
 }
 
-// A lane's two pieces as fp32.
+// Two fp32 values handled by one instruction.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+    F2 v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+    return v;
+}
+__device__ __forceinline__ float2 unf2(F2 v) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// A lane's two pieces as pairs of fp32.
 template <typename T>
 struct Lane {
-    static constexpr int E = Elem<T>::per16;
-    float f[2][E];
+    static constexpr int P = Elem<T>::per16 / 2;
+    F2 f[2][P];
     __device__ __forceinline__ void from(const uint4 (&r)[2]) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            float2 p[E / 2];
+            float2 p[P];
             unpack(r[c], p, T());
 #pragma unroll
-            for (int e = 0; e < E / 2; ++e) {
-                f[c][2 * e] = p[e].x;
-                f[c][2 * e + 1] = p[e].y;
-            }
+            for (int e = 0; e < P; ++e) f[c][e] = f2(p[e].x, p[e].y);
         }
     }
     __device__ __forceinline__ void store(T* row, const int (&at)[2], int nchunk) const {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             if (at[c] >= nchunk) continue;
-            float2 p[E / 2];
+            float2 p[P];
 #pragma unroll
-            for (int e = 0; e < E / 2; ++e) p[e] = make_float2(f[c][2 * e], f[c][2 * e + 1]);
-            st_global(row + at[c] * E, pack(p, T()));
+            for (int e = 0; e < P; ++e) p[e] = unf2(f[c][e]);
+            st_global(row + at[c] * 2 * P, pack(p, T()));
         }
     }
 };
@@ -91,7 +111,7 @@ struct Warp {
     int lane, grp, hpw, nchunk, H;
     int at[2];       // the lane's pieces
     int pair;        // the lane's first pair, E from there on; -1: its pieces are not turned
-    float2* cs;      // cos and sin of the tokens' pairs
+    float *cs, *sn;  // cos and sin of the tokens' pairs
     float* buf;      // D floats of this lane group (exchange)
 
     __device__ __forceinline__ Warp(const QkNormArgs& a, const Shape& sh, float* smem) {
@@ -105,7 +125,8 @@ struct Warp {
         at[0] = first ? p : 2 * p;
         at[1] = first ? p + sh.apart : 2 * p + 1;
         pair = MODE == kNeighbours ? (at[0] * E < a.R ? p * E : -1) : first ? p * E : -1;
-        cs = reinterpret_cast<float2*>(smem) + warp * kMaxPairs;
+        cs = smem + warp * 2 * kMaxPairs;
+        sn = cs + kMaxPairs;
         buf = smem + kWarps * kMaxPairs * 2 + (warp * hpw + grp) * a.D;
     }
     // the angles of `count` tokens, each formed by one lane
@@ -118,9 +139,7 @@ struct Warp {
             const float pos = __ldg(a.pos + (tok + t) * a.axes + (i >= per ? 1 : 0));
             double f = static_cast<double>(pos) * static_cast<double>(__ldg(a.inv_freq + i));
             f -= kTwoPi * rint(f * kInvTwoPi);
-            float s, c;
-            sincosf(static_cast<float>(f), &s, &c);
-            cs[e] = make_float2(c, s);
+            sincosf(static_cast<float>(f), sn + e, cs + e);
         }
         __syncwarp();
     }
@@ -128,80 +147,94 @@ struct Warp {
     __device__ __forceinline__ void turn(Lane<T>& x, const QkNormArgs& a, int t, float dir) {
         if (MODE == kNone) return;
         const int h = a.R >> 1;
-        const float2* q = cs + t * h;
-        if (MODE != kExchange) {
+        const float *c = cs + t * h, *n = sn + t * h;
+        if (MODE == kHalves) {
             if (pair < 0) return;
-            q += pair;
-            // halves: pair e of the lane is (f[0][e], f[1][e]); neighbours: (f[c][2 e], f[c][2 e + 1]) of piece c,
-            // of which some may lie beyond R
-            const int here = MODE == kNeighbours ? h - pair : E;
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                if (MODE == kNeighbours && e >= here) break;
-                float &u = MODE == kHalves ? x.f[0][e] : x.f[e / (E / 2)][2 * (e % (E / 2))],
-                      &v = MODE == kHalves ? x.f[1][e] : x.f[e / (E / 2)][2 * (e % (E / 2)) + 1];
-                const float2 r = q[e];
-                const float s = r.y * dir, w = u;
-                u = w * r.x - v * s;
-                v = v * r.x + w * s;
-            }
-            return;
-        }
-        __syncwarp();  // the previous head's reads of buf are done
+            for (int e = 0; e < E / 2; e += 2) {  // four pairs: h is a multiple of E here
+                const float4 c4 = *reinterpret_cast<const float4*>(c + pair + 2 * e), n4 = *reinterpret_cast<const float4*>(n + pair + 2 * e);
+                const F2 cc[2] = {f2(c4.x, c4.y), f2(c4.z, c4.w)};
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-            if (at[c] < nchunk)
-#pragma unroll
-                for (int e = 0; e < E; ++e) buf[at[c] * E + e] = x.f[c][e];
-        __syncwarp();
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const int d = at[c] * E + e;
-                if (d < a.R) {
-                    const bool lo = d < h;
-                    const float2 r = q[lo ? d : d - h];
-                    const float s = r.y * dir, o = buf[lo ? d + h : d - h];
-                    x.f[c][e] = lo ? x.f[c][e] * r.x - o * s : x.f[c][e] * r.x + o * s;
+                for (int k = 0; k < 2; ++k) {
+                    const float sx = (k ? n4.z : n4.x) * dir, sy = (k ? n4.w : n4.y) * dir;
+                    const F2 u = x.f[0][e + k], v = x.f[1][e + k];
+                    x.f[0][e + k] = fma2(v, f2(-sx, -sy), mul2(u, cc[k]));
+                    x.f[1][e + k] = fma2(u, f2(sx, sy), mul2(v, cc[k]));
                 }
             }
-    }
-};
-
-// A unit's heads of one side (queries or keys): `count` tokens from tok on, heads [h0, h0 + heads) of H.
-template <typename T>
-struct Side {
-    const T* x;
-    long long batch, row;
-    int H, h0, heads;
-    __device__ __forceinline__ Side(const QkNormArgs& a, int side, int lo, int hi) {
-        x = static_cast<const T*>(side ? a.k : a.q);
-        batch = side ? a.k_batch : a.q_batch;
-        row = side ? a.k_row : a.q_row;
-        H = side ? a.Hk : a.Hq;
-        h0 = max(lo - (side ? a.Hq : 0), 0);
-        heads = max(min(hi - (side ? a.Hq : 0), H) - h0, 0);
-    }
-    // item `it` of the unit: its token, and where its head lies in the input and in a dense tensor
-    __device__ __forceinline__ void place(const QkNormArgs& a, long long tok, int it, int& t, long long& in, long long& dense, int D) const {
-        t = it / heads;
-        const int h = h0 + it - t * heads;
-        const long long at = tok + t, n = at / a.L;
-        in = n * batch + (at - n * a.L) * row + static_cast<long long>(h) * D;
-        dense = (at * H + h) * D;
-    }
-};
-
-template <typename T>
-__device__ __forceinline__ void load_weight(Lane<T>& w, const void* p, const int (&at)[2], int nchunk) {
-    if (p) {
-        uint4 r[2];
-        load_pieces<T>(r, static_cast<const T*>(p), at, nchunk);
-        w.from(r);
-    } else {
+        } else if (MODE == kNeighbours) {
+            if (pair < 0) return;
 #pragma unroll
-        for (int e = 0; e < 2 * Elem<T>::per16; ++e) w.f[e / Elem<T>::per16][e % Elem<T>::per16] = 1.f;
+            for (int e = 0; e < E; ++e) {  // of the lane's pairs some may lie beyond R
+                if (pair + e >= h) break;
+                F2& v = x.f[e / (E / 2)][e % (E / 2)];
+                const float2 p = unf2(v);
+                const float ce = c[pair + e], se = n[pair + e] * dir;
+                v = f2(p.x * ce - p.y * se, p.y * ce + p.x * se);
+            }
+        } else {
+            __syncwarp();  // the previous head's reads of buf are done
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                if (at[k] < nchunk)
+#pragma unroll
+                    for (int e = 0; e < E / 2; ++e) *reinterpret_cast<float2*>(buf + at[k] * E + 2 * e) = unf2(x.f[k][e]);
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int e = 0; e < E / 2; ++e) {
+                    const int d = at[k] * E + 2 * e;
+                    float2 v = unf2(x.f[k][e]);
+                    auto one = [&](float w, int d) {
+                        if (d >= a.R) return w;
+                        const bool lo = d < h;
+                        const int i = lo ? d : d - h;
+                        const float s = n[i] * dir, o = buf[lo ? d + h : d - h];
+                        return lo ? w * c[i] - o * s : w * c[i] + o * s;
+                    };
+                    v.x = one(v.x, d);
+                    v.y = one(v.y, d + 1);
+                    x.f[k][e] = f2(v.x, v.y);
+                }
+        }
+    }
+};
+
+// Where a lane group is among a unit's heads of one side (queries or keys): tokens
+// from tok = (n, l) on, `heads` heads of each from h0 on.  It goes on by the warp's
+// groups with additions only (a division an item cost more than its arithmetic).
+struct Walk {
+    int heads, t, h, dt, dh;
+    __device__ __forceinline__ Walk(int heads, int grp, int hpw) : heads(heads) {
+        t = grp / heads;
+        h = grp - t * heads;
+        dt = hpw / heads;
+        dh = hpw - dt * heads;
+    }
+    __device__ __forceinline__ void next() {
+        t += dt;
+        h += dh;
+        if (h >= heads) h -= heads, ++t;
+    }
+};
+// Elements from token (n, l) on to the token t behind it.
+__device__ __forceinline__ long long ahead(int L, int l, int t, long long batch, long long row) {
+    if (l + t < L) return t * row;
+    const int at = l + t;
+    return at / L * batch + (at % L - l) * row;
+}
+
+// A lane's pieces of a weight, as they are stored; NULL: ones.
+template <typename T>
+__device__ __forceinline__ void load_weight(uint4 (&w)[2], const void* p, const int (&at)[2], int nchunk) {
+    if (p) {
+        load_pieces<T>(w, static_cast<const T*>(p), at, nchunk);
+    } else {
+        float2 one[Elem<T>::per16 / 2];
+#pragma unroll
+        for (int e = 0; e < Elem<T>::per16 / 2; ++e) one[e] = make_float2(1.f, 1.f);
+        w[0] = w[1] = pack(one, T());
     }
 }
 
@@ -211,44 +244,52 @@ __global__ void __launch_bounds__(kThreads, 6) qknorm_forward_kernel(QkNormArgs 
     extern __shared__ __align__(16) float qk_smem[];
     Warp<T, MODE> wp(a, sh, qk_smem);
     const long long total = static_cast<long long>(a.N) * a.L;
+    const float inv_d = 1.f / a.D;
     for (long long u = blockIdx.x * static_cast<long long>(kWarps) + (threadIdx.x >> 5); u < sh.units; u += static_cast<long long>(gridDim.x) * kWarps) {
         const long long tok = u / sh.chunks * sh.tokens;
         const int count = static_cast<int>(total - tok < sh.tokens ? total - tok : sh.tokens);
         const int lo = static_cast<int>(u % sh.chunks) * sh.heads;
+        const long long n = tok / a.L;
+        const int l = static_cast<int>(tok - n * a.L);
 #pragma unroll 1
         for (int side = 0; side < 2; ++side) {
-            const Side<T> sd(a, side, lo, lo + sh.heads);
-            const int items = count * sd.heads;
-            if (items) {
+            const int H = side ? a.Hk : a.Hq, h0 = max(lo - (side ? a.Hq : 0), 0), heads = min(lo + sh.heads - (side ? a.Hq : 0), H) - h0;
+            if (heads > 0) {
+                const long long batch = side ? a.k_batch : a.q_batch, row = side ? a.k_row : a.q_row;
+                const T* src = static_cast<const T*>(side ? a.k : a.q) + n * batch + l * row + static_cast<long long>(h0) * a.D;
+                const int items = count * heads;
+                Walk at_head(heads, wp.grp, wp.hpw);
                 uint4 raw[2];
-                long long dense;
-                int t;
                 auto fetch = [&](int it) {
-                    long long in;
-                    sd.place(a, tok, min(it, items - 1), t, in, dense, a.D);
-                    load_pieces<T>(raw, sd.x + in, wp.at, it < items ? wp.nchunk : 0);
+                    const bool on = it < items;
+                    load_pieces<T>(raw, src + (on ? ahead(a.L, l, at_head.t, batch, row) + at_head.h * a.D : 0), wp.at, on ? wp.nchunk : 0);
                 };
                 fetch(wp.grp);
                 Lane<T> w;
-                load_weight<T>(w, side ? a.wk : a.wq, wp.at, wp.nchunk);
+                uint4 raw_w[2];
+                load_weight<T>(raw_w, side ? a.wk : a.wq, wp.at, wp.nchunk);
+                w.from(raw_w);
                 if (side == 0 || lo >= a.Hq) wp.angles(a, tok, count);
-                T* out = side ? ko : qo;
+                T* out = (side ? ko : qo) + (tok * H + h0) * a.D;
                 for (int at = 0; at < items; at += wp.hpw) {  // whole warps: the lanes shuffle
                     Lane<T> x;
                     x.from(raw);
-                    const long long to = dense;
-                    const int tx = t;
+                    // (a unit's tokens are few; a group past the last item turns zeros)
+                    const int tx = min(at_head.t, count - 1), to = (at_head.t * H + at_head.h) * a.D;
+                    at_head.next();
                     if (at + wp.hpw < items) fetch(at + wp.hpw + wp.grp);
-                    float ss = 0.f;
+                    F2 ss = 0;
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
 #pragma unroll
-                        for (int e = 0; e < E; ++e) ss = fmaf(x.f[c][e], x.f[c][e], ss);
-                    const float s = rsqrtf(group_sum(ss, sh.lph) / a.D + a.eps);
+                        for (int e = 0; e < E / 2; ++e) ss = fma2(x.f[c][e], x.f[c][e], ss);
+                    const float2 sq = unf2(ss);
+                    const float s = rsqrtf(fmaf(group_sum(sq.x + sq.y, sh.lph), inv_d, a.eps));
+                    const F2 s2 = f2(s, s);
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
 #pragma unroll
-                        for (int e = 0; e < E; ++e) x.f[c][e] = x.f[c][e] * s * w.f[c][e];
+                        for (int e = 0; e < E / 2; ++e) x.f[c][e] = mul2(mul2(x.f[c][e], s2), w.f[c][e]);
                     wp.turn(x, a, tx, 1.f);
                     if (at + wp.grp < items) x.store(out + to, wp.at, wp.nchunk);
                 }
@@ -266,57 +307,64 @@ __global__ void __launch_bounds__(kThreads, 4)
     extern __shared__ __align__(16) float qk_smem[];
     Warp<T, MODE> wp(a, sh, qk_smem);
     const long long total = static_cast<long long>(a.N) * a.L;
-    float acc[2][2][E] = {};  // queries' and keys' sums of the lane's entries
+    const float inv_d = 1.f / a.D;
+    F2 acc[2][2][E / 2] = {};  // queries' and keys' sums of the lane's entries
     for (long long u = blockIdx.x * static_cast<long long>(kWarps) + (threadIdx.x >> 5); u < sh.units; u += static_cast<long long>(gridDim.x) * kWarps) {
         const long long tok = u / sh.chunks * sh.tokens;
         const int count = static_cast<int>(total - tok < sh.tokens ? total - tok : sh.tokens);
         const int lo = static_cast<int>(u % sh.chunks) * sh.heads;
+        const long long n = tok / a.L;
+        const int l = static_cast<int>(tok - n * a.L);
 #pragma unroll
         for (int side = 0; side < 2; ++side) {
-            const Side<T> sd(a, side, lo, lo + sh.heads);
-            const int items = count * sd.heads;
-            if (items) {
+            const int H = side ? a.Hk : a.Hq, h0 = max(lo - (side ? a.Hq : 0), 0), heads = min(lo + sh.heads - (side ? a.Hq : 0), H) - h0;
+            if (heads > 0) {
+                const T* up = (side ? gko : gqo) + (tok * H + h0) * a.D;
+                const long long batch = side ? a.k_batch : a.q_batch, row = side ? a.k_row : a.q_row;
+                const T* src = static_cast<const T*>(side ? a.k : a.q) + n * batch + l * row + static_cast<long long>(h0) * a.D;
+                const int items = count * heads;
+                Walk at_head(heads, wp.grp, wp.hpw);
                 uint4 raw_x[2], raw_g[2];
-                long long dense;
-                int t;
                 auto fetch = [&](int it) {
-                    long long in;
-                    sd.place(a, tok, min(it, items - 1), t, in, dense, a.D);
-                    const int pieces = it < items ? wp.nchunk : 0;
-                    load_pieces<T>(raw_x, sd.x + in, wp.at, pieces);
-                    load_pieces<T>(raw_g, (side ? gko : gqo) + dense, wp.at, pieces);
+                    const bool on = it < items;
+                    load_pieces<T>(raw_x, src + (on ? ahead(a.L, l, at_head.t, batch, row) + at_head.h * a.D : 0), wp.at, on ? wp.nchunk : 0);
+                    load_pieces<T>(raw_g, up + (on ? (at_head.t * H + at_head.h) * a.D : 0), wp.at, on ? wp.nchunk : 0);
                 };
                 fetch(wp.grp);
-                Lane<T> w;
-                load_weight<T>(w, side ? a.wk : a.wq, wp.at, wp.nchunk);
+                uint4 raw_w[2];
+                load_weight<T>(raw_w, side ? a.wk : a.wq, wp.at, wp.nchunk);
                 if (side == 0 || lo >= a.Hq) wp.angles(a, tok, count);
                 for (int at = 0; at < items; at += wp.hpw) {
                     Lane<T> x, g;
                     x.from(raw_x);
                     g.from(raw_g);
-                    const long long to = dense;
-                    const int tx = t;
+                    // (a unit's tokens are few; a group past the last item turns zeros)
+                    const int tx = min(at_head.t, count - 1), to = (at_head.t * H + at_head.h) * a.D;
+                    at_head.next();
                     if (at + wp.hpw < items) fetch(at + wp.hpw + wp.grp);
                     wp.turn(g, a, tx, -1.f);
-                    float ss = 0.f, gx = 0.f;
+                    Lane<T> w;
+                    w.from(raw_w);
+                    F2 ss = 0, gx = 0;
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
 #pragma unroll
-                        for (int e = 0; e < E; ++e) {
-                            ss = fmaf(x.f[c][e], x.f[c][e], ss);
-                            gx = fmaf(g.f[c][e] * w.f[c][e], x.f[c][e], gx);
+                        for (int e = 0; e < E / 2; ++e) {
+                            ss = fma2(x.f[c][e], x.f[c][e], ss);
+                            gx = fma2(mul2(g.f[c][e], w.f[c][e]), x.f[c][e], gx);
                         }
-                    ss = group_sum(ss, sh.lph);
-                    gx = group_sum(gx, sh.lph);
-                    const float s = rsqrtf(ss / a.D + a.eps), back = s * s * (gx / a.D);
+                    const float2 sq = unf2(ss), sg = unf2(gx);
+                    const float s = rsqrtf(fmaf(group_sum(sq.x + sq.y, sh.lph), inv_d, a.eps));
+                    const float back = s * s * (group_sum(sg.x + sg.y, sh.lph) * inv_d);
+                    const F2 s2 = f2(s, s), back2 = f2(-back, -back);
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
 #pragma unroll
-                        for (int e = 0; e < E; ++e) {  // (a head past the last has x = g = 0)
-                            acc[side][c][e] = fmaf(g.f[c][e], x.f[c][e] * s, acc[side][c][e]);
-                            x.f[c][e] = s * (g.f[c][e] * w.f[c][e] - x.f[c][e] * back);
+                        for (int e = 0; e < E / 2; ++e) {  // (a head past the last has x = g = 0)
+                            acc[side][c][e] = fma2(g.f[c][e], mul2(x.f[c][e], s2), acc[side][c][e]);
+                            x.f[c][e] = mul2(s2, fma2(x.f[c][e], back2, mul2(g.f[c][e], w.f[c][e])));
                         }
-                    if (at + wp.grp < items) x.store((side ? gk : gq) + to, wp.at, wp.nchunk);
+                    if (at + wp.grp < items) x.store((side ? gk : gq) + (tok * H + h0) * a.D + to, wp.at, wp.nchunk);
                 }
             }
         }
@@ -331,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 4)
         for (int c = 0; c < 2; ++c)
             if (wp.at[c] < wp.nchunk)
 #pragma unroll
-                for (int e = 0; e < E; ++e) wp.buf[wp.at[c] * E + e] = acc[side][c][e];
+                for (int e = 0; e < E / 2; ++e) *reinterpret_cast<float2*>(wp.buf + wp.at[c] * E + 2 * e) = unf2(acc[side][c][e]);
         __syncthreads();
         for (int d = threadIdx.x; d < a.D; d += kThreads) {
             float s = 0.f;
