@@ -396,14 +396,23 @@ def check(status: int) -> None:
 # torch conveniences (device memory and the current stream come from torch)
 # ---------------------------------------------------------------------------
 
+_TORCH_DTYPES = None
+
+
 def _torch_dtype(code: int):
-    import torch
-    return {DCN4_F32: torch.float32, DCN4_F16: torch.float16, DCN4_BF16: torch.bfloat16}[code]
+    global _TORCH_DTYPES
+    if _TORCH_DTYPES is None:
+        import torch
+        _TORCH_DTYPES = {DCN4_F32: torch.float32, DCN4_F16: torch.float16, DCN4_BF16: torch.bfloat16}
+    return _TORCH_DTYPES[code]
 
 
 def _stream_handle(device):
     import torch
-    return torch.cuda.current_stream(device).cuda_stream
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without a Stream object: 2 us less a call
+    if raw is None or device.index is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return raw(device.index)
 
 
 def forward(p: dcn4_params, value, offset_mask, out=None):
@@ -567,21 +576,21 @@ def rel_buckets(nb: int, M: int, both: bool = True, device="cuda"):
     return torch.tensor(list(table), dtype=torch.int32, device=device)
 
 
-class _on_device:
-    """Makes a tensor's device the current one for a launch, where it is not."""
+def _launch(device, call, *args):
+    """check(call(*args, stream)) with `device` the current one and its current stream."""
+    import torch
+    here = torch.cuda.current_device()
+    if device.index == here:
+        check(call(*args, _stream_handle(device)))
+        return
+    with torch.cuda.device(device):
+        check(call(*args, _stream_handle(device)))
 
-    def __init__(self, t):
-        import torch
-        self.torch, self.index = torch, t.device.index
 
-    def __enter__(self):
-        self.was = self.torch.cuda.current_device()
-        if self.was != self.index:
-            self.torch.cuda.set_device(self.index)
-
-    def __exit__(self, *exc):
-        if self.was != self.index:
-            self.torch.cuda.set_device(self.was)
+def _dense_like(t, shape):
+    """An uninitialised contiguous tensor of `shape`, of t's type and device."""
+    import torch
+    return torch.empty_like(t) if t.shape == shape and t.is_contiguous() else t.new_empty(shape)
 
 
 def _ptr(t):
@@ -653,18 +662,19 @@ def band_params_for(q, k, v, *, left=-1, right=-1, sinks=0, scale=None, bias=Non
     return p
 
 
-def _same_call(p, *tensors):
-    """ValueError unless each (name, tensor, shape, batch stride, row stride) is what p was made for."""
-    for name, t, shape, batch, row in tensors:
-        sb, sl = t.stride()[:2]
-        if t.shape != shape or t.dtype != _torch_dtype(p.dtype) or (batch and shape[0] > 1 and sb != batch) or (
-                row and shape[1] > 1 and sl != row):
-            raise ValueError(f"{name} is not the tensor these parameters were made for")
+def _same(name, t, shape, dtype, batch, row):
+    """ValueError unless t is the tensor (its shape and strides, 0 for dense ones) that the parameters are for."""
+    sb, sl = t.stride()[:2]
+    if t.shape != shape or t.dtype != dtype or (batch and shape[0] > 1 and sb != batch) or (
+            row and shape[1] > 1 and sl != row):
+        raise ValueError(f"{name} is not the tensor these parameters were made for")
 
 
 def _band_call(p, q, k, v):
-    _same_call(p, ("q", q, (p.N, p.Lq, p.Hq, p.D), p.q_batch, p.q_row),
-               ("k", k, (p.N, p.Lk, p.Hk, p.D), p.k_batch, p.k_row), ("v", v, (p.N, p.Lk, p.Hk, p.D), p.v_batch, p.v_row))
+    dt, keys = _torch_dtype(p.dtype), (p.N, p.Lk, p.Hk, p.D)
+    _same("q", q, (p.N, p.Lq, p.Hq, p.D), dt, p.q_batch, p.q_row)
+    _same("k", k, keys, dt, p.k_batch, p.k_row)
+    _same("v", v, keys, dt, p.v_batch, p.v_row)
 
 
 def band_forward(p: dcn4_band_params, q, k, v, bias=None, buckets=None, q_start=None, q_len=None, k_len=None, out=None):
@@ -672,17 +682,16 @@ def band_forward(p: dcn4_band_params, q, k, v, bias=None, buckets=None, q_start=
     for CUDA tensors as band_params_for takes them."""
     import torch
     _band_call(p, q, k, v)
+    shape = (p.N, p.Lq, p.Hq, p.D)
     if out is None:
-        out = torch.empty((p.N, p.Lq, p.Hq, p.D), dtype=q.dtype, device=q.device)
+        out = _dense_like(q, shape)
     else:
-        _dense("out", out, (p.N, p.Lq, p.Hq, p.D), q.dtype, q.device)
-    lse = torch.empty((p.N, p.Hq, p.Lq), dtype=torch.float32, device=q.device)
+        _dense("out", out, shape, q.dtype, q.device)
+    lse = q.new_empty((p.N, p.Hq, p.Lq), dtype=torch.float32)
     need = dcn4_band_forward_workspace_size(p)
     ws = _workspace(need, q)
-    with _on_device(q):
-        check(dcn4_band_forward(p, q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(bias), _ptr(buckets), _ptr(q_start),
-                                _ptr(q_len), _ptr(k_len), out.data_ptr(), lse.data_ptr(), _ptr(ws), need,
-                                _stream_handle(q.device)))
+    _launch(q.device, dcn4_band_forward, p, q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(bias), _ptr(buckets),
+            _ptr(q_start), _ptr(q_len), _ptr(k_len), out.data_ptr(), lse.data_ptr(), _ptr(ws), need)
     return out, lse
 
 
@@ -696,17 +705,15 @@ def band_backward(p: dcn4_band_params, q, k, v, out, lse, grad_out, bias=None, b
     for name, t in (("out", out), ("grad_out", grad_out)):
         _dense(name, t, (p.N, p.Lq, p.Hq, p.D), dt, dev)
     _dense("lse", lse, (p.N, p.Hq, p.Lq), torch.float32, dev)
-    gq = torch.empty((p.N, p.Lq, p.Hq, p.D), dtype=dt, device=dev)
-    gk = torch.empty((p.N, p.Lk, p.Hk, p.D), dtype=dt, device=dev)
-    gv = torch.empty((p.N, p.Lk, p.Hk, p.D), dtype=dt, device=dev)
-    gb = torch.empty((p.nb, p.Hq), dtype=dt, device=dev) if bias is not None and want_bias else None
+    gq = torch.empty_like(grad_out)
+    keys = (p.N, p.Lk, p.Hk, p.D)
+    gk, gv = _dense_like(k, keys), _dense_like(v, keys)
+    gb = torch.empty_like(bias) if bias is not None and want_bias else None
     need = dcn4_band_backward_workspace_size(p)
     ws = _workspace(need, q)
-    with _on_device(q):
-        check(dcn4_band_backward(p, q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(bias), _ptr(buckets), _ptr(q_start),
-                                 _ptr(q_len), _ptr(k_len), out.data_ptr(), lse.data_ptr(), grad_out.data_ptr(),
-                                 gq.data_ptr(), gk.data_ptr(), gv.data_ptr(), _ptr(gb), _ptr(ws), need,
-                                 _stream_handle(dev)))
+    _launch(dev, dcn4_band_backward, p, q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(bias), _ptr(buckets), _ptr(q_start),
+            _ptr(q_len), _ptr(k_len), out.data_ptr(), lse.data_ptr(), grad_out.data_ptr(), gq.data_ptr(), gk.data_ptr(),
+            gv.data_ptr(), _ptr(gb), _ptr(ws), need)
     return gq, gk, gv, gb
 
 
@@ -740,19 +747,18 @@ def qknorm_params_for(q, k, wq=None, wk=None, pos=None, inv_freq=None, *, interl
 
 
 def _qknorm_call(p, q, k):
-    _same_call(p, ("q", q, (p.N, p.L, p.Hq, p.D), p.q_batch, p.q_row), ("k", k, (p.N, p.L, p.Hk, p.D), p.k_batch, p.k_row))
+    dt = _torch_dtype(p.dtype)
+    _same("q", q, (p.N, p.L, p.Hq, p.D), dt, p.q_batch, p.q_row)
+    _same("k", k, (p.N, p.L, p.Hk, p.D), dt, p.k_batch, p.k_row)
 
 
 def qknorm_forward(p: dcn4_qknorm_params, q, k, wq=None, wk=None, pos=None, inv_freq=None):
     """(q_out [N, L, Hq, D], k_out [N, L, Hk, D]): the heads of q and k RMS-normed, weighted and
     rotated by their positions, for CUDA tensors as qknorm_params_for takes them."""
-    import torch
     _qknorm_call(p, q, k)
-    qo = torch.empty((p.N, p.L, p.Hq, p.D), dtype=q.dtype, device=q.device)
-    ko = torch.empty((p.N, p.L, p.Hk, p.D), dtype=q.dtype, device=q.device)
-    with _on_device(q):
-        check(dcn4_qknorm_forward(p, q.data_ptr(), k.data_ptr(), _ptr(wq), _ptr(wk), _ptr(pos), _ptr(inv_freq),
-                                  qo.data_ptr(), ko.data_ptr(), _stream_handle(q.device)))
+    qo, ko = _dense_like(q, (p.N, p.L, p.Hq, p.D)), _dense_like(k, (p.N, p.L, p.Hk, p.D))
+    _launch(q.device, dcn4_qknorm_forward, p, q.data_ptr(), k.data_ptr(), _ptr(wq), _ptr(wk), _ptr(pos), _ptr(inv_freq),
+            qo.data_ptr(), ko.data_ptr())
     return qo, ko
 
 
@@ -769,10 +775,8 @@ def qknorm_backward(p: dcn4_qknorm_params, q, k, wq, wk, pos, inv_freq, grad_q_o
     gwk = torch.empty_like(wk) if wk is not None else None
     need = dcn4_qknorm_backward_workspace_size(p) if wq is not None or wk is not None else 0
     ws = _workspace(need, q)
-    with _on_device(q):
-        check(dcn4_qknorm_backward(p, q.data_ptr(), k.data_ptr(), _ptr(wq), _ptr(wk), _ptr(pos), _ptr(inv_freq),
-                                   grad_q_out.data_ptr(), grad_k_out.data_ptr(), gq.data_ptr(), gk.data_ptr(),
-                                   _ptr(gwq), _ptr(gwk), _ptr(ws), need, _stream_handle(dev)))
+    _launch(dev, dcn4_qknorm_backward, p, q.data_ptr(), k.data_ptr(), _ptr(wq), _ptr(wk), _ptr(pos), _ptr(inv_freq),
+            grad_q_out.data_ptr(), grad_k_out.data_ptr(), gq.data_ptr(), gk.data_ptr(), _ptr(gwq), _ptr(gwk), _ptr(ws), need)
     return gq, gk, gwq, gwk
 
 

@@ -791,16 +791,17 @@ __global__ void __launch_bounds__(256) kv_join_kernel(BandArgs a, KvShape sh, in
     *reinterpret_cast<uint2*>(to) = make_uint2(pack2<T>(s.x, s.y), pack2<T>(s.z, s.w));
 }
 
-// sums[h][rel] = the warps' diagonal sums of head h, in a fixed order: 8 warps of `per` CTAs an image.
+// sums[z][h][rel] = the warps' diagonal sums of head h, in a fixed order: 8 warps of
+// `per` CTAs an image, a z-th of the CTAs a block.
 __global__ void __launch_bounds__(256) diag_sum_kernel(BandArgs a, int per, const float* __restrict__ diag, float* __restrict__ sums) {
     __shared__ float s_part[8][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.y, len = 2 * a.M + 1, rel = blockIdx.x * 32 + lane;
     const int hk = h / a.G, g = h - hk * a.G;
-    const long long ctas = static_cast<long long>(a.N) * per;
+    const long long ctas = static_cast<long long>(a.N) * per, c0 = ctas * blockIdx.z / gridDim.z, c1 = ctas * (blockIdx.z + 1) / gridDim.z;
     float s = 0.f;
     if (rel < len) {
-#pragma unroll 4
-        for (long long c = 0; c < ctas; ++c) {
+#pragma unroll 8
+        for (long long c = c0; c < c1; ++c) {
             const long long n = c / per, cta = (n * a.Hk + hk) * per + c - n * per;
             s += diag[((cta * 8 + warp) * a.G + g) * len + rel];
         }
@@ -809,18 +810,21 @@ __global__ void __launch_bounds__(256) diag_sum_kernel(BandArgs a, int per, cons
     __syncthreads();
     if (warp || rel >= len) return;
     for (int w = 1; w < 8; ++w) s += s_part[w][lane];
-    sums[static_cast<long long>(h) * len + rel] = s;
+    sums[(static_cast<long long>(blockIdx.z) * a.Hq + h) * len + rel] = s;
 }
 
 // gbias[b][h]: a warp sums the relative positions of its bucket.
 template <typename T>
-__global__ void __launch_bounds__(256) bucket_sum_kernel(BandArgs a, const float* __restrict__ sums, T* __restrict__ gbias) {
+__global__ void __launch_bounds__(256) bucket_sum_kernel(BandArgs a, int parts, const float* __restrict__ sums, T* __restrict__ gbias) {
     const int e = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31, len = 2 * a.M + 1;
     if (e >= a.nb * a.Hq) return;
     const int b = e / a.Hq, h = e - b * a.Hq;
     float s = 0.f;
     for (int r = lane; r < len; r += 32)
-        if (__ldg(a.buckets + r) == b) s += sums[static_cast<long long>(h) * len + r];
+        if (__ldg(a.buckets + r) == b) {
+#pragma unroll 8
+            for (int z = 0; z < parts; ++z) s += sums[(static_cast<long long>(z) * a.Hq + h) * len + r];
+        }
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (lane == 0) gbias[e] = from_f32<T>(s);
 }
@@ -853,11 +857,12 @@ size_t part_bytes(const BandArgs& a, const KvShape& s) {
 size_t diag_bytes(const BandArgs& a, const KvShape& s) {
     return a.nb ? up256(static_cast<size_t>(a.N) * a.Hq * s.items() * 8 * (2 * a.M + 1) * sizeof(float)) : 0;
 }
-size_t sums_bytes(const BandArgs& a) { return a.nb ? up256(static_cast<size_t>(a.Hq) * (2 * a.M + 1) * sizeof(float)) : 0; }
-
-template <typename K>
-cudaError_t allow_smem(K kernel, size_t bytes) {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+// blocks of a diagonal's sum: some eight CTAs each
+int sum_parts(const BandArgs& a, const KvShape& s) {
+    return static_cast<int>(std::min<long long>(32, (static_cast<long long>(a.N) * s.items() + 7) / 8));
+}
+size_t sums_bytes(const BandArgs& a, const KvShape& s) {
+    return a.nb ? up256(static_cast<size_t>(sum_parts(a, s)) * a.Hq * (2 * a.M + 1) * sizeof(float)) : 0;
 }
 
 template <typename T, int NB, bool BIAS, bool EXACT>
@@ -873,9 +878,8 @@ cudaError_t launch(const BandArgs& a, const void* out, const float* lse, const v
     const long long dense = static_cast<long long>(a.Hq) * a.D;
     const size_t smem_q = QCfg<NB>::smem + (BIAS ? static_cast<size_t>(a.G) * kv.floats * sizeof(float) : 0),
                  smem_kv = KvCfg<NB>::smem + (BIAS ? static_cast<size_t>(a.G) * kv.floats * sizeof(float) : 0);
-    // (first, for the context: another thread may run the backward, and the maps' encoder asks for one)
-    cudaError_t e = allow_smem(grad_q_kernel<T, NB, BIAS, EXACT>, smem_q);
-    if (e == cudaSuccess) e = allow_smem(grad_kv_kernel<T, NB, BIAS, EXACT>, smem_kv);
+    cudaError_t e = allow_smem<grad_q_kernel<T, NB, BIAS, EXACT>>();
+    if (e == cudaSuccess) e = allow_smem<grad_kv_kernel<T, NB, BIAS, EXACT>>();
     if (e == cudaSuccess && BIAS) e = cudaMemsetAsync(diag, 0, diag_bytes(a, kv), stream);
     if (e != cudaSuccess) return e;
     CUtensorMap mq, mg, mk, mv, mq1, mg1, mk1, mv1;
@@ -905,9 +909,10 @@ cudaError_t launch(const BandArgs& a, const void* out, const float* lse, const v
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     if (!BIAS || !gbias) return cudaSuccess;
-    diag_sum_kernel<<<dim3((2 * a.M + 32) / 32, a.Hq), 256, 0, stream>>>(a, kv.items(), diag, sums);
+    const int zs = sum_parts(a, kv);
+    diag_sum_kernel<<<dim3((2 * a.M + 32) / 32, a.Hq, zs), 256, 0, stream>>>(a, kv.items(), diag, sums);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    bucket_sum_kernel<T><<<(a.nb * a.Hq + 7) / 8, 256, 0, stream>>>(a, sums, static_cast<T*>(gbias));
+    bucket_sum_kernel<T><<<(a.nb * a.Hq + 7) / 8, 256, 0, stream>>>(a, zs, sums, static_cast<T*>(gbias));
     return cudaGetLastError();
 }
 
@@ -920,7 +925,7 @@ bool band_bwd_tc_fits(const BandArgs& a) {
 
 size_t band_bwd_tc_workspace(const BandArgs& a) {
     const KvShape kv = kv_shape(a);
-    return stats_bytes(a) + part_bytes(a, kv) + diag_bytes(a, kv) + sums_bytes(a);
+    return stats_bytes(a) + part_bytes(a, kv) + diag_bytes(a, kv) + sums_bytes(a, kv);
 }
 
 cudaError_t launch_band_bwd_tc(const BandArgs& a, const void* out, const float* lse, const void* gout, void* gq, void* gk, void* gv,

@@ -521,7 +521,7 @@ cudaError_t launch(const BandArgs& a, const FwdShape& s, void* out, float* lse, 
     using C = Cfg<NB>;
     const size_t smem = 1024 + static_cast<size_t>(s.alt ? 1 : 2) * NB * kTcBlock + static_cast<size_t>(C::slots) * 2 * NB * kKeyBlock +
                         s.pack * s.table * sizeof(float);
-    cudaError_t e = cudaFuncSetAttribute(fwd_kernel<T, NB, BIAS, EXACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    cudaError_t e = allow_smem<fwd_kernel<T, NB, BIAS, EXACT>>();
     if (e != cudaSuccess) return e;
     CUtensorMap mq, mk, mv;
     if (!make_map(&mq, a.dtype, a.q, a.N, a.Lq, a.Hq, a.D, a.q_batch, a.q_row, s.pack, s.tq) ||

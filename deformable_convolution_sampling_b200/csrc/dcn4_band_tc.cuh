@@ -210,6 +210,21 @@ __device__ __forceinline__ uint32_t pack_low(float lo, float hi, uint32_t pair) 
     }
 }
 
+// Lets a kernel have all of an SM's shared memory, once a thread and device (which
+// also gives the thread its context: another thread may run a backward, and the
+// maps' encoder asks for one).
+constexpr int kMaxDynamicSmem = 225 << 10;
+template <auto kernel>
+cudaError_t allow_smem() {
+    static thread_local unsigned long long done = 0;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && (done >> dev & 1))) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamicSmem);
+    if (e == cudaSuccess && dev < 64) done |= 1ull << dev;
+    return e;
+}
+
 // cuTensorMapEncodeTiled from the driver (resolved once through the runtime).
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
