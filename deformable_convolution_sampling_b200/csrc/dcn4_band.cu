@@ -41,19 +41,40 @@ __global__ void __launch_bounds__(256) join_kernel(BandArgs a, int splits, BandP
     if (lane == 0) lse[r] = l == 0.f ? -INFINITY : m + logf(l);
 }
 
-// A warp per entry of gbias: its parts of every image and block, in a fixed order.
-template <typename T>
-__global__ void __launch_bounds__(256) bias_sum_kernel(BandArgs a, const float* __restrict__ bpart, int blocks, int heads,
-                                                       T* __restrict__ gbias) {
-    const int e = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (e >= a.nb * a.Hq) return;
-    const int b = e / a.Hq, h = e - b * a.Hq, grp = h / heads, in = h - grp * heads, groups = a.Hq / heads;
+// sums[z][h][rel] = the diagonal sums of head h, in a fixed order; a z-th of the CTAs a block.
+__global__ void __launch_bounds__(256) diag_sum_kernel(BandArgs a, int per, int each, const float* __restrict__ diag, float* __restrict__ sums) {
+    __shared__ float s_part[8][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.y, len = 2 * a.M + 1, rel = blockIdx.x * 32 + lane;
+    const int hk = h / a.G, g = h - hk * a.G;
+    const long long ctas = static_cast<long long>(a.N) * per, c0 = ctas * blockIdx.z / gridDim.z, c1 = ctas * (blockIdx.z + 1) / gridDim.z;
     float s = 0.f;
-    const long long count = static_cast<long long>(a.N) * blocks;
-    for (long long c = lane; c < count; c += 32) {
-        const long long n = c / blocks, blk = c - n * blocks;
-        s += bpart[(((n * groups + grp) * blocks + blk) * a.nb + b) * heads + in];
+    if (rel < len) {
+        // (CTA, sum) pairs, dealt to the warps
+#pragma unroll 8
+        for (long long e = c0 * each + warp; e < c1 * each; e += 8) {
+            const long long c = e / each, n = c / per, cta = (n * a.Hk + hk) * per + c - n * per;
+            s += diag[((cta * each + e - c * each) * a.G + g) * len + rel];
+        }
     }
+    s_part[warp][lane] = s;
+    __syncthreads();
+    if (warp || rel >= len) return;
+    for (int w = 1; w < 8; ++w) s += s_part[w][lane];
+    sums[(static_cast<long long>(blockIdx.z) * a.Hq + h) * len + rel] = s;
+}
+
+// gbias[b][h]: a warp sums the relative positions of its bucket.
+template <typename T>
+__global__ void __launch_bounds__(256) bucket_sum_kernel(BandArgs a, int parts, const float* __restrict__ sums, T* __restrict__ gbias) {
+    const int e = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31, len = 2 * a.M + 1;
+    if (e >= a.nb * a.Hq) return;
+    const int b = e / a.Hq, h = e - b * a.Hq;
+    float s = 0.f;
+    for (int r = lane; r < len; r += 32)
+        if (__ldg(a.buckets + r) == b) {
+#pragma unroll 8
+            for (int z = 0; z < parts; ++z) s += sums[(static_cast<long long>(z) * a.Hq + h) * len + r];
+        }
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (lane == 0) gbias[e] = from_f32<T>(s);
 }
@@ -65,7 +86,10 @@ __global__ void __launch_bounds__(256) no_keys_kernel(float* __restrict__ lse, l
 
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
-size_t delta_bytes(const BandArgs& a) { return round256(static_cast<size_t>(band_rows(a)) * sizeof(float)); }
+// Blocks that share a diagonal's sum: some 64 sums each.
+int sum_parts(const BandArgs& a, int per, int each) {
+    return static_cast<int>(std::min<long long>(32, (static_cast<long long>(a.N) * per * each + 63) / 64));
+}
 
 }  // namespace
 
@@ -81,13 +105,21 @@ cudaError_t launch_band_join(const BandArgs& a, int splits, BandPart part, void*
     return cudaGetLastError();
 }
 
-cudaError_t launch_band_bias_sum(const BandArgs& a, const float* bpart, int blocks, int heads, void* gbias,
+size_t band_sum_bytes(const BandArgs& a) {
+    return static_cast<size_t>(32) * a.Hq * (2 * a.M + 1) * sizeof(float);
+}
+
+cudaError_t launch_band_bias_sum(const BandArgs& a, int per, int each, const float* diag, float* sums, void* gbias,
                                  cudaStream_t stream) {
+    const int zs = sum_parts(a, per, each);
+    diag_sum_kernel<<<dim3((2 * a.M + 32) / 32, a.Hq, zs), 256, 0, stream>>>(a, per, each, diag, sums);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
     const unsigned grid = static_cast<unsigned>((a.nb * a.Hq + 7) / 8);
     switch (a.dtype) {
-        case 0: bias_sum_kernel<float><<<grid, 256, 0, stream>>>(a, bpart, blocks, heads, static_cast<float*>(gbias)); break;
-        case 1: bias_sum_kernel<__half><<<grid, 256, 0, stream>>>(a, bpart, blocks, heads, static_cast<__half*>(gbias)); break;
-        case 2: bias_sum_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(a, bpart, blocks, heads, static_cast<__nv_bfloat16*>(gbias)); break;
+        case 0: bucket_sum_kernel<float><<<grid, 256, 0, stream>>>(a, zs, sums, static_cast<float*>(gbias)); break;
+        case 1: bucket_sum_kernel<__half><<<grid, 256, 0, stream>>>(a, zs, sums, static_cast<__half*>(gbias)); break;
+        case 2: bucket_sum_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(a, zs, sums, static_cast<__nv_bfloat16*>(gbias)); break;
         default: return cudaErrorInvalidValue;
     }
     return cudaGetLastError();
@@ -115,8 +147,7 @@ cudaError_t band_status(unsigned* status, bool reset) {
 
 size_t band_backward_workspace_bytes(const BandArgs& a) {
     if (band_bwd_tc_fits(a)) return band_bwd_tc_workspace(a);
-    const size_t parts = static_cast<size_t>(a.N) * a.Hk * simt_row_blocks(a) * a.nb * a.G;
-    return delta_bytes(a) + round256(parts * sizeof(float));
+    return band_simt_backward_workspace(a);
 }
 
 cudaError_t launch_band_forward(const BandArgs& a, void* out, float* lse, void* ws, cudaStream_t stream) {
@@ -126,9 +157,7 @@ cudaError_t launch_band_forward(const BandArgs& a, void* out, float* lse, void* 
 cudaError_t launch_band_backward(const BandArgs& a, const void* out, const float* lse, const void* gout, void* gq,
                                  void* gk, void* gv, void* gbias, void* ws, cudaStream_t stream) {
     if (band_bwd_tc_fits(a)) return launch_band_bwd_tc(a, out, lse, gout, gq, gk, gv, gbias, ws, stream);
-    float* delta = static_cast<float*>(ws);
-    float* bpart = reinterpret_cast<float*>(static_cast<char*>(ws) + delta_bytes(a));
-    return launch_band_simt_backward(a, out, lse, gout, gq, gk, gv, gbias, delta, bpart, stream);
+    return launch_band_simt_backward(a, out, lse, gout, gq, gk, gv, gbias, ws, stream);
 }
 
 }  // namespace dcn4

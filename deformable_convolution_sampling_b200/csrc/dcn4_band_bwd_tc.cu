@@ -52,36 +52,44 @@ __device__ __forceinline__ void fill_table(const BandArgs& a, float* table, int 
     }
 }
 
-// (lse, delta) of every row, [N][Hq][padded Lq]; 16 lanes a row.  Without a bias lse is
-// in log2 units, as the scores are formed there.
+// (lse, delta) of every row, [N][Hq][padded Lq].  Without a bias lse is in log2
+// units, as the scores are formed there.  `lanes` lanes a row, four rows a thread:
+// bound by HBM.
 template <typename T>
-__global__ void __launch_bounds__(256) stats_kernel(BandArgs a, const T* __restrict__ out, const float* __restrict__ lse,
+__global__ void __launch_bounds__(256) stats_kernel(BandArgs a, int lanes, const T* __restrict__ out, const float* __restrict__ lse,
                                                     const T* __restrict__ gout, float2* __restrict__ stats) {
-    const int LP = padded_queries(a.Lq);
-    const long long r = blockIdx.x * 16ll + (threadIdx.x >> 4), rows = static_cast<long long>(a.N) * LP * a.Hq;
-    const int piece = threadIdx.x & 15;
-    const bool on = r < rows;
-    const int h = on ? static_cast<int>(r % a.Hq) : 0;
-    const long long ni = on ? r / a.Hq : 0;
-    const int n = static_cast<int>(ni / LP), i = static_cast<int>(ni - static_cast<long long>(n) * LP);
-    const bool live = on && i < band_qlen(a, n);
-    float d = 0.f;
-    if (live && piece * 8 < a.D) {
-        const long long at = ((static_cast<long long>(n) * a.Lq + i) * a.Hq + h) * a.D + piece * 8;
-        float2 x[4], y[4];
-        unpack(__ldg(reinterpret_cast<const uint4*>(out + at)), x, T());
-        unpack(__ldg(reinterpret_cast<const uint4*>(gout + at)), y, T());
+    constexpr int U = 4;
+    const int LP = padded_queries(a.Lq), groups = 256 / lanes, blocks = (LP + groups * U - 1) / (groups * U);
+    const int nh = blockIdx.x / blocks, n = nh / a.Hq, h = nh - n * a.Hq, i0 = (blockIdx.x - nh * blocks) * groups * U + threadIdx.x / lanes;
+    const int piece = threadIdx.x % lanes, qlen = band_qlen(a, n);
+    uint4 x[U], y[U];
+    float l[U];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) d = fmaf(x[e].x, y[e].x, fmaf(x[e].y, y[e].y, d));
+    for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * groups;
+        x[u] = y[u] = make_uint4(0u, 0u, 0u, 0u);
+        l[u] = INFINITY;
+        if (i >= qlen) continue;
+        const long long at = ((static_cast<long long>(n) * a.Lq + i) * a.Hq + h) * a.D + piece * 8;
+        if (piece * 8 < a.D) {
+            x[u] = __ldg(reinterpret_cast<const uint4*>(out + at));
+            y[u] = __ldg(reinterpret_cast<const uint4*>(gout + at));
+        }
+        if (piece == 0) l[u] = band_lse_ref(lse[static_cast<long long>(nh) * a.Lq + i]);
     }
-    for (int o = 8; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-    if (on && piece == 0) {
-        const long long nh = static_cast<long long>(n) * a.Hq + h;
-        const float l = live ? band_lse_ref(lse[nh * a.Lq + i]) : INFINITY;
-        stats[nh * LP + i] = make_float2(a.nb ? l : l * kLog2e, d);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        float2 p[4], q[4];
+        unpack(x[u], p, T());
+        unpack(y[u], q, T());
+        float d = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) d = fmaf(p[e].x, q[e].x, fmaf(p[e].y, q[e].y, d));
+        for (int o = lanes >> 1; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+        const int i = i0 + u * groups;
+        if (i < LP && piece == 0) stats[static_cast<long long>(nh) * LP + i] = make_float2(a.nb ? l[u] : l[u] * kLog2e, d);
     }
 }
-
 
 // ---------------------------------------------------------------------------
 // grad_q
@@ -292,7 +300,9 @@ __global__ void __launch_bounds__(QCfg<NB>::threads, 1)
                         const float bb = table[g * floats + (side > 0 ? floats - 1 : 0)];
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
-                            x[c][e] = __float_as_uint((fmaf(__uint_as_float(x[c][e]), sc, side ? bb : tab[j + e]) - st.x) * kLog2e);
+                            x[c][e] = __float_as_uint(fmaf(__uint_as_float(x[c][e]), sc, side ? bb : tab[j + e]));
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) sub_mul2(x[c][e], x[c][e + 1], st.x, kLog2e);
                     } else {
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) fma2(x[c][e], x[c][e + 1], sc, -st.x);
@@ -791,44 +801,6 @@ __global__ void __launch_bounds__(256) kv_join_kernel(BandArgs a, KvShape sh, in
     *reinterpret_cast<uint2*>(to) = make_uint2(pack2<T>(s.x, s.y), pack2<T>(s.z, s.w));
 }
 
-// sums[z][h][rel] = the warps' diagonal sums of head h, in a fixed order: 8 warps of
-// `per` CTAs an image, a z-th of the CTAs a block.
-__global__ void __launch_bounds__(256) diag_sum_kernel(BandArgs a, int per, const float* __restrict__ diag, float* __restrict__ sums) {
-    __shared__ float s_part[8][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.y, len = 2 * a.M + 1, rel = blockIdx.x * 32 + lane;
-    const int hk = h / a.G, g = h - hk * a.G;
-    const long long ctas = static_cast<long long>(a.N) * per, c0 = ctas * blockIdx.z / gridDim.z, c1 = ctas * (blockIdx.z + 1) / gridDim.z;
-    float s = 0.f;
-    if (rel < len) {
-#pragma unroll 8
-        for (long long c = c0; c < c1; ++c) {
-            const long long n = c / per, cta = (n * a.Hk + hk) * per + c - n * per;
-            s += diag[((cta * 8 + warp) * a.G + g) * len + rel];
-        }
-    }
-    s_part[warp][lane] = s;
-    __syncthreads();
-    if (warp || rel >= len) return;
-    for (int w = 1; w < 8; ++w) s += s_part[w][lane];
-    sums[(static_cast<long long>(blockIdx.z) * a.Hq + h) * len + rel] = s;
-}
-
-// gbias[b][h]: a warp sums the relative positions of its bucket.
-template <typename T>
-__global__ void __launch_bounds__(256) bucket_sum_kernel(BandArgs a, int parts, const float* __restrict__ sums, T* __restrict__ gbias) {
-    const int e = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31, len = 2 * a.M + 1;
-    if (e >= a.nb * a.Hq) return;
-    const int b = e / a.Hq, h = e - b * a.Hq;
-    float s = 0.f;
-    for (int r = lane; r < len; r += 32)
-        if (__ldg(a.buckets + r) == b) {
-#pragma unroll 8
-            for (int z = 0; z < parts; ++z) s += sums[(static_cast<long long>(z) * a.Hq + h) * len + r];
-        }
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) gbias[e] = from_f32<T>(s);
-}
-
 KvShape kv_shape(const BandArgs& a) {
     KvShape s;
     s.floats = a.nb ? table_floats(a.M) : 0;
@@ -857,13 +829,7 @@ size_t part_bytes(const BandArgs& a, const KvShape& s) {
 size_t diag_bytes(const BandArgs& a, const KvShape& s) {
     return a.nb ? up256(static_cast<size_t>(a.N) * a.Hq * s.items() * 8 * (2 * a.M + 1) * sizeof(float)) : 0;
 }
-// blocks of a diagonal's sum: some eight CTAs each
-int sum_parts(const BandArgs& a, const KvShape& s) {
-    return static_cast<int>(std::min<long long>(32, (static_cast<long long>(a.N) * s.items() + 7) / 8));
-}
-size_t sums_bytes(const BandArgs& a, const KvShape& s) {
-    return a.nb ? up256(static_cast<size_t>(sum_parts(a, s)) * a.Hq * (2 * a.M + 1) * sizeof(float)) : 0;
-}
+size_t sums_bytes(const BandArgs& a) { return a.nb ? up256(band_sum_bytes(a)) : 0; }
 
 template <typename T, int NB, bool BIAS, bool EXACT>
 cudaError_t launch(const BandArgs& a, const void* out, const float* lse, const void* gout, void* gq, void* gk, void* gv, void* gbias,
@@ -892,9 +858,12 @@ cudaError_t launch(const BandArgs& a, const void* out, const float* lse, const v
         !make_map(&mk1, a.dtype, a.k, a.N, a.Lk, a.Hk, a.D, a.k_batch, a.k_row, 1, kTcRows) ||
         !make_map(&mv1, a.dtype, a.v, a.N, a.Lk, a.Hk, a.D, a.v_batch, a.v_row, 1, kTcRows))
         return cudaErrorInvalidValue;
-    const long long rows = static_cast<long long>(a.N) * padded_queries(a.Lq) * a.Hq;
-    stats_kernel<T><<<static_cast<unsigned>((rows + 15) / 16), 256, 0, stream>>>(a, static_cast<const T*>(out), lse,
-                                                                              static_cast<const T*>(gout), stats);
+    int lanes = 1;
+    while (lanes * 8 < a.D) lanes *= 2;
+    const int each = 4 * 256 / lanes;
+    const long long row_blocks = static_cast<long long>(a.N) * a.Hq * ((padded_queries(a.Lq) + each - 1) / each);
+    stats_kernel<T><<<static_cast<unsigned>(row_blocks), 256, 0, stream>>>(a, lanes, static_cast<const T*>(out), lse,
+                                                                                      static_cast<const T*>(gout), stats);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     grad_q_kernel<T, NB, BIAS, EXACT><<<static_cast<unsigned>(static_cast<long long>(a.N) * (a.Hq / pack) * blocks), QCfg<NB>::threads, smem_q, stream>>>(
         mq, mg, mk, mv, a, pack, tq, blocks, kv.floats, band_most_keys(a) <= kFewKeys, stats, static_cast<T*>(gq));
@@ -908,12 +877,7 @@ cudaError_t launch(const BandArgs& a, const void* out, const float* lse, const v
         kv_join_kernel<T><<<static_cast<unsigned>((n4 + 255) / 256), 256, 0, stream>>>(a, kv, tiles, part, static_cast<T*>(gk), static_cast<T*>(gv));
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
-    if (!BIAS || !gbias) return cudaSuccess;
-    const int zs = sum_parts(a, kv);
-    diag_sum_kernel<<<dim3((2 * a.M + 32) / 32, a.Hq, zs), 256, 0, stream>>>(a, kv.items(), diag, sums);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    bucket_sum_kernel<T><<<(a.nb * a.Hq + 7) / 8, 256, 0, stream>>>(a, zs, sums, static_cast<T*>(gbias));
-    return cudaGetLastError();
+    return BIAS && gbias ? launch_band_bias_sum(a, kv.items(), 8, diag, sums, gbias, stream) : cudaSuccess;
 }
 
 }  // namespace
@@ -925,7 +889,7 @@ bool band_bwd_tc_fits(const BandArgs& a) {
 
 size_t band_bwd_tc_workspace(const BandArgs& a) {
     const KvShape kv = kv_shape(a);
-    return stats_bytes(a) + part_bytes(a, kv) + diag_bytes(a, kv) + sums_bytes(a, kv);
+    return stats_bytes(a) + part_bytes(a, kv) + diag_bytes(a, kv) + sums_bytes(a);
 }
 
 cudaError_t launch_band_bwd_tc(const BandArgs& a, const void* out, const float* lse, const void* gout, void* gq, void* gk, void* gv,

@@ -400,13 +400,12 @@ __global__ void __launch_bounds__(Cfg<NB>::threads, Cfg<NB>::ctas)
                     for (int e = 0; e < 32; e += 2) {
                         uint32_t &lo = x[c][e], &hi = x[c][e + 1];
                         if (BIAS) {  // the difference first: scores may be of the type's lowest value
-                            lo = __float_as_uint(ex2((__uint_as_float(lo) - ref) * kLog2e));
-                            hi = __float_as_uint(ex2((__uint_as_float(hi) - ref) * kLog2e));
+                            sub_mul2(lo, hi, ref, kLog2e);
                         } else {
                             fma2(lo, hi, sc, -ref);
-                            lo = __float_as_uint(ex2(__uint_as_float(lo)));
-                            hi = __float_as_uint(ex2(__uint_as_float(hi)));
                         }
+                        lo = __float_as_uint(ex2(__uint_as_float(lo)));
+                        hi = __float_as_uint(ex2(__uint_as_float(hi)));
                         add2(sum[(e >> 1) & 1], lo, hi);
                         p[e >> 1] = pack2<T>(__uint_as_float(lo), __uint_as_float(hi));
                     }

@@ -16,7 +16,7 @@ struct BandPart {
     float* o;
     float2* ml;
 };
-inline long long band_rows(const BandArgs& a) { return static_cast<long long>(a.N) * a.Hq * a.Lq; }
+__host__ __device__ inline long long band_rows(const BandArgs& a) { return static_cast<long long>(a.N) * a.Hq * a.Lq; }
 inline size_t band_part_bytes(const BandArgs& a, int splits) {
     return splits > 1 ? static_cast<size_t>(band_rows(a)) * splits * (a.D * sizeof(float) + sizeof(float2)) : 0;
 }
@@ -45,8 +45,10 @@ inline long long band_most_keys(const BandArgs& a) {
 
 // out and lse of every row from its parts.
 cudaError_t launch_band_join(const BandArgs& a, int splits, BandPart part, void* out, float* lse, cudaStream_t stream);
-// gbias[b][h] from parts bpart[(n Hq / heads + group) blocks + block][nb][heads].
-cudaError_t launch_band_bias_sum(const BandArgs& a, const float* bpart, int blocks, int heads, void* gbias,
+// gbias from sums of ds along diagonals: diag[((n Hk + hk) per + c) each + w][G][2 M + 1], c < per
+// CTAs of an image and key head, w < each sums a CTA.  Needs band_sum_bytes of scratch.
+size_t band_sum_bytes(const BandArgs& a);
+cudaError_t launch_band_bias_sum(const BandArgs& a, int per, int each, const float* diag, float* sums, void* gbias,
                                  cudaStream_t stream);
 
 // 16-bit types on the tensor cores (dcn4_band_fwd_tc.cu).
@@ -66,6 +68,7 @@ int simt_row_blocks(const BandArgs& a);
 int simt_splits(const BandArgs& a);
 cudaError_t launch_band_simt_forward(const BandArgs& a, void* out, float* lse, void* ws, cudaStream_t stream);
 cudaError_t launch_band_simt_backward(const BandArgs& a, const void* out, const float* lse, const void* gout, void* gq,
-                                      void* gk, void* gv, void* gbias, float* delta, float* bpart, cudaStream_t stream);
+                                      void* gk, void* gv, void* gbias, void* ws, cudaStream_t stream);
+size_t band_simt_backward_workspace(const BandArgs& a);
 
 }  // namespace dcn4

@@ -44,16 +44,16 @@ __device__ __forceinline__ void load_tile(float* dst, int D, Row row) {
     }
 }
 
-// x[r][c] = sum_d A[4 ty + r][d] B[tx + 16 c][d]
+// x[r][c] = sum_{d < D} A[4 ty + r][d] B[tx + 16 c][d]
 template <int DP>
-__device__ __forceinline__ void product(float (&x)[4][4], const float* A, const float* B, int ty, int tx) {
+__device__ __forceinline__ void product(float (&x)[4][4], const float* A, const float* B, int D, int ty, int tx) {
     constexpr int LD = DP + 4;
 #pragma unroll
     for (int r = 0; r < 4; ++r)
 #pragma unroll
         for (int c = 0; c < 4; ++c) x[r][c] = 0.f;
 #pragma unroll 4
-    for (int d = 0; d < DP; d += 4) {
+    for (int d = 0; d < D; d += 4) {
         float4 u[4], w[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) u[r] = *reinterpret_cast<const float4*>(A + (4 * ty + r) * LD + d);
@@ -138,6 +138,27 @@ __device__ __forceinline__ float bias_of(const BandArgs& a, int rel, int h) {
     const int b = bucket_of(a, rel);
     return static_cast<unsigned>(b) < static_cast<unsigned>(a.nb) ? to_f32(static_cast<const T*>(a.bias)[static_cast<long long>(b) * a.Hq + h]) : 0.f;
 }
+// The bias of a group's heads by relative position, in shared memory where that fits
+// (two loads that wait for one another are a pair's whole arithmetic otherwise).
+constexpr int kTableBytes = 24 << 10;
+inline int simt_table(const BandArgs& a) {  // floats, 0: none
+    const long long n = static_cast<long long>(a.G) * (2 * a.M + 1);
+    return a.nb && n * 4 <= kTableBytes ? static_cast<int>(n) : 0;
+}
+template <typename T>
+struct Bias {
+    const float* table;  // [G][2 M + 1], or NULL
+    __device__ __forceinline__ Bias(const BandArgs& a, float* smem, int floats, int h0) : table(floats ? smem : nullptr) {
+        for (int e = threadIdx.x; e < floats; e += kThreads) {
+            const int g = e / (2 * a.M + 1);
+            smem[e] = bias_of<T>(a, e - g * (2 * a.M + 1) - a.M, h0 + g);
+        }
+    }
+    __device__ __forceinline__ float at(const BandArgs& a, int rel, int g, int h0) const {
+        if (!a.nb) return 0.f;
+        return table ? table[g * (2 * a.M + 1) + max(-a.M, min(rel, a.M)) + a.M] : bias_of<T>(a, rel, h0 + g);
+    }
+};
 
 // Maximum and sum over the 16 lanes that share a row.
 __device__ __forceinline__ float row_max(float v) {
@@ -151,7 +172,7 @@ __device__ __forceinline__ float row_sum(float v) {
 
 template <typename T, int DP>
 __global__ void __launch_bounds__(kThreads)
-    simt_forward_kernel(BandArgs a, int blocks, int splits, T* __restrict__ out, float* __restrict__ lse, BandPart part) {
+    simt_forward_kernel(BandArgs a, int blocks, int splits, int floats, T* __restrict__ out, float* __restrict__ lse, BandPart part) {
     constexpr int LD = DP + 4;
     extern __shared__ __align__(16) float smem[];
     float *Qs = smem, *Ks = Qs + kB * LD, *Vs = Ks + kB * LD, *Ps = Vs + kB * LD;
@@ -159,6 +180,7 @@ __global__ void __launch_bounds__(kThreads)
     const int n = nh / a.Hk, hk = nh - n * a.Hk;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int klen = band_klen(a, n), qlen = band_qlen(a, n), start = band_start(a, n);
+    const Bias<T> bias(a, Ps + kB * kPL, floats, hk * a.G);
     const int rows = a.Lq * a.G, r0 = blk * kB;
     const int i0 = r0 / a.G, i1 = min((min(r0 + kB, rows) - 1) / a.G, qlen - 1);
     const T* q = static_cast<const T*>(a.q) + n * a.q_batch + static_cast<long long>(hk) * a.G * a.D;
@@ -193,7 +215,7 @@ __global__ void __launch_bounds__(kThreads)
             load_tile<T, DP>(Vs, a.D, [&](int j) -> const T* { return j0 + j < klen ? v + (j0 + j) * a.v_row : nullptr; });
             __syncthreads();
             float x[4][4];
-            product<DP>(x, Qs, Ks, ty, tx);
+            product<DP>(x, Qs, Ks, a.D, ty, tx);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 float top = -INFINITY;
@@ -201,7 +223,7 @@ __global__ void __launch_bounds__(kThreads)
                 for (int c = 0; c < 4; ++c) {
                     const int j = j0 + tx + 16 * c;
                     const bool see = live[r] && band_sees(a, pos[r], j, klen);
-                    x[r][c] = see ? x[r][c] * a.scale + (a.nb ? bias_of<T>(a, j - pos[r], head[r]) : 0.f) : -INFINITY;
+                    x[r][c] = see ? x[r][c] * a.scale + bias.at(a, j - pos[r], head[r] - hk * a.G, hk * a.G) : -INFINITY;
                     top = fmaxf(top, x[r][c]);
                 }
                 const float mn = fmaxf(m[r], row_max(top));
@@ -240,18 +262,21 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
-// gq of 64 rows, their D (into delta) and, with a bias, the CTA's part of gbias.
+// gq of 64 rows over a range of their keys, their D (into delta) and, with a bias, the
+// sums of ds along diagonals: diag[CTA][G][2 M + 1], of relative position -M .. M (the ends: and beyond).
 template <typename T, int DP>
 __global__ void __launch_bounds__(kThreads)
-    simt_grad_q_kernel(BandArgs a, int blocks, const T* __restrict__ out, const float* __restrict__ lse,
+    simt_grad_q_kernel(BandArgs a, int blocks, int splits, int floats, const T* __restrict__ out, const float* __restrict__ lse,
                        const T* __restrict__ gout, T* __restrict__ gq, float* __restrict__ delta,
-                       float* __restrict__ bpart) {
+                       float* __restrict__ part, float* __restrict__ diag) {
     constexpr int LD = DP + 4;
     extern __shared__ __align__(16) float smem[];
-    float *Qs = smem, *Gs = Qs + kB * LD, *Ks = Gs + kB * LD, *Vs = Ks + kB * LD, *Ps = Vs + kB * LD, *diag = Ps + kB * kPL;
-    const int blk = blockIdx.x % blocks, nh = blockIdx.x / blocks;
+    float *Qs = smem, *Gs = Qs + kB * LD, *Ks = Gs + kB * LD, *Vs = Ks + kB * LD, *Ps = Vs + kB * LD, *sums = Ps + kB * kPL;
+    const int sp = blockIdx.x % splits, blk = blockIdx.x / splits % blocks, nh = blockIdx.x / splits / blocks;
     const int n = nh / a.Hk, hk = nh - n * a.Hk;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int spread = (kB + a.G - 1) / a.G + 1 + kB;  // relative positions of one tile and head at most
+    const Bias<T> bias(a, sums + (a.nb ? spread * a.G : 0), floats, hk * a.G);
     const int klen = band_klen(a, n), qlen = band_qlen(a, n), start = band_start(a, n);
     const int rows = a.Lq * a.G, r0 = blk * kB;
     const int i0 = r0 / a.G, ilast = (min(r0 + kB, rows) - 1) / a.G, i1 = min(ilast, qlen - 1);
@@ -280,23 +305,26 @@ __global__ void __launch_bounds__(kThreads)
         float d = 0.f;
         for (int e = tx; e < DP; e += 16) d = fmaf(Gs[(4 * ty + r) * LD + e], Ks[(4 * ty + r) * LD + e], d);
         de[r] = row_sum(d);
-        if (tx == 0 && row < rows) delta[at] = de[r];
+        if (tx == 0 && row < rows && sp == 0) delta[at] = de[r];
 #pragma unroll
         for (int c = 0; c < DP / 16; ++c) o[r][c] = 0.f;
     }
-    float* mine = bpart + static_cast<long long>(blockIdx.x) * a.nb * a.G;
-    for (int e = threadIdx.x; e < a.nb * a.G; e += kThreads) mine[e] = 0.f;
+    float* mine = diag + static_cast<long long>(blockIdx.x) * a.G * (2 * a.M + 1);
+    if (a.nb)
+        for (int e = threadIdx.x; e < a.G * (2 * a.M + 1); e += kThreads) mine[e] = 0.f;
     if (i0 <= i1) {
         const BandTiles bt = band_tiles(a, start + i0, start + i1, klen, kB);
-        for (int t = 0; t < bt.count(); ++t) {
+        const int cnt = bt.count(), t0 = static_cast<int>(static_cast<long long>(cnt) * sp / splits),
+                  t1 = static_cast<int>(static_cast<long long>(cnt) * (sp + 1) / splits);
+        for (int t = t0; t < t1; ++t) {
             const int j0 = bt.tile(t) * kB;
             __syncthreads();
             load_tile<T, DP>(Ks, a.D, [&](int j) -> const T* { return j0 + j < klen ? k + (j0 + j) * a.k_row : nullptr; });
             load_tile<T, DP>(Vs, a.D, [&](int j) -> const T* { return j0 + j < klen ? v + (j0 + j) * a.v_row : nullptr; });
             __syncthreads();
             float x[4][4], y[4][4];
-            product<DP>(x, Qs, Ks, ty, tx);
-            product<DP>(y, Gs, Vs, ty, tx);
+            product<DP>(x, Qs, Ks, a.D, ty, tx);
+            product<DP>(y, Gs, Vs, a.D, ty, tx);
 #pragma unroll
             for (int r = 0; r < 4; ++r)
 #pragma unroll
@@ -304,7 +332,7 @@ __global__ void __launch_bounds__(kThreads)
                     const int j = j0 + tx + 16 * c;
                     float ds = 0.f;
                     if (live[r] && band_sees(a, pos[r], j, klen)) {
-                        const float s = x[r][c] * a.scale + (a.nb ? bias_of<T>(a, j - pos[r], head[r]) : 0.f);
+                        const float s = x[r][c] * a.scale + bias.at(a, j - pos[r], head[r] - hk * a.G, hk * a.G);
                         ds = expf(s - le[r]) * (y[r][c] - de[r]);
                     }
                     Ps[(4 * ty + r) * kPL + tx + 16 * c] = ds;
@@ -312,26 +340,29 @@ __global__ void __launch_bounds__(kThreads)
             __syncthreads();
             accumulate_rows<DP>(o, Ps, Ks, ty, tx);
             if (a.nb) {
-                // the tile's sums along each head's diagonals (all pairs of one relative position),
-                // then each bucket's owner adds its diagonals in order
+                // the tile's sums along each head's diagonals (all pairs of one relative position): one thread
+                // adds a diagonal's to its place, one warp those of a head beyond M
                 const int nd = ilast - i0 + kB;  // relative positions j0 - (start + ilast) ...
                 const int rel0 = j0 - start - ilast;
                 for (int e = threadIdx.x; e < nd * a.G; e += kThreads) {
-                    const int g = e / nd, d = e - g * nd;
+                    const int g = e / nd, d = e - g * nd, rel = rel0 + d;
                     float s = 0.f;
                     for (int i = i0; i <= ilast; ++i) {
                         const int j = d + i - ilast, row = i * a.G + g - r0;
                         if (j >= 0 && j < kB && row >= 0 && row < kB) s += Ps[row * kPL + j];
                     }
-                    diag[e] = s;
+                    sums[e] = s;
+                    if (rel > -a.M && rel < a.M) mine[g * (2 * a.M + 1) + rel + a.M] += s;
                 }
+                if (rel0 > -a.M && rel0 + nd - 1 < a.M) continue;
                 __syncthreads();
-                for (int e = threadIdx.x; e < a.nb * a.G; e += kThreads) {
-                    const int b = e / a.G, g = e - b * a.G;
+                for (int e = threadIdx.x >> 5; e < 2 * a.G; e += kThreads / 32) {
+                    const int g = e >> 1, lane = threadIdx.x & 31;
                     float s = 0.f;
-                    for (int d = 0; d < nd; ++d)
-                        if (bucket_of(a, rel0 + d) == b) s += diag[g * nd + d];
-                    mine[e] += s;
+                    for (int d = lane; d < nd; d += 32)
+                        if (e & 1 ? rel0 + d >= a.M : rel0 + d <= -a.M) s += sums[g * nd + d];
+                    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                    if (lane == 0) mine[g * (2 * a.M + 1) + (e & 1 ? 2 * a.M : 0)] += s;
                 }
             }
         }
@@ -339,21 +370,26 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
         const int row = r0 + 4 * ty + r;
-        if (row < rows) store_rows<T, DP>(gq + dense(row), a.D, o, r, tx, a.scale);
+        if (row >= rows) continue;
+        if (splits > 1)
+            store_rows<float, DP>(part + sp * band_rows(a) * a.D + dense(row), a.D, o, r, tx, a.scale);
+        else
+            store_rows<T, DP>(gq + dense(row), a.D, o, r, tx, a.scale);
     }
 }
 
-// gk and gv of 64 keys.
+// gk and gv of 64 keys over a range of the queries that see them.
 template <typename T, int DP>
 __global__ void __launch_bounds__(kThreads)
-    simt_grad_kv_kernel(BandArgs a, int blocks, const float* __restrict__ lse, const T* __restrict__ gout,
-                        const float* __restrict__ delta, T* __restrict__ gk, T* __restrict__ gv) {
+    simt_grad_kv_kernel(BandArgs a, int blocks, int splits, int floats, const float* __restrict__ lse, const T* __restrict__ gout,
+                        const float* __restrict__ delta, T* __restrict__ gk, T* __restrict__ gv, float* __restrict__ part) {
     constexpr int LD = DP + 4;
     extern __shared__ __align__(16) float smem[];
     float *Qs = smem, *Gs = Qs + kB * LD, *Ks = Gs + kB * LD, *Vs = Ks + kB * LD, *Ps = Vs + kB * LD, *Ds = Ps + kB * kPL;
-    const int blk = blockIdx.x % blocks, nh = blockIdx.x / blocks;
+    const int sp = blockIdx.x % splits, blk = blockIdx.x / splits % blocks, nh = blockIdx.x / splits / blocks;
     const int n = nh / a.Hk, hk = nh - n * a.Hk;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const Bias<T> bias(a, Ds + kB * kPL, floats, hk * a.G);
     const int klen = band_klen(a, n), qlen = band_qlen(a, n), start = band_start(a, n);
     const int j0 = blk * kB;
     const T* q = static_cast<const T*>(a.q) + n * a.q_batch + static_cast<long long>(hk) * a.G * a.D;
@@ -368,7 +404,9 @@ __global__ void __launch_bounds__(kThreads)
         for (int c = 0; c < DP / 16; ++c) ok[r][c] = ov[r][c] = 0.f;
     int ilo = 0, ihi = 0;
     if (j0 < klen) band_queries(a, start, qlen, j0, min(j0 + kB, klen), ilo, ihi);
-    const int rlo = ilo * a.G, rhi = ihi * a.G;
+    const int first = ilo * a.G, last = ihi * a.G, tiles = (last - first + kB - 1) / kB;
+    const int rlo = first + static_cast<int>(static_cast<long long>(tiles) * sp / splits) * kB,
+              rhi = min(last, first + static_cast<int>(static_cast<long long>(tiles) * (sp + 1) / splits) * kB);
     for (int r0 = rlo; r0 < rhi; r0 += kB) {
         __syncthreads();
         load_tile<T, DP>(Qs, a.D, [&](int r) -> const T* {
@@ -379,8 +417,8 @@ __global__ void __launch_bounds__(kThreads)
         });
         __syncthreads();
         float x[4][4], y[4][4];
-        product<DP>(x, Qs, Ks, ty, tx);
-        product<DP>(y, Gs, Vs, ty, tx);
+        product<DP>(x, Qs, Ks, a.D, ty, tx);
+        product<DP>(y, Gs, Vs, a.D, ty, tx);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int row = r0 + 4 * ty + r, i = row / a.G, h = hk * a.G + row % a.G, pos = start + i;
@@ -392,7 +430,7 @@ __global__ void __launch_bounds__(kThreads)
                 const int j = j0 + tx + 16 * c;
                 float p = 0.f;
                 if (live && band_sees(a, pos, j, klen))
-                    p = expf(x[r][c] * a.scale + (a.nb ? bias_of<T>(a, j - pos, h) : 0.f) - le);
+                    p = expf(x[r][c] * a.scale + bias.at(a, j - pos, h - hk * a.G, hk * a.G) - le);
                 Ps[(4 * ty + r) * kPL + tx + 16 * c] = p;
                 Ds[(4 * ty + r) * kPL + tx + 16 * c] = p == 0.f ? 0.f : p * (y[r][c] - de);
             }
@@ -406,14 +444,44 @@ __global__ void __launch_bounds__(kThreads)
         const int j = j0 + 4 * ty + r;
         if (j >= a.Lk) continue;
         const long long at = ((static_cast<long long>(n) * a.Lk + j) * a.Hk + hk) * a.D;
-        store_rows<T, DP>(gk + at, a.D, ok, r, tx, a.scale);
-        store_rows<T, DP>(gv + at, a.D, ov, r, tx, 1.f);
+        if (splits > 1) {
+            const long long all = static_cast<long long>(a.N) * a.Lk * a.Hk * a.D;
+            store_rows<float, DP>(part + 2 * sp * all + at, a.D, ok, r, tx, a.scale);
+            store_rows<float, DP>(part + (2 * sp + 1) * all + at, a.D, ov, r, tx, 1.f);
+        } else {
+            store_rows<T, DP>(gk + at, a.D, ok, r, tx, a.scale);
+            store_rows<T, DP>(gv + at, a.D, ov, r, tx, 1.f);
+        }
     }
+}
+
+// out[e] = the sum of its parts, `apart` elements from one another, in order.
+template <typename T>
+__global__ void __launch_bounds__(256) sum_parts_kernel(const float* __restrict__ part, int parts, long long apart, long long n, T* __restrict__ out) {
+    const long long e = 4 * (blockIdx.x * 256ll + threadIdx.x);
+    if (e >= n) return;  // n is a multiple of 4
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int p = 0; p < parts; ++p) {
+        const float4 v = __ldg(reinterpret_cast<const float4*>(part + p * apart + e));
+        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+    out[e] = from_f32<T>(s.x);
+    out[e + 1] = from_f32<T>(s.y);
+    out[e + 2] = from_f32<T>(s.z);
+    out[e + 3] = from_f32<T>(s.w);
 }
 
 template <int DP>
 constexpr size_t tiles_smem(int tiles, int probs) {
     return (static_cast<size_t>(tiles) * kB * (DP + 4) + static_cast<size_t>(probs) * kB * kPL) * sizeof(float);
+}
+
+// Ranges along the other side for `ctas` CTAs of `tiles` tiles each: up to one CTA an SM,
+// down to a tile each (at 333 x 333 keys, grad_kv's 24 CTAs of up to 11 tiles took 164 us,
+// 144 of up to 2 take 32).
+int split_count(long long ctas, long long tiles) {
+    return static_cast<int>(std::max<long long>(1, std::min<long long>(kBandSms / std::max<long long>(ctas, 1), std::min<long long>(tiles, 256))));
 }
 
 template <typename K>
@@ -423,38 +491,76 @@ cudaError_t allow_smem(K kernel, size_t bytes) {
 
 template <typename T, int DP>
 cudaError_t forward_typed(const BandArgs& a, void* out, float* lse, void* ws, cudaStream_t stream) {
-    const int blocks = simt_row_blocks(a), splits = simt_splits(a);
-    const size_t smem = tiles_smem<DP>(3, 1);
+    const int blocks = simt_row_blocks(a), splits = simt_splits(a), floats = simt_table(a);
+    const size_t smem = tiles_smem<DP>(3, 1) + floats * sizeof(float);
     cudaError_t e = allow_smem(simt_forward_kernel<T, DP>, smem);
     if (e != cudaSuccess) return e;
     const BandPart part = band_part(a, splits, ws);
     simt_forward_kernel<T, DP><<<static_cast<unsigned>(static_cast<long long>(a.N) * a.Hk * blocks * splits), kThreads, smem, stream>>>(
-        a, blocks, splits, static_cast<T*>(out), lse, part);
+        a, blocks, splits, floats, static_cast<T*>(out), lse, part);
     e = cudaGetLastError();
     if (e != cudaSuccess || splits == 1) return e;
     return launch_band_join(a, splits, part, out, lse, stream);
 }
 
+// Ranges of the queries that see a key tile (splits of grad_kv).
+int kv_splits(const BandArgs& a) {
+    const long long ctas = static_cast<long long>(a.N) * a.Hk * ((a.Lk + kB - 1) / kB);
+    const long long reach = std::min<long long>(a.Lq, static_cast<long long>(std::min(a.left, kBandMaxLen)) + std::min(a.right, kBandMaxLen) + kB);
+    return split_count(ctas, ((a.sinks ? static_cast<long long>(a.Lq) : reach) * a.G + kB - 1) / kB);
+}
+size_t up256(size_t b) { return (b + 255) / 256 * 256; }
+// Workspace of the backward: delta, parts (grad_q's, then grad_kv's in the same place), diagonal sums, their sums by head.
+struct Workspace {
+    size_t delta, part, diag, sums;
+    explicit Workspace(const BandArgs& a) {
+        const int sq = simt_splits(a), sk = kv_splits(a);
+        const size_t nq = static_cast<size_t>(band_rows(a)) * a.D, nk = static_cast<size_t>(a.N) * a.Lk * a.Hk * a.D;
+        delta = up256(static_cast<size_t>(band_rows(a)) * sizeof(float));
+        part = up256(std::max(sq > 1 ? nq * sq : 0, sk > 1 ? 2 * nk * sk : 0) * sizeof(float));
+        const size_t ctas = static_cast<size_t>(a.N) * a.Hk * simt_row_blocks(a) * sq;
+        diag = a.nb ? up256(ctas * a.G * (2 * a.M + 1) * sizeof(float)) : 0;
+        sums = a.nb ? up256(band_sum_bytes(a)) : 0;
+    }
+};
+
+template <typename T>
+cudaError_t launch_sum_parts(const float* part, int parts, long long apart, long long n, void* out, cudaStream_t stream) {
+    sum_parts_kernel<T><<<static_cast<unsigned>((n / 4 + 255) / 256), 256, 0, stream>>>(part, parts, apart, n, static_cast<T*>(out));
+    return cudaGetLastError();
+}
+
 template <typename T, int DP>
 cudaError_t backward_typed(const BandArgs& a, const void* out, const float* lse, const void* gout, void* gq, void* gk,
-                           void* gv, void* gbias, float* delta, float* bpart, cudaStream_t stream) {
-    const int blocks = simt_row_blocks(a);
+                           void* gv, void* gbias, void* ws, cudaStream_t stream) {
+    const Workspace w(a);
+    char* at = static_cast<char*>(ws);
+    float* delta = reinterpret_cast<float*>(at);
+    float* part = reinterpret_cast<float*>(at += w.delta);
+    float* diag = reinterpret_cast<float*>(at += w.part);
+    float* sums = reinterpret_cast<float*>(at += w.diag);
+    const int blocks = simt_row_blocks(a), sq = simt_splits(a), sk = kv_splits(a), floats = simt_table(a);
     const int spread = (kB + a.G - 1) / a.G + 1 + kB;  // relative positions of one tile and head at most
-    const size_t smem_q = tiles_smem<DP>(4, 1) + (a.nb ? static_cast<size_t>(spread) * a.G * sizeof(float) : 0);
+    const size_t smem_q = tiles_smem<DP>(4, 1) + (a.nb ? (static_cast<size_t>(spread) * a.G + floats) * sizeof(float) : 0),
+                 smem_kv = tiles_smem<DP>(4, 2) + floats * sizeof(float);
     cudaError_t e = allow_smem(simt_grad_q_kernel<T, DP>, smem_q);
-    if (e == cudaSuccess) e = allow_smem(simt_grad_kv_kernel<T, DP>, tiles_smem<DP>(4, 2));
+    if (e == cudaSuccess) e = allow_smem(simt_grad_kv_kernel<T, DP>, smem_kv);
     if (e != cudaSuccess) return e;
-    const long long ctas = static_cast<long long>(a.N) * a.Hk * blocks;
+    const long long ctas = static_cast<long long>(a.N) * a.Hk * blocks * sq;
     simt_grad_q_kernel<T, DP><<<static_cast<unsigned>(ctas), kThreads, smem_q, stream>>>(
-        a, blocks, static_cast<const T*>(out), lse, static_cast<const T*>(gout), static_cast<T*>(gq), delta, bpart);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+        a, blocks, sq, floats, static_cast<const T*>(out), lse, static_cast<const T*>(gout), static_cast<T*>(gq), delta, part, diag);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const long long nq = band_rows(a) * a.D, nk = static_cast<long long>(a.N) * a.Lk * a.Hk * a.D;
+    if (sq > 1 && (e = launch_sum_parts<T>(part, sq, nq, nq, gq, stream)) != cudaSuccess) return e;
     const int kblocks = (a.Lk + kB - 1) / kB;
-    simt_grad_kv_kernel<T, DP><<<static_cast<unsigned>(static_cast<long long>(a.N) * a.Hk * kblocks), kThreads, tiles_smem<DP>(4, 2), stream>>>(
-        a, kblocks, lse, static_cast<const T*>(gout), delta, static_cast<T*>(gk), static_cast<T*>(gv));
-    e = cudaGetLastError();
-    if (e != cudaSuccess || !a.nb) return e;
-    return launch_band_bias_sum(a, bpart, blocks, a.G, gbias, stream);
+    simt_grad_kv_kernel<T, DP><<<static_cast<unsigned>(static_cast<long long>(a.N) * a.Hk * kblocks * sk), kThreads, smem_kv, stream>>>(
+        a, kblocks, sk, floats, lse, static_cast<const T*>(gout), delta, static_cast<T*>(gk), static_cast<T*>(gv), part);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (sk > 1) {
+        if ((e = launch_sum_parts<T>(part, sk, 2 * nk, nk, gk, stream)) != cudaSuccess) return e;
+        if ((e = launch_sum_parts<T>(part + nk, sk, 2 * nk, nk, gv, stream)) != cudaSuccess) return e;
+    }
+    return a.nb && gbias ? launch_band_bias_sum(a, blocks * sq, 1, diag, sums, gbias, stream) : cudaSuccess;
 }
 
 }  // namespace
@@ -463,7 +569,13 @@ int simt_row_blocks(const BandArgs& a) {
     return static_cast<int>((static_cast<long long>(a.Lq) * a.G + kB - 1) / kB);
 }
 int simt_splits(const BandArgs& a) {
-    return band_splits(a, static_cast<long long>(a.N) * a.Hk * simt_row_blocks(a), std::min(a.Lq, kB / a.G + 2), kB, 2);
+    const long long span = std::min<long long>(a.Lk, static_cast<long long>(std::min(a.left, kBandMaxLen)) +
+                                                         std::min(a.right, kBandMaxLen) + std::min(a.Lq, kB / a.G + 2) + a.sinks);
+    return split_count(static_cast<long long>(a.N) * a.Hk * simt_row_blocks(a), (span + kB - 1) / kB);
+}
+size_t band_simt_backward_workspace(const BandArgs& a) {
+    const Workspace w(a);
+    return w.delta + w.part + w.diag + w.sums;
 }
 
 cudaError_t launch_band_simt_forward(const BandArgs& a, void* out, float* lse, void* ws, cudaStream_t stream) {
@@ -477,11 +589,11 @@ cudaError_t launch_band_simt_forward(const BandArgs& a, void* out, float* lse, v
 }
 
 cudaError_t launch_band_simt_backward(const BandArgs& a, const void* out, const float* lse, const void* gout, void* gq,
-                                      void* gk, void* gv, void* gbias, float* delta, float* bpart, cudaStream_t stream) {
+                                      void* gk, void* gv, void* gbias, void* ws, cudaStream_t stream) {
     const bool wide = a.D > 64;
 #define DCN4_BAND_BWD(T)                                                                                             \
-    (wide ? backward_typed<T, 128>(a, out, lse, gout, gq, gk, gv, gbias, delta, bpart, stream)                       \
-          : backward_typed<T, 64>(a, out, lse, gout, gq, gk, gv, gbias, delta, bpart, stream))
+    (wide ? backward_typed<T, 128>(a, out, lse, gout, gq, gk, gv, gbias, ws, stream)                                 \
+          : backward_typed<T, 64>(a, out, lse, gout, gq, gk, gv, gbias, ws, stream))
     switch (a.dtype) {
         case 0: return DCN4_BAND_BWD(float);
         case 1: return DCN4_BAND_BWD(__half);

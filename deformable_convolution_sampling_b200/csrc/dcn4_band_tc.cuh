@@ -145,6 +145,13 @@ __device__ __forceinline__ void fma2(uint32_t& x, uint32_t& y, float m, float c)
         : "+r"(x), "+r"(y)
         : "f"(m), "f"(c));
 }
+// (x - c) * m of two values at once.
+__device__ __forceinline__ void sub_mul2(uint32_t& x, uint32_t& y, float c, float m) {
+    asm("{\n\t.reg .b64 v, w, z;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 w, {%2, %2};\n\tmov.b64 z, {%3, %3};\n\t"
+        "add.rn.f32x2 v, v, w;\n\tmul.rn.f32x2 v, v, z;\n\tmov.b64 {%0, %1}, v;\n\t}"
+        : "+r"(x), "+r"(y)
+        : "f"(-c), "f"(m));
+}
 __device__ __forceinline__ void add2(float2& s, uint32_t x, uint32_t y) {
     asm("{\n\t.reg .b64 v, w;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 w, {%2, %3};\n\tadd.rn.f32x2 v, v, w;\n\tmov.b64 {%0, %1}, v;\n\t}"
         : "+f"(s.x), "+f"(s.y)
