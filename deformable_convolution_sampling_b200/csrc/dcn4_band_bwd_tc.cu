@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(QCfg<NB>::threads, 1)
                   int tq, int blocks, int floats, int twice, float2* __restrict__ stats, T* __restrict__ gq) {
     constexpr int kSlots = QCfg<NB>::slots;
     extern __shared__ __align__(1024) unsigned char band_smem[];
-    __shared__ __align__(8) uint64_t full[kSlots], empty[kSlots], raw, rows_full, s_full[2], p_full[2], o_done[2];
+    __shared__ __align__(8) uint64_t full[kSlots], empty[kSlots], raw, rows_full, s_full[2], e_full[2], p_full[2], o_done[2];
     __shared__ uint32_t taddr_s;
     __shared__ int s_abort;
     const int tid = threadIdx.x, warp = static_cast<int>(uniform(tid >> 5)), lane = tid & 31;
@@ -133,6 +133,7 @@ __global__ void __launch_bounds__(QCfg<NB>::threads, 1)
         mbar_init(smem_u32(&rows_full), 1);
         for (int w = 0; w < 2; ++w) {
             mbar_init(smem_u32(&s_full[w]), 1);
+            mbar_init(smem_u32(&e_full[w]), 1);
             mbar_init(smem_u32(&p_full[w]), 4);
             mbar_init(smem_u32(&o_done[w]), 1);
         }
@@ -214,6 +215,9 @@ __global__ void __launch_bounds__(QCfg<NB>::threads, 1)
             const uint32_t at_s = tmem + w * 256, at_o = at_s + 128;
             bool ok = warp_wait(&rows_full, 0u, abort), some = false;
             uint32_t p_phase = 0;
+            // half a step behind the first half, so that one's products run under the other's exponentials
+            int ca0, cb0;
+            if (w == 1 && active(0, 0, ca0, cb0)) ok = ok && warp_wait(&p_full[0], 0u, abort);
             int s = 0;
             uint32_t ph = 0;
 #pragma unroll 1
@@ -227,8 +231,9 @@ __global__ void __launch_bounds__(QCfg<NB>::threads, 1)
                     if (elect_one()) {
                         const uint32_t id = id_s | (static_cast<uint32_t>((cb - ca) * (kTcChunk / 8)) << 17);
                         issue_rows<NB>(at_s + ca * kTcChunk, q_desc, kTcBlock, step_desc(k_desc, row), kTileBlock, id, steps);
+                        umma_commit(smem_u32(&s_full[w]));  // the exponentials run under the second product
                         issue_rows<NB>(at_s + 64 + ca * kTcChunk, g_desc, kTcBlock, step_desc(v_desc, row), kTileBlock, id, steps);
-                        umma_commit(smem_u32(&s_full[w]));
+                        umma_commit(smem_u32(&e_full[w]));
                     }
                     __syncwarp();
                     if (!(ok = warp_wait(&p_full[w], p_phase, abort))) break;
@@ -282,21 +287,17 @@ __global__ void __launch_bounds__(QCfg<NB>::threads, 1)
             if (!(ok = warp_wait(&s_full[w], nw & 1, abort))) break;
             tc_fence_after();
             if (warp_live) {
-                uint32_t x[kChunks][32], y[kChunks][32];
+                uint32_t x[kChunks][32];
 #pragma unroll
                 for (int c = 0; c < kChunks; ++c)
-                    if (c >= ca && c < cb) {
-                        tmem_ld32_async(at_s + c * kTcChunk, x[c]);
-                        tmem_ld32_async(at_s + 64 + c * kTcChunk, y[c]);
-                    }
+                    if (c >= ca && c < cb) tmem_ld32_async(at_s + c * kTcChunk, x[c]);
 #pragma unroll
                 for (int c = 0; c < kChunks; ++c) {
                     if (c < ca || c >= cb) continue;
                     const int j = j0 + c * kTcChunk;
                     tmem_ld_wait(x[c]);
-                    tmem_ld_wait(y[c]);
-                    const int side = j - phi >= a.M ? 1 : j + kTcChunk - 1 - plo <= -a.M ? -1 : 0;
                     if (BIAS) {
+                        const int side = j - phi >= a.M ? 1 : j + kTcChunk - 1 - plo <= -a.M ? -1 : 0;
                         const float bb = table[g * floats + (side > 0 ? floats - 1 : 0)];
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
@@ -308,8 +309,20 @@ __global__ void __launch_bounds__(QCfg<NB>::threads, 1)
                         for (int e = 0; e < 32; e += 2) fma2(x[c][e], x[c][e + 1], sc, -st.x);
                     }
 #pragma unroll
+                    for (int e = 0; e < 32; ++e) x[c][e] = __float_as_uint(ex2(__uint_as_float(x[c][e])));
+                }
+                if (!(ok = warp_wait(&e_full[w], nw & 1, abort))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) {
+                    if (c < ca || c >= cb) continue;
+                    const int j = j0 + c * kTcChunk;
+                    uint32_t y[32];
+                    tmem_ld32_async(at_s + 64 + c * kTcChunk, y);
+                    tmem_ld_wait(y);
+#pragma unroll
                     for (int e = 0; e < 32; ++e)
-                        x[c][e] = __float_as_uint(ex2(__uint_as_float(x[c][e])) * (__uint_as_float(y[c][e]) - delta));
+                        x[c][e] = __float_as_uint(__uint_as_float(x[c][e]) * (__uint_as_float(y[e]) - delta));
                     if (j < all_lo || j > all_hi) {
                         const uint32_t see = (low_bits(jhi - j) & ~low_bits(jlo - j)) | low_bits(jsink - j);
 #pragma unroll
@@ -470,7 +483,7 @@ __global__ void __launch_bounds__(KvCfg<NB>::threads, 1)
     using C = KvCfg<NB>;
     constexpr int kSlots = C::slots;
     extern __shared__ __align__(1024) unsigned char band_smem[];
-    __shared__ __align__(8) uint64_t full[kSlots], empty[kSlots], raw, keys_full, s_full[2], p_full[2], done;
+    __shared__ __align__(8) uint64_t full[kSlots], empty[kSlots], raw, keys_full, s_full[2], e_full[2], p_full[2], done;
     __shared__ uint32_t taddr_s;
     __shared__ int s_abort;
     const int tid = threadIdx.x, warp = static_cast<int>(uniform(tid >> 5)), lane = tid & 31;
@@ -505,6 +518,7 @@ __global__ void __launch_bounds__(KvCfg<NB>::threads, 1)
         mbar_init(smem_u32(&done), 1);
         for (int w = 0; w < 2; ++w) {
             mbar_init(smem_u32(&s_full[w]), 1);
+            mbar_init(smem_u32(&e_full[w]), 1);
             mbar_init(smem_u32(&p_full[w]), 4);
         }
         s_abort = 0;
@@ -524,11 +538,17 @@ __global__ void __launch_bounds__(KvCfg<NB>::threads, 1)
     // (even steps go through the first half of them, odd ones through the second: each softmax
     // half then meets neighbouring tiles)
     const int half = (cnt + 1) >> 1;
-    auto step_of = [&](int t, int& g, int& i) {
-        const int u = t0 + (t >> 1) + (t & 1 ? half : 0);
-        g = u / nq;
-        i = (q0 + u - g * nq) * kTile;
+    struct Step {  // goes through every other step with additions only
+        int g, r, nq;
+        __device__ __forceinline__ Step(int u, int nq) : nq(nq) {
+            g = nq ? u / nq : 0;
+            r = u - g * nq;
+        }
+        __device__ __forceinline__ void next() {
+            if (++r == nq) r = 0, ++g;
+        }
     };
+    auto first_of = [&](int odd) { return Step(t0 + (odd ? half : 0), nq); };
     auto chunks = [&](int i, int& ca, int& cb) {
         ca = (max(ilo, i) - i) >> 5;
         cb = (min(ihi, i + kTile) - i + kTcChunk - 1) >> 5;
@@ -544,10 +564,11 @@ __global__ void __launch_bounds__(KvCfg<NB>::threads, 1)
         }
         int raws = 0;
         const int LP = padded_queries(a.Lq);
+        Step even = first_of(0), odd = first_of(1);
         for (int t = 0; t < cnt; ++t) {
             const int s = t % kSlots;
-            int g, i;
-            step_of(t, g, i);
+            const int g = t & 1 ? odd.g : even.g, i = (q0 + (t & 1 ? odd.r : even.r)) * kTile;
+            if (t & 1) odd.next(); else even.next();
             if (!warp_wait(&empty[s], ((t / kSlots) & 1) ^ 1u, abort)) break;
             const uint32_t at_q = ring + s * C::stage, at_g = at_q + NB * kTileBlock;
             const bool clear = i + kTile > qlen && qlen < a.Lq;  // queries past the sequence meet p and d of 0
@@ -576,37 +597,29 @@ __global__ void __launch_bounds__(KvCfg<NB>::threads, 1)
                            q_desc = umma_desc_sw128(ring, 16, 1024), g_desc = step_desc(q_desc, NB * kTileBlock),
                            q_sum = umma_desc_sw128(ring, kTileBlock, 1024), g_sum = step_desc(q_sum, NB * kTileBlock);
             bool ok = warp_wait(&keys_full, 0u, abort);
-            int s = 0;          // slot of step t + 2 as the loop goes on
+            int s = 0, sum_slot = 0;   // slots of steps t + 2 and t
             uint32_t ph = 0;
-            auto scores = [&](int t) {
-                int g, i, ca, cb;
-                step_of(t, g, i);
-                chunks(i, ca, cb);
-                ok = ok && warp_wait(&full[s], ph, abort);
-                if (!ok) return;
-                tc_fence_after();
-                const uint32_t off = s * C::stage + ca * kTcChunk * 128, at = tmem + (t & 1) * 128 + ca * kTcChunk;
-                if (elect_one()) {
-                    const uint32_t id = id_s | (static_cast<uint32_t>((cb - ca) * (kTcChunk / 8)) << 17);
-                    issue_rows<NB>(at, k_desc, kTcBlock, step_desc(q_desc, off), kTileBlock, id, steps);
-                    issue_rows<NB>(at + 64, v_desc, kTcBlock, step_desc(g_desc, off), kTileBlock, id, steps);
-                    umma_commit(smem_u32(&s_full[t & 1]));
-                }
-                __syncwarp();
-                s = s + 1 == kSlots ? 0 : s + 1;
-                ph ^= s == 0;
-            };
-            int sum_slot = 0;
+            Step even = first_of(0), odd = first_of(1);
+            int span0 = 0, span1 = 0;  // chunks ca | cb << 8 of the even and the odd step in work
 #pragma unroll 1
             for (int t = -2; t < cnt && ok; ++t) {
+                const int z = t & 1;
+                const bool more = t + 2 < cnt;
+                int span = 0;
+                if (more) {  // all of the next step that needs no wait for this one
+                    int ca, cb;
+                    chunks((q0 + (z ? odd.r : even.r)) * kTile, ca, cb);
+                    if (z) odd.next(); else even.next();
+                    span = ca | cb << 8;
+                    if (!(ok = warp_wait(&full[s], ph, abort))) break;
+                }
+                const uint32_t at = tmem + z * 128;
                 if (t >= 0) {
-                    int g, i, ca, cb;
-                    step_of(t, g, i);
-                    chunks(i, ca, cb);
-                    if (!(ok = warp_wait(&p_full[t & 1], (t >> 1) & 1, abort))) break;
+                    const int ca = (z ? span1 : span0) & 255, cb = (z ? span1 : span0) >> 8;
+                    if (!(ok = warp_wait(&p_full[z], (t >> 1) & 1, abort))) break;
                     tc_fence_after();
                     if (elect_one()) {
-                        const uint32_t off = sum_slot * C::stage, at = tmem + (t & 1) * 128;
+                        const uint32_t off = sum_slot * C::stage;
                         issue_sum<kTile / 16>(tmem + 256, at, step_desc(g_sum, off), id_o, ca * 2, cb * 2, t > 0);
                         issue_sum<kTile / 16>(tmem + 256 + 64 * NB, at + 64, step_desc(q_sum, off), id_o, ca * 2, cb * 2, t > 0);
                         if (EXACT) {
@@ -618,7 +631,22 @@ __global__ void __launch_bounds__(KvCfg<NB>::threads, 1)
                     __syncwarp();
                     sum_slot = sum_slot + 1 == kSlots ? 0 : sum_slot + 1;
                 }
-                if (t + 2 < cnt) scores(t + 2);  // over the place of p and d of step t
+                if (more) {  // over the place of p and d of step t
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const int ca = span & 255, cb = span >> 8;
+                        const uint32_t off = s * C::stage + ca * kTcChunk * 128, to = at + ca * kTcChunk,
+                                       id = id_s | (static_cast<uint32_t>((cb - ca) * (kTcChunk / 8)) << 17);
+                        issue_rows<NB>(to, k_desc, kTcBlock, step_desc(q_desc, off), kTileBlock, id, steps);
+                        umma_commit(smem_u32(&s_full[z]));  // the exponentials run under the second product
+                        issue_rows<NB>(to + 64, v_desc, kTcBlock, step_desc(g_desc, off), kTileBlock, id, steps);
+                        umma_commit(smem_u32(&e_full[z]));
+                    }
+                    __syncwarp();
+                    (z ? span1 : span0) = span;
+                    s = s + 1 == kSlots ? 0 : s + 1;
+                    ph ^= s == 0;
+                }
             }
             if (elect_one()) umma_commit(smem_u32(&done));
             __syncwarp();
@@ -643,9 +671,11 @@ __global__ void __launch_bounds__(KvCfg<NB>::threads, 1)
         dg.rel31 = kw + 31 - start;
         bool ok = true;
         int s = w;
+        Step st_w = first_of(w);
         for (int t = w; t < cnt; t += 2) {
-            int g, i, ca, cb;
-            step_of(t, g, i);
+            int ca, cb;
+            const int g = st_w.g, i = (q0 + st_w.r) * kTile;
+            st_w.next();
             if (BIAS && warp_live && g != dg_head) {
                 if (dg_head >= 0) dg.finish(lane);
                 dg.start(diag + ((static_cast<long long>(blockIdx.x) * 8 + warp) * a.G + g) * (2 * a.M + 1));
@@ -659,33 +689,46 @@ __global__ void __launch_bounds__(KvCfg<NB>::threads, 1)
             if (warp_live) {
                 const float4* st = stat_s + s * (C::stat / 16);
                 const float* tab = table + g * sh.floats + a.M + kTableExtra + j - start;
-                uint32_t x[32], y[32];
+                uint32_t px[kChunks][32];
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c)
+                    if (c >= ca && c < cb) tmem_ld32_async(at_s + c * kTcChunk, px[c]);
 #pragma unroll
                 for (int c = 0; c < kChunks; ++c) {
                     if (c < ca || c >= cb) continue;
+                    uint32_t (&x)[32] = px[c];
                     const int ic = i + c * kTcChunk;
-                    tmem_ld32_async(at_s + c * kTcChunk, x);
-                    tmem_ld32_async(at_s + 64 + c * kTcChunk, y);
                     tmem_ld_wait(x);
-                    tmem_ld_wait(y);
                     // relative positions k0 - (start + ic + 31) ... k1 - 1 - (start + ic)
                     const int side = k0 - (start + ic + kTcChunk - 1) >= a.M ? 1 : k1 - 1 - (start + ic) <= -a.M ? -1 : 0;
                     const float bb = BIAS ? table[g * sh.floats + (side > 0 ? sh.floats - 1 : 0)] : 0.f;
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
                         const float4 u = st[(c * kTcChunk + e) >> 1];  // lse, delta of two queries
-                        float p0, p1;
                         if (BIAS) {
-                            p0 = ex2((fmaf(__uint_as_float(x[e]), sc, side ? bb : tab[-(ic + e)]) - u.x) * kLog2e);
-                            p1 = ex2((fmaf(__uint_as_float(x[e + 1]), sc, side ? bb : tab[-(ic + e + 1)]) - u.z) * kLog2e);
+                            x[e] = __float_as_uint(ex2((fmaf(__uint_as_float(x[e]), sc, side ? bb : tab[-(ic + e)]) - u.x) * kLog2e));
+                            x[e + 1] = __float_as_uint(ex2((fmaf(__uint_as_float(x[e + 1]), sc, side ? bb : tab[-(ic + e + 1)]) - u.z) * kLog2e));
                         } else {
-                            p0 = ex2(fmaf(__uint_as_float(x[e]), sc, -u.x));
-                            p1 = ex2(fmaf(__uint_as_float(x[e + 1]), sc, -u.z));
+                            x[e] = __float_as_uint(ex2(fmaf(__uint_as_float(x[e]), sc, -u.x)));
+                            x[e + 1] = __float_as_uint(ex2(fmaf(__uint_as_float(x[e + 1]), sc, -u.z)));
                         }
-                        x[e] = __float_as_uint(p0);
-                        x[e + 1] = __float_as_uint(p1);
-                        y[e] = __float_as_uint(p0 * (__uint_as_float(y[e]) - u.y));
-                        y[e + 1] = __float_as_uint(p1 * (__uint_as_float(y[e + 1]) - u.w));
+                    }
+                }
+                if (!(ok = warp_wait(&e_full[w], (t >> 1) & 1, abort))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) {
+                    if (c < ca || c >= cb) continue;
+                    uint32_t (&x)[32] = px[c];
+                    uint32_t y[32];
+                    const int ic = i + c * kTcChunk;
+                    tmem_ld32_async(at_s + 64 + c * kTcChunk, y);
+                    tmem_ld_wait(y);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const float4 u = st[(c * kTcChunk + e) >> 1];
+                        y[e] = __float_as_uint(__uint_as_float(x[e]) * (__uint_as_float(y[e]) - u.y));
+                        y[e + 1] = __float_as_uint(__uint_as_float(x[e + 1]) * (__uint_as_float(y[e + 1]) - u.w));
                     }
                     if (ic < all_lo || ic > all_hi) {
                         const uint32_t see = low_bits(vhi - ic) & ~low_bits(vlo - ic);
