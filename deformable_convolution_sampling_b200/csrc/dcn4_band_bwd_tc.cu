@@ -398,25 +398,28 @@ struct KvShape {
 
 // Diagonal sums.  All pairs of a diagonal of the score matrix share a relative
 // position, so the bias gradient is the sum of d along diagonals, then over the
-// diagonals of a bucket.  A lane holds a key; as the queries go by, a partial sum
-// moves from lane to lane: after query i, lane j holds the sum over the warp's keys
-// up to its own of the diagonal through (i, j).  Lane 31's is complete, and is handed
-// to lane i mod 32, so that 32 queries end in one store of 32 neighbouring relative
-// positions: two shuffles a query, no shared memory, no atomics, one order.
+// diagonals of a bucket.  A warp's lanes hold keys; 32 queries at a time go through 32
+// rows of 33 floats of shared memory and come back by diagonals: lane k adds those of
+// key - query = k and, apart, of k - 32.  With the next 32 queries the latter go on as
+// the former, so that every 32 queries end in one store of 32 neighbouring relative
+// positions.  No atomics, one order.  (Handing the partial sums from lane to lane by
+// shuffles needs no shared memory, but is a chain of 32 of them: 900 cycles, not 250.)
+constexpr int kDiagBuf = 32 * 33;
 struct Diagonals {
     float* mine;    // this warp's sums, of relative position -M .. M (the ends: and beyond)
-    int M, rel31;   // relative position of lane 31's key and query 0
+    float* buf;     // this warp's kDiagBuf floats
+    int M, rel0;    // relative position of lane 0's key and query 0
     int next;       // query the run goes on with; -1: no run
     bool again;     // a run of this head has been stored already: add
-    float s, below, above;
+    float carry, below, above;
     __device__ __forceinline__ void start(float* to) {
         mine = to;
         next = -1;
         again = false;
-        s = below = above = 0.f;
+        carry = below = above = 0.f;
     }
     __device__ __forceinline__ void store(int i, int lane, float v) {
-        const int rel = rel31 - i - lane;
+        const int rel = rel0 - i + lane;
         if (rel <= -M) below += v;
         else if (rel >= M) above += v;
         else {
@@ -426,30 +429,30 @@ struct Diagonals {
     }
     __device__ __forceinline__ void flush(int lane) {
         if (next < 0) return;
-        float got = 0.f;
-        for (int e = 0; e < 31; ++e) {
-            s = __shfl_up_sync(0xffffffffu, s, 1);
-            if (lane == 0) s = 0.f;
-            const float o = __shfl_sync(0xffffffffu, s, 31);
-            if (lane == e) got = o;
-        }
-        store(next, lane, got);  // lane 31 adds a 0
+        store(next, lane, carry);
         __syncwarp();
         again = true;
         next = -1;
-        s = 0.f;
+        carry = 0.f;
     }
     __device__ __forceinline__ void chunk(int i, int lane, const uint32_t (&d)[32]) {
         if (i != next) flush(lane);
-        float got = 0.f;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-            s = __shfl_up_sync(0xffffffffu, s, 1);
-            s = (lane == 0 ? 0.f : s) + __uint_as_float(d[e]);
-            const float o = __shfl_sync(0xffffffffu, s, 31);
-            if (lane == e) got = o;
+        for (int e = 0; e < 32; ++e) buf[lane * 33 + e] = __uint_as_float(d[e]);
+        __syncwarp();
+        // row r, column r - lane or, where that is below 0, r - lane + 32
+        float a[2] = {carry, 0.f}, b[2] = {};
+        const float *pa = buf - lane, *pb = pa + 32;
+#pragma unroll
+        for (int r = 0; r < 32; ++r) {
+            const bool on = r >= lane;
+            const float v = (on ? pa : pb)[34 * r];
+            if (on) a[r & 1] += v;
+            else b[r & 1] += v;
         }
-        store(i, lane, got);
+        __syncwarp();
+        store(i, lane, a[0] + a[1]);
+        carry = b[0] + b[1];
         next = i + 32;
     }
     __device__ __forceinline__ void finish(int lane) {
@@ -465,22 +468,22 @@ struct Diagonals {
     }
 };
 
-template <int NB>
+template <int NB, bool BIAS>
 struct KvCfg {
-    static constexpr int slots = NB == 1 ? 6 : 4;
+    static constexpr int slots = NB == 1 ? 6 : BIAS ? 3 : 4;
     static constexpr int threads = 320;
     static constexpr int stage = 2 * NB * kTileBlock;      // Q, G
     static constexpr int stat = kTile * sizeof(float2);
-    static constexpr size_t smem = 1024 + 2 * NB * kTcBlock + slots * (stage + stat);
+    static constexpr size_t smem = 1024 + 2 * NB * kTcBlock + slots * (stage + stat) + (BIAS ? 8 * kDiagBuf * sizeof(float) : 0);
 };
 
 template <typename T, int NB, bool BIAS, bool EXACT>
-__global__ void __launch_bounds__(KvCfg<NB>::threads, 1)
+__global__ void __launch_bounds__(KvCfg<NB, BIAS>::threads, 1)
     grad_kv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_g,
                    const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, BandArgs a, KvShape sh,
                    const float2* __restrict__ stats, T* __restrict__ gk, T* __restrict__ gv, float* __restrict__ part,
                    float* __restrict__ diag) {
-    using C = KvCfg<NB>;
+    using C = KvCfg<NB, BIAS>;
     constexpr int kSlots = C::slots;
     extern __shared__ __align__(1024) unsigned char band_smem[];
     __shared__ __align__(8) uint64_t full[kSlots], empty[kSlots], raw, keys_full, s_full[2], e_full[2], p_full[2], done;
@@ -490,7 +493,8 @@ __global__ void __launch_bounds__(KvCfg<NB>::threads, 1)
     const uint32_t base = (smem_u32(band_smem) + 1023u) & ~1023u;
     const uint32_t ks = base, ring = base + 2 * NB * kTcBlock, stat_at = ring + kSlots * C::stage;
     const float4* stat_s = reinterpret_cast<const float4*>(band_smem + (stat_at - smem_u32(band_smem)));
-    float* table = reinterpret_cast<float*>(band_smem + (stat_at - smem_u32(band_smem)) + kSlots * C::stat);
+    float* diag_s = reinterpret_cast<float*>(band_smem + (stat_at - smem_u32(band_smem)) + kSlots * C::stat);
+    float* table = diag_s + (BIAS ? 8 * kDiagBuf : 0);
 
     const int items = sh.items(), nh = blockIdx.x / items, item = blockIdx.x - nh * items;
     const int n = nh / a.Hk, hk = nh - n * a.Hk;
@@ -668,7 +672,8 @@ __global__ void __launch_bounds__(KvCfg<NB>::threads, 1)
         Diagonals dg;
         int dg_head = -1;
         dg.M = a.M;
-        dg.rel31 = kw + 31 - start;
+        dg.rel0 = kw - start;
+        dg.buf = diag_s + warp * kDiagBuf;
         bool ok = true;
         int s = w;
         Step st_w = first_of(w);
@@ -886,7 +891,7 @@ cudaError_t launch(const BandArgs& a, const void* out, const float* lse, const v
     const int pack = a.G, tq = kTcRows / pack, blocks = (a.Lq + 2 * tq - 1) / (2 * tq);
     const long long dense = static_cast<long long>(a.Hq) * a.D;
     const size_t smem_q = QCfg<NB>::smem + (BIAS ? static_cast<size_t>(a.G) * kv.floats * sizeof(float) : 0),
-                 smem_kv = KvCfg<NB>::smem + (BIAS ? static_cast<size_t>(a.G) * kv.floats * sizeof(float) : 0);
+                 smem_kv = KvCfg<NB, BIAS>::smem + (BIAS ? static_cast<size_t>(a.G) * kv.floats * sizeof(float) : 0);
     cudaError_t e = allow_smem<grad_q_kernel<T, NB, BIAS, EXACT>>();
     if (e == cudaSuccess) e = allow_smem<grad_kv_kernel<T, NB, BIAS, EXACT>>();
     if (e == cudaSuccess && BIAS) e = cudaMemsetAsync(diag, 0, diag_bytes(a, kv), stream);
@@ -911,7 +916,7 @@ cudaError_t launch(const BandArgs& a, const void* out, const float* lse, const v
     grad_q_kernel<T, NB, BIAS, EXACT><<<static_cast<unsigned>(static_cast<long long>(a.N) * (a.Hq / pack) * blocks), QCfg<NB>::threads, smem_q, stream>>>(
         mq, mg, mk, mv, a, pack, tq, blocks, kv.floats, band_most_keys(a) <= kFewKeys, stats, static_cast<T*>(gq));
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    grad_kv_kernel<T, NB, BIAS, EXACT><<<static_cast<unsigned>(static_cast<long long>(a.N) * a.Hk * kv.items()), KvCfg<NB>::threads, smem_kv, stream>>>(
+    grad_kv_kernel<T, NB, BIAS, EXACT><<<static_cast<unsigned>(static_cast<long long>(a.N) * a.Hk * kv.items()), KvCfg<NB, BIAS>::threads, smem_kv, stream>>>(
         mq1, mg1, mk1, mv1, a, kv, stats, static_cast<T*>(gk), static_cast<T*>(gv), part, diag);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (kv.split()) {
