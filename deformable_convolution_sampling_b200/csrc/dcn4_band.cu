@@ -41,19 +41,20 @@ __global__ void __launch_bounds__(256) join_kernel(BandArgs a, int splits, BandP
     if (lane == 0) lse[r] = l == 0.f ? -INFINITY : m + logf(l);
 }
 
-// sums[z][h][rel] = the diagonal sums of head h, in a fixed order; a z-th of the CTAs a block.
-__global__ void __launch_bounds__(256) diag_sum_kernel(BandArgs a, int per, int each, const float* __restrict__ diag, float* __restrict__ sums) {
+// sums[z][h][rel] = the diagonal sums of head h, in a fixed order; a z-th of them a block.
+// 2^shift sums a CTA, `per` CTAs an image and key head.
+__global__ void __launch_bounds__(256) diag_sum_kernel(BandArgs a, int per, int shift, const float* __restrict__ diag, float* __restrict__ sums) {
     __shared__ float s_part[8][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.y, len = 2 * a.M + 1, rel = blockIdx.x * 32 + lane;
     const int hk = h / a.G, g = h - hk * a.G;
-    const long long ctas = static_cast<long long>(a.N) * per, c0 = ctas * blockIdx.z / gridDim.z, c1 = ctas * (blockIdx.z + 1) / gridDim.z;
+    const long long all = (static_cast<long long>(a.N) * per) << shift, e0 = all * blockIdx.z / gridDim.z, e1 = all * (blockIdx.z + 1) / gridDim.z;
     float s = 0.f;
     if (rel < len) {
-        // (CTA, sum) pairs, dealt to the warps
 #pragma unroll 8
-        for (long long e = c0 * each + warp; e < c1 * each; e += 8) {
-            const long long c = e / each, n = c / per, cta = (n * a.Hk + hk) * per + c - n * per;
-            s += diag[((cta * each + e - c * each) * a.G + g) * len + rel];
+        for (long long e = e0 + warp; e < e1; e += 8) {
+            const unsigned c = static_cast<unsigned>(e >> shift), n = c / per;  // N Hk per is a grid: 31 bits
+            const long long cta = (static_cast<long long>(n) * a.Hk + hk) * per + c - n * per;
+            s += diag[(((cta << shift) + (e & ((1 << shift) - 1))) * a.G + g) * len + rel];
         }
     }
     s_part[warp][lane] = s;
@@ -63,20 +64,26 @@ __global__ void __launch_bounds__(256) diag_sum_kernel(BandArgs a, int per, int 
     sums[(static_cast<long long>(blockIdx.z) * a.Hq + h) * len + rel] = s;
 }
 
-// gbias[b][h]: a warp sums the relative positions of its bucket.
+// gbias[b][h], b of a block's 64: head h's sums by relative position into shared memory,
+// then a warp sums those of its bucket.
 template <typename T>
 __global__ void __launch_bounds__(256) bucket_sum_kernel(BandArgs a, int parts, const float* __restrict__ sums, T* __restrict__ gbias) {
-    const int e = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31, len = 2 * a.M + 1;
-    if (e >= a.nb * a.Hq) return;
-    const int b = e / a.Hq, h = e - b * a.Hq;
-    float s = 0.f;
-    for (int r = lane; r < len; r += 32)
-        if (__ldg(a.buckets + r) == b) {
+    __shared__ float s_sum[2 * kBandMaxReach + 1];
+    const int h = blockIdx.x, len = 2 * a.M + 1, lane = threadIdx.x & 31;
+    for (int r = threadIdx.x; r < len; r += 256) {
+        float s = 0.f;
 #pragma unroll 8
-            for (int z = 0; z < parts; ++z) s += sums[(static_cast<long long>(z) * a.Hq + h) * len + r];
-        }
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) gbias[e] = from_f32<T>(s);
+        for (int z = 0; z < parts; ++z) s += sums[(static_cast<long long>(z) * a.Hq + h) * len + r];
+        s_sum[r] = s;
+    }
+    __syncthreads();
+    for (int b = blockIdx.y * 64 + (threadIdx.x >> 5); b < min(a.nb, static_cast<int>(blockIdx.y + 1) * 64); b += 8) {
+        float s = 0.f;
+        for (int r = lane; r < len; r += 32)
+            if (__ldg(a.buckets + r) == b) s += s_sum[r];
+        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane == 0) gbias[static_cast<long long>(b) * a.Hq + h] = from_f32<T>(s);
+    }
 }
 
 __global__ void __launch_bounds__(256) no_keys_kernel(float* __restrict__ lse, long long rows) {
@@ -111,11 +118,11 @@ size_t band_sum_bytes(const BandArgs& a) {
 
 cudaError_t launch_band_bias_sum(const BandArgs& a, int per, int each, const float* diag, float* sums, void* gbias,
                                  cudaStream_t stream) {
-    const int zs = sum_parts(a, per, each);
-    diag_sum_kernel<<<dim3((2 * a.M + 32) / 32, a.Hq, zs), 256, 0, stream>>>(a, per, each, diag, sums);
+    const int zs = sum_parts(a, per, each), shift = each == 1 ? 0 : 4;  // one sum a CTA, or sixteen
+    diag_sum_kernel<<<dim3((2 * a.M + 32) / 32, a.Hq, zs), 256, 0, stream>>>(a, per, shift, diag, sums);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const unsigned grid = static_cast<unsigned>((a.nb * a.Hq + 7) / 8);
+    const dim3 grid(a.Hq, (a.nb + 63) / 64);
     switch (a.dtype) {
         case 0: bucket_sum_kernel<float><<<grid, 256, 0, stream>>>(a, zs, sums, static_cast<float*>(gbias)); break;
         case 1: bucket_sum_kernel<__half><<<grid, 256, 0, stream>>>(a, zs, sums, static_cast<__half*>(gbias)); break;

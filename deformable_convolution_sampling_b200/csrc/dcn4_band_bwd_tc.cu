@@ -398,65 +398,53 @@ struct KvShape {
 
 // Diagonal sums.  All pairs of a diagonal of the score matrix share a relative
 // position, so the bias gradient is the sum of d along diagonals, then over the
-// diagonals of a bucket.  A warp's lanes hold keys; 32 queries at a time go through 32
-// rows of 33 floats of shared memory and come back by diagonals: lane k adds those of
-// key - query = k and, apart, of k - 32.  With the next 32 queries the latter go on as
-// the former, so that every 32 queries end in one store of 32 neighbouring relative
-// positions.  No atomics, one order.  (Handing the partial sums from lane to lane by
-// shuffles needs no shared memory, but is a chain of 32 of them: 900 cycles, not 250.)
-constexpr int kDiagBuf = 32 * 33;
+// diagonals of a bucket.  A warp's lanes hold keys; a chunk of 32 queries goes, in two
+// halves, through 32 rows of 17 floats of shared memory and comes back by diagonals:
+// lane k adds those of key - query = k and, apart, of k - 32, and each ends in one store
+// of 32 neighbouring relative positions.  A warp meets every second chunk of 32 queries at
+// most, so that no two of its stores meet: no atomics, one order.  (Handing partial
+// sums from lane to lane needs no shared memory, but is a chain of 32 shuffles: 900
+// cycles a chunk instead of 250.)
+constexpr int kDiagBuf = 32 * 17;
+constexpr int kDiagWarps = 16;  // sums a CTA leaves
 struct Diagonals {
     float* mine;    // this warp's sums, of relative position -M .. M (the ends: and beyond)
     float* buf;     // this warp's kDiagBuf floats
     int M, rel0;    // relative position of lane 0's key and query 0
-    int next;       // query the run goes on with; -1: no run
-    bool again;     // a run of this head has been stored already: add
-    float carry, below, above;
+    float below, above;
     __device__ __forceinline__ void start(float* to) {
         mine = to;
-        next = -1;
-        again = false;
-        carry = below = above = 0.f;
+        below = above = 0.f;
     }
-    __device__ __forceinline__ void store(int i, int lane, float v) {
-        const int rel = rel0 - i + lane;
+    __device__ __forceinline__ void store(int rel, float v) {
         if (rel <= -M) below += v;
         else if (rel >= M) above += v;
-        else {
-            float* to = mine + rel + M;
-            *to = again ? *to + v : v;
-        }
-    }
-    __device__ __forceinline__ void flush(int lane) {
-        if (next < 0) return;
-        store(next, lane, carry);
-        __syncwarp();
-        again = true;
-        next = -1;
-        carry = 0.f;
+        else mine[rel + M] = v;
     }
     __device__ __forceinline__ void chunk(int i, int lane, const uint32_t (&d)[32]) {
-        if (i != next) flush(lane);
+        float a[2] = {}, b[2] = {};  // of the halves: key - query of the half = lane, and lane - 32
 #pragma unroll
-        for (int e = 0; e < 32; ++e) buf[lane * 33 + e] = __uint_as_float(d[e]);
-        __syncwarp();
-        // row r, column r - lane or, where that is below 0, r - lane + 32
-        float a[2] = {carry, 0.f}, b[2] = {};
-        const float *pa = buf - lane, *pb = pa + 32;
+        for (int z = 0; z < 2; ++z) {
 #pragma unroll
-        for (int r = 0; r < 32; ++r) {
-            const bool on = r >= lane;
-            const float v = (on ? pa : pb)[34 * r];
-            if (on) a[r & 1] += v;
-            else b[r & 1] += v;
+            for (int e = 0; e < 16; ++e) buf[lane * 17 + e] = __uint_as_float(d[16 * z + e]);
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int r = (lane + e) & 31;
+                const float v = buf[r * 17 + e];
+                if (r >= e) a[z] += v;
+                else b[z] += v;
+            }
+            __syncwarp();
         }
-        __syncwarp();
-        store(i, lane, a[0] + a[1]);
-        carry = b[0] + b[1];
-        next = i + 32;
+        // the second half's queries are 16 later
+        const float a1 = __shfl_xor_sync(0xffffffffu, a[1], 16), b1 = __shfl_xor_sync(0xffffffffu, b[1], 16);
+        if (lane < 16) a[0] += a1, b[0] += b1;
+        else b[0] += a1;
+        store(rel0 - i + lane, a[0]);
+        store(rel0 - i + lane - 32, b[0]);  // (lane 0's is an empty sum)
     }
     __device__ __forceinline__ void finish(int lane) {
-        flush(lane);
         for (int o = 16; o; o >>= 1) {
             below += __shfl_xor_sync(0xffffffffu, below, o);
             above += __shfl_xor_sync(0xffffffffu, above, o);
@@ -468,13 +456,18 @@ struct Diagonals {
     }
 };
 
+// Scores of 128 keys x 64 queries of two steps are in work at a time; each has two
+// warpgroups, a chunk of 32 queries each (the probabilities need no maximum, so chunks
+// are independent; one warpgroup a step left the SM's schedulers two warps to hide
+// latencies with).
+constexpr int kKvProducer = 16, kKvMma = 17;
 template <int NB, bool BIAS>
 struct KvCfg {
     static constexpr int slots = NB == 1 ? 6 : BIAS ? 3 : 4;
-    static constexpr int threads = 320;
+    static constexpr int threads = (kKvMma + 1) * 32;
     static constexpr int stage = 2 * NB * kTileBlock;      // Q, G
     static constexpr int stat = kTile * sizeof(float2);
-    static constexpr size_t smem = 1024 + 2 * NB * kTcBlock + slots * (stage + stat) + (BIAS ? 8 * kDiagBuf * sizeof(float) : 0);
+    static constexpr size_t smem = 1024 + 2 * NB * kTcBlock + slots * (stage + stat) + (BIAS ? kDiagWarps * kDiagBuf * sizeof(float) : 0);
 };
 
 template <typename T, int NB, bool BIAS, bool EXACT>
@@ -494,7 +487,7 @@ __global__ void __launch_bounds__(KvCfg<NB, BIAS>::threads, 1)
     const uint32_t ks = base, ring = base + 2 * NB * kTcBlock, stat_at = ring + kSlots * C::stage;
     const float4* stat_s = reinterpret_cast<const float4*>(band_smem + (stat_at - smem_u32(band_smem)));
     float* diag_s = reinterpret_cast<float*>(band_smem + (stat_at - smem_u32(band_smem)) + kSlots * C::stat);
-    float* table = diag_s + (BIAS ? 8 * kDiagBuf : 0);
+    float* table = diag_s + (BIAS ? kDiagWarps * kDiagBuf : 0);
 
     const int items = sh.items(), nh = blockIdx.x / items, item = blockIdx.x - nh * items;
     const int n = nh / a.Hk, hk = nh - n * a.Hk;
@@ -523,12 +516,12 @@ __global__ void __launch_bounds__(KvCfg<NB, BIAS>::threads, 1)
         for (int w = 0; w < 2; ++w) {
             mbar_init(smem_u32(&s_full[w]), 1);
             mbar_init(smem_u32(&e_full[w]), 1);
-            mbar_init(smem_u32(&p_full[w]), 4);
+            mbar_init(smem_u32(&p_full[w]), 8);
         }
         s_abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == kMma) {
+    if (warp == kKvMma) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&taddr_s)), "r"(kTmem));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
@@ -558,7 +551,7 @@ __global__ void __launch_bounds__(KvCfg<NB, BIAS>::threads, 1)
         cb = (min(ihi, i + kTile) - i + kTcChunk - 1) >> 5;
     };
 
-    if (warp == kProducer) {
+    if (warp == kKvProducer) {
         if (cnt && elect_one()) {
             mbar_expect_tx(smem_u32(&keys_full), 2 * NB * kTcBlock);
             for (int c = 0; c < NB; ++c) {
@@ -593,7 +586,7 @@ __global__ void __launch_bounds__(KvCfg<NB, BIAS>::threads, 1)
                 if (elect_one()) mbar_arrive(smem_u32(&full[s]));
             }
         }
-    } else if (warp == kMma) {
+    } else if (warp == kKvMma) {
         if (cnt) {
             const int steps = (a.D + 15) / 16;
             const uint32_t id_s = umma_idesc<T>(kTcRows, 0, 0, 0), id_o = umma_idesc<T>(kTcRows, steps * 16, 0, 1);
@@ -658,10 +651,10 @@ __global__ void __launch_bounds__(KvCfg<NB, BIAS>::threads, 1)
             if (!ok && lane == 0) mbar_wait_or(smem_u32(&done), 0u, &never);
         }
         __syncwarp();
-    } else if (warp < kProducer) {
-        const int w = warp >> 2, row = tid & 127, j = k0 + row;
+    } else {
+        const int w = (warp >> 2) & 1, c = warp >> 3, row = tid & 127, j = k0 + row;  // steps of parity w, their chunk c
         const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        const uint32_t at_s = lane_base + w * 128;
+        const uint32_t at_s = lane_base + w * 128 + c * kTcChunk;
         const bool warp_live = k0 + (warp & 3) * 32 < klen;
         // queries that see this key
         const int vlo = j - a.right - start, vhi = j >= klen ? 0 : j < a.sinks ? qlen : min(qlen, j + a.left - start + 1);
@@ -679,11 +672,11 @@ __global__ void __launch_bounds__(KvCfg<NB, BIAS>::threads, 1)
         Step st_w = first_of(w);
         for (int t = w; t < cnt; t += 2) {
             int ca, cb;
-            const int g = st_w.g, i = (q0 + st_w.r) * kTile;
+            const int g = st_w.g, i = (q0 + st_w.r) * kTile, ic = i + c * kTcChunk;
             st_w.next();
             if (BIAS && warp_live && g != dg_head) {
                 if (dg_head >= 0) dg.finish(lane);
-                dg.start(diag + ((static_cast<long long>(blockIdx.x) * 8 + warp) * a.G + g) * (2 * a.M + 1));
+                dg.start(diag + ((static_cast<long long>(blockIdx.x) * kDiagWarps + warp) * a.G + g) * (2 * a.M + 1));
                 dg_head = g;
             }
             chunks(i, ca, cb);
@@ -691,104 +684,103 @@ __global__ void __launch_bounds__(KvCfg<NB, BIAS>::threads, 1)
             ok = warp_wait(&full[s], (t / kSlots) & 1, abort) && warp_wait(&s_full[w], (t >> 1) & 1, abort);
             if (!ok) break;
             tc_fence_after();
-            if (warp_live) {
-                const float4* st = stat_s + s * (C::stat / 16);
-                const float* tab = table + g * sh.floats + a.M + kTableExtra + j - start;
-                uint32_t px[kChunks][32];
-#pragma unroll
-                for (int c = 0; c < kChunks; ++c)
-                    if (c >= ca && c < cb) tmem_ld32_async(at_s + c * kTcChunk, px[c]);
-#pragma unroll
-                for (int c = 0; c < kChunks; ++c) {
-                    if (c < ca || c >= cb) continue;
-                    uint32_t (&x)[32] = px[c];
-                    const int ic = i + c * kTcChunk;
-                    tmem_ld_wait(x);
+            uint32_t x[32], y[32];
+            const bool on = warp_live && c >= ca && c < cb;
+            if (on) {
+                const float4* st = stat_s + s * (C::stat / 16) + c * (kTcChunk / 2);  // lse, delta of two queries each
+                tmem_ld32_async(at_s, x);
+                tmem_ld_wait(x);
+                if (BIAS) {
                     // relative positions k0 - (start + ic + 31) ... k1 - 1 - (start + ic)
                     const int side = k0 - (start + ic + kTcChunk - 1) >= a.M ? 1 : k1 - 1 - (start + ic) <= -a.M ? -1 : 0;
-                    const float bb = BIAS ? table[g * sh.floats + (side > 0 ? sh.floats - 1 : 0)] : 0.f;
+                    const float* tab = table + g * sh.floats;
+                    if (side) {
+                        const float bb = tab[side > 0 ? sh.floats - 1 : 0];
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const float4 u = st[(c * kTcChunk + e) >> 1];  // lse, delta of two queries
-                        if (BIAS) {
-                            x[e] = __float_as_uint(ex2((fmaf(__uint_as_float(x[e]), sc, side ? bb : tab[-(ic + e)]) - u.x) * kLog2e));
-                            x[e + 1] = __float_as_uint(ex2((fmaf(__uint_as_float(x[e + 1]), sc, side ? bb : tab[-(ic + e + 1)]) - u.z) * kLog2e));
-                        } else {
-                            x[e] = __float_as_uint(ex2(fmaf(__uint_as_float(x[e]), sc, -u.x)));
-                            x[e + 1] = __float_as_uint(ex2(fmaf(__uint_as_float(x[e + 1]), sc, -u.z)));
-                        }
+                        for (int e = 0; e < 32; e += 2) fma2(x[e], x[e + 1], sc, bb);
+                    } else {
+                        tab += a.M + kTableExtra + j - start - ic;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(fmaf(__uint_as_float(x[e]), sc, tab[-e]));
                     }
                 }
-                if (!(ok = warp_wait(&e_full[w], (t >> 1) & 1, abort))) break;
-                tc_fence_after();
 #pragma unroll
-                for (int c = 0; c < kChunks; ++c) {
-                    if (c < ca || c >= cb) continue;
-                    uint32_t (&x)[32] = px[c];
-                    uint32_t y[32];
-                    const int ic = i + c * kTcChunk;
-                    tmem_ld32_async(at_s + 64 + c * kTcChunk, y);
-                    tmem_ld_wait(y);
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const float4 u = st[(c * kTcChunk + e) >> 1];
-                        y[e] = __float_as_uint(__uint_as_float(x[e]) * (__uint_as_float(y[e]) - u.y));
-                        y[e + 1] = __float_as_uint(__uint_as_float(x[e + 1]) * (__uint_as_float(y[e + 1]) - u.w));
-                    }
-                    if (ic < all_lo || ic > all_hi) {
-                        const uint32_t see = low_bits(vhi - ic) & ~low_bits(vlo - ic);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!(see & (1u << e))) x[e] = y[e] = 0u;
-                    }
-                    uint32_t p[16], d[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        p[e] = pack2<T>(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
-                        d[e] = pack2<T>(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1]));
-                    }
-                    tmem_st16(at_s + c * kTcChunk, p);
-                    tmem_st16(at_s + 64 + c * kTcChunk, d);
-                    if (EXACT) {
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            p[e] = pack_low<T>(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]), p[e]);
-                            d[e] = pack_low<T>(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1]), d[e]);
-                        }
-                        tmem_st16(at_s + c * kTcChunk + kLow, p);
-                        tmem_st16(at_s + 64 + c * kTcChunk + kLow, d);
-                    }
+                for (int e = 0; e < 32; e += 2) {
+                    const float4 u = st[e >> 1];
                     if (BIAS) {
-                        const bool above = kw - (start + ic + kTcChunk - 1) >= a.M, below = kw + 31 - (start + ic) <= -a.M;
-                        if (above || below) {
-                            float2 sum[2] = {};
-#pragma unroll
-                            for (int e = 0; e < 32; e += 2) add2(sum[(e >> 1) & 1], y[e], y[e + 1]);
-                            (above ? dg.above : dg.below) += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                        } else {
-                            dg.chunk(ic, lane, y);
-                        }
+                        x[e] = __float_as_uint(ex2((__uint_as_float(x[e]) - u.x) * kLog2e));
+                        x[e + 1] = __float_as_uint(ex2((__uint_as_float(x[e + 1]) - u.z) * kLog2e));
+                    } else {
+                        x[e] = __float_as_uint(ex2(fmaf(__uint_as_float(x[e]), sc, -u.x)));
+                        x[e + 1] = __float_as_uint(ex2(fmaf(__uint_as_float(x[e + 1]), sc, -u.z)));
                     }
+                }
+            }
+            if (!(ok = warp_wait(&e_full[w], (t >> 1) & 1, abort))) break;
+            tc_fence_after();
+            if (on) {
+                const float4* st = stat_s + s * (C::stat / 16) + c * (kTcChunk / 2);
+                tmem_ld32_async(at_s + 64, y);
+                tmem_ld_wait(y);
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    const float4 u = st[e >> 1];
+                    y[e] = __float_as_uint(__uint_as_float(x[e]) * (__uint_as_float(y[e]) - u.y));
+                    y[e + 1] = __float_as_uint(__uint_as_float(x[e + 1]) * (__uint_as_float(y[e + 1]) - u.w));
+                }
+                if (ic < all_lo || ic > all_hi) {
+                    const uint32_t see = low_bits(vhi - ic) & ~low_bits(vlo - ic);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (!(see & (1u << e))) x[e] = y[e] = 0u;
+                }
+                uint32_t p[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) p[e] = pack2<T>(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+                tmem_st16(at_s, p);
+                if (EXACT) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) p[e] = pack_low<T>(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]), p[e]);
+                    tmem_st16(at_s + kLow, p);
+                }
+#pragma unroll
+                for (int e = 0; e < 16; ++e) p[e] = pack2<T>(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1]));
+                tmem_st16(at_s + 64, p);
+                if (EXACT) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) p[e] = pack_low<T>(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1]), p[e]);
+                    tmem_st16(at_s + 64 + kLow, p);
                 }
                 tmem_st_wait();
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&p_full[w]));
+            if (BIAS && on) {  // under the products that p and d go into
+                const bool above = kw - (start + ic + kTcChunk - 1) >= a.M, below = kw + 31 - (start + ic) <= -a.M;
+                if (above || below) {
+                    float2 sum[2] = {};
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) add2(sum[(e >> 1) & 1], y[e], y[e + 1]);
+                    (above ? dg.above : dg.below) += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                } else {
+                    dg.chunk(ic, lane, y);
+                }
+            }
             s += 2;
             if (s >= kSlots) s -= kSlots;
         }
         if (BIAS && dg_head >= 0) dg.finish(lane);
         if (ok && cnt) ok = warp_wait(&done, 0u, abort);
         tc_fence_after();
-        // the first four warps store gv, the others gk
+        // parity 0 stores gv, 1 gk, each chunk's warps every second 32 columns
         const bool row_here = parts > 1 || j < a.Lk;
         const uint32_t at_o = lane_base + 256 + w * 64 * NB;
         const float f = w ? a.scale : 1.f;
         const bool zero = !cnt || j >= klen;
         T* to = (w ? gk : gv) + ((static_cast<long long>(n) * a.Lk + j) * a.Hk + hk) * a.D;
         float* po = part + ((static_cast<long long>(blockIdx.x) * 2 + w) * kTcRows + row) * a.D;
-        for (int d = 0; d < a.D && ok; d += 32) {
+        for (int d = 32 * c; d < a.D && ok; d += 64) {
             uint32_t x[32];
             if (cnt) {
                 tmem_ld32_async(at_o + d, x);
@@ -815,7 +807,7 @@ __global__ void __launch_bounds__(KvCfg<NB, BIAS>::threads, 1)
     tc_fence_before();
     __syncthreads();
     if (tid == 0 && *abort) atomicOr(&g_band_bwd_status, 1u);
-    if (warp == kMma) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmem));
+    if (warp == kKvMma) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmem));
 }
 
 // Sums the parts of tiles that were split, in order: a thread per four entries.
@@ -875,7 +867,7 @@ size_t part_bytes(const BandArgs& a, const KvShape& s) {
     return s.split() ? up256(static_cast<size_t>(a.N) * a.Hk * s.items() * 2 * kTcRows * a.D * sizeof(float)) : 0;
 }
 size_t diag_bytes(const BandArgs& a, const KvShape& s) {
-    return a.nb ? up256(static_cast<size_t>(a.N) * a.Hq * s.items() * 8 * (2 * a.M + 1) * sizeof(float)) : 0;
+    return a.nb ? up256(static_cast<size_t>(a.N) * a.Hq * s.items() * kDiagWarps * (2 * a.M + 1) * sizeof(float)) : 0;
 }
 size_t sums_bytes(const BandArgs& a) { return a.nb ? up256(band_sum_bytes(a)) : 0; }
 
@@ -925,7 +917,7 @@ cudaError_t launch(const BandArgs& a, const void* out, const float* lse, const v
         kv_join_kernel<T><<<static_cast<unsigned>((n4 + 255) / 256), 256, 0, stream>>>(a, kv, tiles, part, static_cast<T*>(gk), static_cast<T*>(gv));
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
-    return BIAS && gbias ? launch_band_bias_sum(a, kv.items(), 8, diag, sums, gbias, stream) : cudaSuccess;
+    return BIAS && gbias ? launch_band_bias_sum(a, kv.items(), kDiagWarps, diag, sums, gbias, stream) : cudaSuccess;
 }
 
 }  // namespace
