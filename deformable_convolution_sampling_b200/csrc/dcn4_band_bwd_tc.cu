@@ -28,7 +28,12 @@ namespace {
 
 using namespace tc;
 
-constexpr int kProducer = 8, kMma = 9;
+// Warps 0-15 form p and d, 16 loads, those from 17 on issue MMAs.  Two tiles of scores
+// are in work at a time, and each has two warpgroups, a chunk of 32 columns each: the
+// probabilities need no maximum, so chunks are independent (with one warpgroup a tile
+// the SM's schedulers had two warps each to hide latencies with, and grad_kv of a
+// 785 x 785 map with a bias took 124 us instead of 93).
+constexpr int kProducer = 16, kMma = 17;
 constexpr int kTile = 64, kChunks = kTile / kTcChunk;  // keys or queries of a streamed tile
 constexpr int kTileBlock = kTile * 128;                // bytes of 64 of its columns
 constexpr int kTableExtra = 160;                       // as in the forward: a chunk and a tile's rows past M
@@ -94,23 +99,24 @@ __global__ void __launch_bounds__(256) stats_kernel(BandArgs a, int lanes, const
 // ---------------------------------------------------------------------------
 // grad_q
 // ---------------------------------------------------------------------------
-template <int NB>
+template <int NB, bool BIAS>
 struct QCfg {
-    static constexpr int slots = NB == 1 ? 4 : 2;
-    static constexpr int threads = 352;              // 8 softmax warps, the loads, an issuing warp a half
+    static constexpr int slots = NB == 1 ? 6 : BIAS ? 2 : 3;
+    static constexpr int threads = (kMma + 2) * 32;  // an issuing warp a half
     static constexpr size_t smem = 1024 + 4 * NB * kTcBlock + slots * 2 * NB * kTileBlock;
 };
 
 template <typename T, int NB, bool BIAS, bool EXACT>
-__global__ void __launch_bounds__(QCfg<NB>::threads, 1)
+__global__ void __launch_bounds__(QCfg<NB, BIAS>::threads, 1)
     grad_q_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_g,
                   const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, BandArgs a, int pack,
                   int tq, int blocks, int floats, int twice, float2* __restrict__ stats, T* __restrict__ gq) {
-    constexpr int kSlots = QCfg<NB>::slots;
+    constexpr int kSlots = QCfg<NB, BIAS>::slots;
     extern __shared__ __align__(1024) unsigned char band_smem[];
     __shared__ __align__(8) uint64_t full[kSlots], empty[kSlots], raw, rows_full, s_full[2], e_full[2], p_full[2], o_done[2];
     __shared__ uint32_t taddr_s;
     __shared__ int s_abort;
+    __shared__ float s_off[2][kTcRows];  // the second chunk's part of a row's sum
     const int tid = threadIdx.x, warp = static_cast<int>(uniform(tid >> 5)), lane = tid & 31;
     const uint32_t base = (smem_u32(band_smem) + 1023u) & ~1023u;
     const uint32_t qs = base, ring = base + 4 * NB * kTcBlock;  // Q, G of the first half, then of the second
@@ -134,7 +140,7 @@ __global__ void __launch_bounds__(QCfg<NB>::threads, 1)
         for (int w = 0; w < 2; ++w) {
             mbar_init(smem_u32(&s_full[w]), 1);
             mbar_init(smem_u32(&e_full[w]), 1);
-            mbar_init(smem_u32(&p_full[w]), 4);
+            mbar_init(smem_u32(&p_full[w]), 8);
             mbar_init(smem_u32(&o_done[w]), 1);
         }
         s_abort = 0;
@@ -144,7 +150,7 @@ __global__ void __launch_bounds__(QCfg<NB>::threads, 1)
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&taddr_s)), "r"(kTmem));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
-    if (BIAS) fill_table<T>(a, table, floats, h0, pack, QCfg<NB>::threads);
+    if (BIAS) fill_table<T>(a, table, floats, h0, pack, QCfg<NB, BIAS>::threads);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -260,8 +266,8 @@ __global__ void __launch_bounds__(QCfg<NB>::threads, 1)
         }
         __syncwarp();
     } else if (warp < kProducer) {
-        const int w = warp >> 2, row = tid & 127;
-        const uint32_t at_s = tmem + w * 256 + (static_cast<uint32_t>((warp & 3) * 32) << 16), at_o = at_s + 128;
+        const int w = (warp >> 2) & 1, c = warp >> 3, row = tid & 127;  // a half's rows, the chunk c of its columns
+        const uint32_t at_h = tmem + w * 256 + (static_cast<uint32_t>((warp & 3) * 32) << 16), at_s = at_h + c * kTcChunk, at_o = at_h + 128;
         const int ql = row / pack, g = row - ql * pack, i = i0 + w * tq + ql;
         const bool live = ql < tq && i < qlen;
         const bool warp_live = __any_sync(0xffffffffu, live);
@@ -275,89 +281,97 @@ __global__ void __launch_bounds__(QCfg<NB>::threads, 1)
         float delta = twice ? 0.f : st.y, off = 0.f;  // off: the sum of the row's d, or in the first pass of p E
         const float sc = BIAS ? a.scale : a.scale * kLog2e;
         const float* tab = table + g * floats + a.M + kTableExtra - pos;
+        // the row's sum over both chunks, for the first chunk's thread (and, with `back`, the second's)
+        auto both = [&](float v, bool back) {
+            if (c) s_off[w][row] = v;
+            asm volatile("bar.sync %0, 256;" ::"r"(1 + w) : "memory");
+            if (!c) v += s_off[w][row];
+            if (back) {
+                if (!c) s_off[w][row] = v;
+                asm volatile("bar.sync %0, 256;" ::"r"(1 + w) : "memory");
+                v = s_off[w][row];
+            }
+            return v;
+        };
         int nw = 0, ca, cb;
         bool ok = true;
-        for (int t = 0; t < cnt; ++t) {
+        for (int t = 0; t < cnt && ok; ++t) {
             if (t == first && twice) {
-                delta = off;
+                delta = both(off, true);
                 off = 0.f;
             }
             if (!active(w, t, ca, cb)) continue;
-            const int j0 = tile_at(t);
-            if (!(ok = warp_wait(&s_full[w], nw & 1, abort))) break;
-            tc_fence_after();
-            if (warp_live) {
-                uint32_t x[kChunks][32];
-#pragma unroll
-                for (int c = 0; c < kChunks; ++c)
-                    if (c >= ca && c < cb) tmem_ld32_async(at_s + c * kTcChunk, x[c]);
-#pragma unroll
-                for (int c = 0; c < kChunks; ++c) {
-                    if (c < ca || c >= cb) continue;
-                    const int j = j0 + c * kTcChunk;
-                    tmem_ld_wait(x[c]);
-                    if (BIAS) {
-                        const int side = j - phi >= a.M ? 1 : j + kTcChunk - 1 - plo <= -a.M ? -1 : 0;
+            const int j = tile_at(t) + c * kTcChunk;
+            const bool on = warp_live && c >= ca && c < cb;
+            uint32_t x[32];
+            ok = warp_wait(&s_full[w], nw & 1, abort);
+            if (ok && on) {
+                tc_fence_after();
+                tmem_ld32_async(at_s, x);
+                tmem_ld_wait(x);
+                if (BIAS) {
+                    const int side = j - phi >= a.M ? 1 : j + kTcChunk - 1 - plo <= -a.M ? -1 : 0;
+                    if (side) {
                         const float bb = table[g * floats + (side > 0 ? floats - 1 : 0)];
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            x[c][e] = __float_as_uint(fmaf(__uint_as_float(x[c][e]), sc, side ? bb : tab[j + e]));
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) sub_mul2(x[c][e], x[c][e + 1], st.x, kLog2e);
+                        for (int e = 0; e < 32; e += 2) fma2(x[e], x[e + 1], sc, bb);
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) fma2(x[c][e], x[c][e + 1], sc, -st.x);
+                        for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(fmaf(__uint_as_float(x[e]), sc, tab[j + e]));
                     }
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) x[c][e] = __float_as_uint(ex2(__uint_as_float(x[c][e])));
-                }
-                if (!(ok = warp_wait(&e_full[w], nw & 1, abort))) break;
-                tc_fence_after();
+                    for (int e = 0; e < 32; e += 2) sub_mul2(x[e], x[e + 1], st.x, kLog2e);
+                } else {
 #pragma unroll
-                for (int c = 0; c < kChunks; ++c) {
-                    if (c < ca || c >= cb) continue;
-                    const int j = j0 + c * kTcChunk;
-                    uint32_t y[32];
-                    tmem_ld32_async(at_s + 64 + c * kTcChunk, y);
-                    tmem_ld_wait(y);
+                    for (int e = 0; e < 32; e += 2) fma2(x[e], x[e + 1], sc, -st.x);
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(ex2(__uint_as_float(x[e])));
+            }
+            ok = ok && warp_wait(&e_full[w], nw & 1, abort);
+            if (ok && on) {
+                tc_fence_after();
+                uint32_t y[32];
+                tmem_ld32_async(at_s + 64, y);
+                tmem_ld_wait(y);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * (__uint_as_float(y[e]) - delta));
+                if (j < all_lo || j > all_hi) {
+                    const uint32_t see = (low_bits(jhi - j) & ~low_bits(jlo - j)) | low_bits(jsink - j);
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
-                        x[c][e] = __float_as_uint(__uint_as_float(x[c][e]) * (__uint_as_float(y[e]) - delta));
-                    if (j < all_lo || j > all_hi) {
-                        const uint32_t see = (low_bits(jhi - j) & ~low_bits(jlo - j)) | low_bits(jsink - j);
+                        if (!(see & (1u << e))) x[e] = 0u;
+                }
+                float2 sum[2] = {};
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!(see & (1u << e))) x[c][e] = 0u;
-                    }
-                    float2 sum[2] = {};
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) add2(sum[(e >> 1) & 1], x[c][e], x[c][e + 1]);
-                    off += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                    if (t < first) continue;
+                for (int e = 0; e < 32; e += 2) add2(sum[(e >> 1) & 1], x[e], x[e + 1]);
+                off += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                if (t >= first) {
                     uint32_t p[16];
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) p[e >> 1] = pack2<T>(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
-                    tmem_st16(at_s + c * kTcChunk, p);
+                    for (int e = 0; e < 16; ++e) p[e] = pack2<T>(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+                    tmem_st16(at_s, p);
                     if (EXACT) {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) p[e] = pack_low<T>(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1]), p[e]);
-                        tmem_st16(at_s + c * kTcChunk + kLow, p);
+                        for (int e = 0; e < 16; ++e) p[e] = pack_low<T>(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]), p[e]);
+                        tmem_st16(at_s + kLow, p);
                     }
+                    tmem_st_wait();
                 }
-                tmem_st_wait();
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&p_full[w]));
             ++nw;
         }
-        if (ok && live) stat->y = delta + off;
+        off = both(off, false);
+        if (ok && live && !c) stat->y = delta + off;
         if (ok && cnt) ok = warp_wait(&o_done[w], 0u, abort);
         tc_fence_after();
         const bool rows_here = ql < tq && i < a.Lq;
         if (ok && __any_sync(0xffffffffu, rows_here)) {
             T* to = gq + ((static_cast<long long>(n) * a.Lq + i) * a.Hq + h0 + g) * a.D;
-            for (int d = 0; d < a.D; d += 32) {
+            for (int d = 32 * c; d < a.D; d += 64) {
                 uint32_t x[32];
                 if (nw) {
                     tmem_ld32_async(at_o + d, x);
@@ -456,15 +470,10 @@ struct Diagonals {
     }
 };
 
-// Scores of 128 keys x 64 queries of two steps are in work at a time; each has two
-// warpgroups, a chunk of 32 queries each (the probabilities need no maximum, so chunks
-// are independent; one warpgroup a step left the SM's schedulers two warps to hide
-// latencies with).
-constexpr int kKvProducer = 16, kKvMma = 17;
 template <int NB, bool BIAS>
 struct KvCfg {
     static constexpr int slots = NB == 1 ? 6 : BIAS ? 3 : 4;
-    static constexpr int threads = (kKvMma + 1) * 32;
+    static constexpr int threads = (kMma + 1) * 32;
     static constexpr int stage = 2 * NB * kTileBlock;      // Q, G
     static constexpr int stat = kTile * sizeof(float2);
     static constexpr size_t smem = 1024 + 2 * NB * kTcBlock + slots * (stage + stat) + (BIAS ? kDiagWarps * kDiagBuf * sizeof(float) : 0);
@@ -521,7 +530,7 @@ __global__ void __launch_bounds__(KvCfg<NB, BIAS>::threads, 1)
         s_abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == kKvMma) {
+    if (warp == kMma) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&taddr_s)), "r"(kTmem));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
@@ -551,7 +560,7 @@ __global__ void __launch_bounds__(KvCfg<NB, BIAS>::threads, 1)
         cb = (min(ihi, i + kTile) - i + kTcChunk - 1) >> 5;
     };
 
-    if (warp == kKvProducer) {
+    if (warp == kProducer) {
         if (cnt && elect_one()) {
             mbar_expect_tx(smem_u32(&keys_full), 2 * NB * kTcBlock);
             for (int c = 0; c < NB; ++c) {
@@ -586,7 +595,7 @@ __global__ void __launch_bounds__(KvCfg<NB, BIAS>::threads, 1)
                 if (elect_one()) mbar_arrive(smem_u32(&full[s]));
             }
         }
-    } else if (warp == kKvMma) {
+    } else if (warp == kMma) {
         if (cnt) {
             const int steps = (a.D + 15) / 16;
             const uint32_t id_s = umma_idesc<T>(kTcRows, 0, 0, 0), id_o = umma_idesc<T>(kTcRows, steps * 16, 0, 1);
@@ -807,7 +816,7 @@ __global__ void __launch_bounds__(KvCfg<NB, BIAS>::threads, 1)
     tc_fence_before();
     __syncthreads();
     if (tid == 0 && *abort) atomicOr(&g_band_bwd_status, 1u);
-    if (warp == kKvMma) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmem));
+    if (warp == kMma) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmem));
 }
 
 // Sums the parts of tiles that were split, in order: a thread per four entries.
@@ -882,7 +891,7 @@ cudaError_t launch(const BandArgs& a, const void* out, const float* lse, const v
     float* sums = reinterpret_cast<float*>(at += diag_bytes(a, kv));
     const int pack = a.G, tq = kTcRows / pack, blocks = (a.Lq + 2 * tq - 1) / (2 * tq);
     const long long dense = static_cast<long long>(a.Hq) * a.D;
-    const size_t smem_q = QCfg<NB>::smem + (BIAS ? static_cast<size_t>(a.G) * kv.floats * sizeof(float) : 0),
+    const size_t smem_q = QCfg<NB, BIAS>::smem + (BIAS ? static_cast<size_t>(a.G) * kv.floats * sizeof(float) : 0),
                  smem_kv = KvCfg<NB, BIAS>::smem + (BIAS ? static_cast<size_t>(a.G) * kv.floats * sizeof(float) : 0);
     cudaError_t e = allow_smem<grad_q_kernel<T, NB, BIAS, EXACT>>();
     if (e == cudaSuccess) e = allow_smem<grad_kv_kernel<T, NB, BIAS, EXACT>>();
@@ -905,7 +914,7 @@ cudaError_t launch(const BandArgs& a, const void* out, const float* lse, const v
     stats_kernel<T><<<static_cast<unsigned>(row_blocks), 256, 0, stream>>>(a, lanes, static_cast<const T*>(out), lse,
                                                                                       static_cast<const T*>(gout), stats);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    grad_q_kernel<T, NB, BIAS, EXACT><<<static_cast<unsigned>(static_cast<long long>(a.N) * (a.Hq / pack) * blocks), QCfg<NB>::threads, smem_q, stream>>>(
+    grad_q_kernel<T, NB, BIAS, EXACT><<<static_cast<unsigned>(static_cast<long long>(a.N) * (a.Hq / pack) * blocks), QCfg<NB, BIAS>::threads, smem_q, stream>>>(
         mq, mg, mk, mv, a, pack, tq, blocks, kv.floats, band_most_keys(a) <= kFewKeys, stats, static_cast<T*>(gq));
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     grad_kv_kernel<T, NB, BIAS, EXACT><<<static_cast<unsigned>(static_cast<long long>(a.N) * a.Hk * kv.items()), KvCfg<NB, BIAS>::threads, smem_kv, stream>>>(
