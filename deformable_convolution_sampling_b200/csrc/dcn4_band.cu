@@ -9,28 +9,49 @@ namespace dcn4 {
 namespace {
 
 // out = (sum_s o_s e^(m_s - m)) / (sum_s l_s e^(m_s - m)), lse = m + log of that
-// sum: a warp per row, a lane per entry.
+// sum: a warp per row.
 template <typename T>
 __global__ void __launch_bounds__(256) join_kernel(BandArgs a, int splits, BandPart part, T* __restrict__ out,
                                                    float* __restrict__ lse, long long rows) {
     const long long r = blockIdx.x * 8ll + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     if (r >= rows) return;
+    // a lane per part for the factors, a lane per entry for the sums; sixteen parts' loads go out before
+    // anything waits for them (one batch mostly: the kernel is a launch and two latencies)
+    constexpr int U = 16;
     const float2* ml = part.ml + r * splits;
-    float m = -INFINITY;
-    for (int s = 0; s < splits; ++s) m = fmaxf(m, ml[s].x);
+    const float* po = part.o + r * splits * a.D + lane;
+    float x[U][4];
+    auto fetch = [&](int s) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                x[u][c] = s + u < splits && lane + 32 * c < a.D ? __ldg(po + static_cast<long long>(s + u) * a.D + 32 * c) : 0.f;
+    };
+    fetch(0);
+    float2 v = lane < splits ? __ldg(ml + lane) : make_float2(-INFINITY, 0.f);
+    float m = v.x;
+    for (int s = 32 + lane; s < splits; s += 32) m = fmaxf(m, __ldg(ml + s).x);
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float ref = m == -INFINITY ? 0.f : m;
     float l = 0.f, o[4] = {};
-    const float* po = part.o + r * splits * a.D;
-    for (int s = 0; s < splits; ++s) {
-        const float2 v = ml[s];
-        if (v.y == 0.f) continue;  // this range holds nothing the row sees
-        const float f = expf(v.x - ref);
-        l += v.y * f;
+    for (int s0 = 0; s0 < splits; s0 += 32) {
+        if (s0) v = s0 + lane < splits ? __ldg(ml + s0 + lane) : make_float2(0.f, 0.f);
+        const float mine = v.y != 0.f ? expf(v.x - ref) : 0.f;  // a range may hold nothing the row sees
+        l += v.y * mine;
+        for (int s = s0; s < min(s0 + 32, splits); s += U) {
+            if (s) fetch(s);
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-            if (lane + 32 * c < a.D) o[c] = fmaf(po[static_cast<long long>(s) * a.D + lane + 32 * c], f, o[c]);
+            for (int u = 0; u < U; ++u) {
+                const float f = __shfl_sync(0xffffffffu, mine, (s + u - s0) & 31);
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (f != 0.f && s + u < splits) o[c] = fmaf(x[u][c], f, o[c]);
+            }
+        }
     }
+    for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
     const int i = static_cast<int>(r % a.Lq);
     const long long nh = r / a.Lq, n = nh / a.Hq, h = nh - n * a.Hq;
     const float f = l == 0.f ? 0.f : 1.f / l;
@@ -141,7 +162,7 @@ cudaError_t launch_band_empty(const BandArgs& a, void* out, float* lse, cudaStre
 }
 
 size_t band_forward_workspace_bytes(const BandArgs& a) {
-    return round256(a.dtype == 0 ? band_part_bytes(a, simt_splits(a)) : band_fwd_tc_part_bytes(a));
+    return round256(a.dtype == 0 ? band_part_bytes(a, simt_splits(a)) : band_few_fits(a) ? band_few_part_bytes(a) : band_fwd_tc_part_bytes(a));
 }
 
 cudaError_t band_status(unsigned* status, bool reset) {
@@ -158,7 +179,8 @@ size_t band_backward_workspace_bytes(const BandArgs& a) {
 }
 
 cudaError_t launch_band_forward(const BandArgs& a, void* out, float* lse, void* ws, cudaStream_t stream) {
-    return a.dtype == 0 ? launch_band_simt_forward(a, out, lse, ws, stream) : launch_band_fwd_tc(a, out, lse, ws, stream);
+    if (a.dtype == 0) return launch_band_simt_forward(a, out, lse, ws, stream);
+    return band_few_fits(a) ? launch_band_few(a, out, lse, ws, stream) : launch_band_fwd_tc(a, out, lse, ws, stream);
 }
 
 cudaError_t launch_band_backward(const BandArgs& a, const void* out, const float* lse, const void* gout, void* gq,

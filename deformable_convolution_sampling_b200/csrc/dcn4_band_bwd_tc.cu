@@ -15,11 +15,11 @@
 // sum of a row's d is that error (it is 0 otherwise), so grad_q corrects delta by it
 // for grad_kv, where it would add up: over the pairs of a bucket most of all.  For
 // gq the error weighs as the mean of a row's keys, that is with the root of their
-// number: where rows see at most kFewKeys, grad_q goes over the keys twice and takes
+// number: where rows see about kFewKeys or fewer, grad_q goes over the keys twice and takes
 // delta = sum p E from the first pass (one more pass of two of its three products).
 //
 // p and d go to the tensor cores as the I/O type (EXACT: as two numbers of it, see
-// kExactKeys), over the scores they came from in
+// kBandExactKeys), over the scores they came from in
 // tensor memory; the sums stay there in fp32 until they are rounded once.
 #include "dcn4_band_tc.cuh"
 
@@ -870,6 +870,12 @@ KvShape kv_shape(const BandArgs& a) {
     return s;
 }
 
+// Rows see few keys on the average (of a causal band's, the first ones see fewer than the most).
+bool few_keys(const BandArgs& a) {
+    const long long most = band_most_keys(a);
+    return (2LL * std::min(a.right, kBandMaxLen) < most ? most / 2 : most) <= kFewKeys;
+}
+
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 size_t stats_bytes(const BandArgs& a) { return up256(static_cast<size_t>(a.N) * a.Hq * padded_queries(a.Lq) * sizeof(float2)); }
 size_t part_bytes(const BandArgs& a, const KvShape& s) {
@@ -915,7 +921,7 @@ cudaError_t launch(const BandArgs& a, const void* out, const float* lse, const v
                                                                                       static_cast<const T*>(gout), stats);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     grad_q_kernel<T, NB, BIAS, EXACT><<<static_cast<unsigned>(static_cast<long long>(a.N) * (a.Hq / pack) * blocks), QCfg<NB, BIAS>::threads, smem_q, stream>>>(
-        mq, mg, mk, mv, a, pack, tq, blocks, kv.floats, band_most_keys(a) <= kFewKeys, stats, static_cast<T*>(gq));
+        mq, mg, mk, mv, a, pack, tq, blocks, kv.floats, few_keys(a), stats, static_cast<T*>(gq));
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     grad_kv_kernel<T, NB, BIAS, EXACT><<<static_cast<unsigned>(static_cast<long long>(a.N) * a.Hk * kv.items()), KvCfg<NB, BIAS>::threads, smem_kv, stream>>>(
         mq1, mg1, mk1, mv1, a, kv, stats, static_cast<T*>(gk), static_cast<T*>(gv), part, diag);
@@ -944,7 +950,7 @@ size_t band_bwd_tc_workspace(const BandArgs& a) {
 cudaError_t launch_band_bwd_tc(const BandArgs& a, const void* out, const float* lse, const void* gout, void* gq, void* gk, void* gv,
                                void* gbias, void* ws, cudaStream_t stream) {
 #define DCN4_BAND_BWD(T, NB, BIAS)                                                                          \
-    (band_most_keys(a) <= kExactKeys ? launch<T, NB, BIAS, true>(a, out, lse, gout, gq, gk, gv, gbias, ws, stream) \
+    (band_most_keys(a) <= kBandExactKeys ? launch<T, NB, BIAS, true>(a, out, lse, gout, gq, gk, gv, gbias, ws, stream) \
                                      : launch<T, NB, BIAS, false>(a, out, lse, gout, gq, gk, gv, gbias, ws, stream))
 #define DCN4_BAND_BWD_T(T)                                                                    \
     (a.D > 64 ? (a.nb ? DCN4_BAND_BWD(T, 2, true) : DCN4_BAND_BWD(T, 2, false))               \

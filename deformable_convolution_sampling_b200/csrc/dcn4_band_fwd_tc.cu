@@ -90,7 +90,7 @@ __device__ __forceinline__ bool chunks_of(const RowBand& b, int j0, int& ca, int
     return b.any && lo < hi;
 }
 
-// EXACT: p as two numbers (kExactKeys)
+// EXACT: p as two numbers (kBandExactKeys)
 template <typename T, int NB, bool BIAS, bool EXACT>
 __global__ void __launch_bounds__(Cfg<NB>::threads, Cfg<NB>::ctas)
     fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
@@ -537,7 +537,7 @@ cudaError_t launch(const BandArgs& a, const FwdShape& s, void* out, float* lse, 
 
 template <typename T, int NB>
 cudaError_t launch_heads(const BandArgs& a, const FwdShape& s, void* out, float* lse, void* ws, cudaStream_t stream) {
-    if (band_most_keys(a) <= kExactKeys)
+    if (band_most_keys(a) <= kBandExactKeys)
         return a.nb ? launch<T, NB, true, true>(a, s, out, lse, ws, stream) : launch<T, NB, false, true>(a, s, out, lse, ws, stream);
     return a.nb ? launch<T, NB, true, false>(a, s, out, lse, ws, stream) : launch<T, NB, false, false>(a, s, out, lse, ws, stream);
 }

@@ -38,6 +38,10 @@ inline int band_splits(const BandArgs& a, long long ctas, int queries, int bn, i
     return static_cast<int>(std::max<long long>(1, std::min<long long>(std::min<long long>(want, tiles / 4), 256)));
 }
 
+// Where a row sees no more keys than this, what meets them (probabilities and their
+// gradients) keeps more than the I/O type's bits on the tensor cores: few roundings do
+// not average out, and a small call's time is not in its products.
+constexpr int kBandExactKeys = 64;
 // The most keys that a row can see.
 inline long long band_most_keys(const BandArgs& a) {
     return std::min<long long>(a.Lk, static_cast<long long>(std::min(a.left, kBandMaxLen)) + std::min(a.right, kBandMaxLen) + 1 + a.sinks);
@@ -55,6 +59,11 @@ cudaError_t launch_band_bias_sum(const BandArgs& a, int per, int each, const flo
 size_t band_fwd_tc_part_bytes(const BandArgs& a);
 cudaError_t launch_band_fwd_tc(const BandArgs& a, void* out, float* lse, void* ws, cudaStream_t stream);
 cudaError_t band_fwd_status(unsigned* status, bool reset);
+
+// 16-bit types, up to 16 rows (dcn4_band_few.cu).
+bool band_few_fits(const BandArgs& a);
+size_t band_few_part_bytes(const BandArgs& a);
+cudaError_t launch_band_few(const BandArgs& a, void* out, float* lse, void* ws, cudaStream_t stream);
 
 // 16-bit backward on the tensor cores (dcn4_band_bwd_tc.cu), where it fits.
 bool band_bwd_tc_fits(const BandArgs& a);

@@ -198,10 +198,8 @@ __device__ __forceinline__ void issue_sum(uint32_t d, uint32_t a, uint64_t b, ui
         }
 }
 
-// Where a row sees no more keys than this, what meets them (p, d) goes to the
-// tensor cores as two numbers of the I/O type, the second what the first leaves: few
-// roundings do not average out, and a small call's time is not in its products.
-constexpr int kExactKeys = 64;
+// Where rows see at most kBandExactKeys keys, p and d go to the tensor cores as two
+// numbers of the I/O type, the second what the first leaves.
 constexpr int kLow = 16;  // columns from the first numbers of a chunk to the second ones
 
 // Two floats as a pair of T, and what the pair leaves of them.

@@ -126,6 +126,11 @@ DECODE = [
     case("bf16", 1, 1, 17, 64, 1, 128),
     case("f16", 1, 7, 6000, 20, 4, 96, right=0, left=4000, sinks=4),
     case("bf16", 2, 2, 4100, 40, 2, 64, right=0),
+    case("bf16", 2, 1, 300, 17, 1, 64),                                                     # one row more than sixteen
+    case("f16", 3, 2, 129, 8, 1, 40, left=70, right=3, sinks=2, nb=5, M=30, k_len=[129, 80, 129],
+         q_start=[100, 10, 128], q_len=[2, 2, 1], poison=True),
+    case("f16", 2, 1, 70, 2, 2, 8, nb=2, M=3),
+    case("bf16", 2, 2, 500, 8, 1, 120, left=90, right=-1, q_start=[1 << 20, -70]),          # one sees nothing
 ]
 
 
@@ -351,11 +356,11 @@ def test_qknorm_matches_the_definition(dcn, c):
 
 def test_qknorm_gradients_against_differences(dcn):
     g = torch.Generator().manual_seed(29)
-    x = torch.randn(2, 9, 3, 16, generator=g)
-    w, up = torch.randn(16, generator=g), torch.randn(2, 9, 3, 16, generator=g)
-    pos, inv = torch.randint(0, 50, (2, 9, 1), generator=g).float(), torch.rand(6, generator=g)
-    xc, leaves = x.cuda(), None
-    leaves = [xc.requires_grad_(True), w.cuda().requires_grad_(True)]
+    f32 = dict(generator=g, dtype=torch.float32)
+    x = torch.randn(2, 9, 3, 16, **f32)
+    w, up = torch.randn(16, **f32), torch.randn(2, 9, 3, 16, **f32)
+    pos, inv = torch.randint(0, 50, (2, 9, 1), generator=g).float(), torch.rand(6, **f32)
+    leaves = [x.cuda().requires_grad_(True), w.cuda().requires_grad_(True)]
     out, _ = dcn.qk_norm_rotate(leaves[0], leaves[0].detach()[:, :, :1], leaves[1], None, pos.cuda(), inv.cuda())
     gx, gw = torch.autograd.grad(out, leaves, up.cuda())
     ref = qknorm_reference(x, w, pos, inv, False, 1e-6, "f32", up)
