@@ -34,7 +34,7 @@ using namespace tc;
 // the SM's schedulers had two warps each to hide latencies with, and grad_kv of a
 // 785 x 785 map with a bias took 124 us instead of 93).
 constexpr int kProducer = 16, kMma = 17;
-constexpr int kTile = 64, kChunks = kTile / kTcChunk;  // keys or queries of a streamed tile
+constexpr int kTile = 64;                              // keys or queries of a streamed tile: two chunks
 constexpr int kTileBlock = kTile * 128;                // bytes of 64 of its columns
 constexpr int kTableExtra = 160;                       // as in the forward: a chunk and a tile's rows past M
 constexpr int kTableBytes = 28 << 10;

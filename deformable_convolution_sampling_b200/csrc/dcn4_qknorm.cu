@@ -43,6 +43,22 @@ struct Shape {
     long long units;
     int grid;
 };
+// CTAs an SM: without spills (at 6 and 4 the registers spill, and uneven shares of the
+// tokens cost a round: 46 and 77 us for 4 x 4096 tokens of 20 heads of 128).
+constexpr int kForwardCtas = 5, kBackwardCtas = 3;
+
+// The units of a warp: all heads of a run of tokens, every warp's as long as the next
+// one's, or, where tokens are few, some heads of one token at a time.
+struct Units {
+    long long at, end, step;
+    __device__ __forceinline__ Units(const Shape& sh, long long total) {
+        const long long w = blockIdx.x * static_cast<long long>(kWarps) + (threadIdx.x >> 5), all = static_cast<long long>(gridDim.x) * kWarps;
+        const bool run = sh.chunks == 1;
+        at = run ? total * w / all : w;
+        end = run ? total * (w + 1) / all : sh.units;
+        step = run ? sh.tokens : all;
+    }
+};
 
 __device__ __forceinline__ float group_sum(float v, int lph) {
     for (int o = lph >> 1; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -239,16 +255,18 @@ __device__ __forceinline__ void load_weight(uint4 (&w)[2], const void* p, const 
 }
 
 template <typename T, int MODE>
-__global__ void __launch_bounds__(kThreads, 6) qknorm_forward_kernel(QkNormArgs a, Shape sh, T* __restrict__ qo, T* __restrict__ ko) {
+__global__ void __launch_bounds__(kThreads, kForwardCtas) qknorm_forward_kernel(QkNormArgs a, Shape sh, T* __restrict__ qo, T* __restrict__ ko) {
     constexpr int E = Elem<T>::per16;
     extern __shared__ __align__(16) float qk_smem[];
     Warp<T, MODE> wp(a, sh, qk_smem);
     const long long total = static_cast<long long>(a.N) * a.L;
     const float inv_d = 1.f / a.D;
-    for (long long u = blockIdx.x * static_cast<long long>(kWarps) + (threadIdx.x >> 5); u < sh.units; u += static_cast<long long>(gridDim.x) * kWarps) {
-        const long long tok = u / sh.chunks * sh.tokens;
-        const int count = static_cast<int>(total - tok < sh.tokens ? total - tok : sh.tokens);
-        const int lo = static_cast<int>(u % sh.chunks) * sh.heads;
+    const Units un(sh, total);
+    for (long long u = un.at; u < un.end; u += un.step) {
+        const bool run = sh.chunks == 1;
+        const long long tok = run ? u : u / sh.chunks;
+        const int count = run ? static_cast<int>(un.end - u < sh.tokens ? un.end - u : sh.tokens) : 1;
+        const int lo = run ? 0 : static_cast<int>(u % sh.chunks) * sh.heads;
         const long long n = tok / a.L;
         const int l = static_cast<int>(tok - n * a.L);
 #pragma unroll 1
@@ -300,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 6) qknorm_forward_kernel(QkNormArgs 
 
 // gx, and this CTA's sums of gw: part[cta][2][D] (queries, keys).
 template <typename T, int MODE>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, kBackwardCtas)
     qknorm_backward_kernel(QkNormArgs a, Shape sh, const T* __restrict__ gqo, const T* __restrict__ gko,
                            T* __restrict__ gq, T* __restrict__ gk, float* __restrict__ part) {
     constexpr int E = Elem<T>::per16;
@@ -309,10 +327,12 @@ __global__ void __launch_bounds__(kThreads, 4)
     const long long total = static_cast<long long>(a.N) * a.L;
     const float inv_d = 1.f / a.D;
     F2 acc[2][2][E / 2] = {};  // queries' and keys' sums of the lane's entries
-    for (long long u = blockIdx.x * static_cast<long long>(kWarps) + (threadIdx.x >> 5); u < sh.units; u += static_cast<long long>(gridDim.x) * kWarps) {
-        const long long tok = u / sh.chunks * sh.tokens;
-        const int count = static_cast<int>(total - tok < sh.tokens ? total - tok : sh.tokens);
-        const int lo = static_cast<int>(u % sh.chunks) * sh.heads;
+    const Units un(sh, total);
+    for (long long u = un.at; u < un.end; u += un.step) {
+        const bool run = sh.chunks == 1;
+        const long long tok = run ? u : u / sh.chunks;
+        const int count = run ? static_cast<int>(un.end - u < sh.tokens ? un.end - u : sh.tokens) : 1;
+        const int lo = run ? 0 : static_cast<int>(u % sh.chunks) * sh.heads;
         const long long n = tok / a.L;
         const int l = static_cast<int>(tok - n * a.L);
 #pragma unroll
@@ -402,7 +422,7 @@ __global__ void __launch_bounds__(kThreads) qknorm_weights_kernel(const float* _
     if (lane == 0 && to) to[e < D ? e : e - D] = from_f32<T>(s);
 }
 
-Shape shape_of(const QkNormArgs& a, int elems) {
+Shape shape_of(const QkNormArgs& a, int elems, int ctas) {
     Shape s;
     const int nchunk = a.D / elems, H = a.Hq + a.Hk;
     s.mode = !a.R ? kNone : a.interleaved ? kNeighbours : (a.R / 2) % elems ? kExchange : kHalves;
@@ -412,18 +432,17 @@ Shape shape_of(const QkNormArgs& a, int elems) {
     s.lph = 1;
     while (s.lph < lanes) s.lph *= 2;
     const int hpw = 32 / s.lph;
-    const long long total = static_cast<long long>(a.N) * a.L, busy = 24LL * kBandSms;  // warps that hide the loads
-    // some sixteen steps of a warp a unit, fewer while that leaves SMs without their warps: then a token's
-    // heads are split, too
-    s.tokens = static_cast<int>(std::max<long long>(1, std::min<long long>(16LL * hpw / H, total / busy)));
+    const long long total = static_cast<long long>(a.N) * a.L, busy = static_cast<long long>(ctas) * kWarps * kBandSms;  // all warps there is room for
+    // some sixteen steps of a warp for the angles of as many tokens; where tokens are too few for the
+    // warps, a token's heads are split
+    s.tokens = static_cast<int>(std::max<long long>(1, std::min<long long>(16LL * hpw / H, (total + busy - 1) / busy)));
     if (a.R) s.tokens = std::min(s.tokens, kMaxPairs / (a.R / 2));
-    const long long sets = (total + s.tokens - 1) / s.tokens;
     const int groups = (H + hpw - 1) / hpw;
-    s.chunks = static_cast<int>(std::max<long long>(1, std::min<long long>(groups, (busy + sets - 1) / std::max<long long>(sets, 1))));
+    s.chunks = total >= busy ? 1 : static_cast<int>(std::min<long long>(groups, (busy + total - 1) / std::max<long long>(total, 1)));
     s.heads = s.chunks == 1 ? H : (groups + s.chunks - 1) / s.chunks * hpw;
     s.chunks = (H + s.heads - 1) / s.heads;
-    s.units = sets * s.chunks;
-    s.grid = static_cast<int>(std::min<long long>((s.units + kWarps - 1) / kWarps, 8LL * kBandSms));
+    s.units = total * s.chunks;
+    s.grid = static_cast<int>(std::min<long long>((s.units + kWarps - 1) / kWarps, static_cast<long long>(ctas) * kBandSms));
     return s;
 }
 
@@ -433,7 +452,7 @@ size_t smem_bytes(const QkNormArgs& a, const Shape& s) {
 
 template <typename T>
 cudaError_t forward_typed(const QkNormArgs& a, void* qo, void* ko, cudaStream_t stream) {
-    const Shape s = shape_of(a, Elem<T>::per16);
+    const Shape s = shape_of(a, Elem<T>::per16, kForwardCtas);
     const auto kernel = s.mode == kNone ? qknorm_forward_kernel<T, kNone> : s.mode == kHalves ? qknorm_forward_kernel<T, kHalves>
                         : s.mode == kNeighbours ? qknorm_forward_kernel<T, kNeighbours> : qknorm_forward_kernel<T, kExchange>;
     kernel<<<s.grid, kThreads, smem_bytes(a, s), stream>>>(a, s, static_cast<T*>(qo), static_cast<T*>(ko));
@@ -443,7 +462,7 @@ cudaError_t forward_typed(const QkNormArgs& a, void* qo, void* ko, cudaStream_t 
 template <typename T>
 cudaError_t backward_typed(const QkNormArgs& a, const void* gqo, const void* gko, void* gq, void* gk, void* gwq,
                            void* gwk, void* ws, cudaStream_t stream) {
-    const Shape s = shape_of(a, Elem<T>::per16);
+    const Shape s = shape_of(a, Elem<T>::per16, kBackwardCtas);
     float* part = (gwq || gwk) ? static_cast<float*>(ws) : nullptr;
     const auto kernel = s.mode == kNone ? qknorm_backward_kernel<T, kNone> : s.mode == kHalves ? qknorm_backward_kernel<T, kHalves>
                         : s.mode == kNeighbours ? qknorm_backward_kernel<T, kNeighbours> : qknorm_backward_kernel<T, kExchange>;
@@ -459,7 +478,7 @@ cudaError_t backward_typed(const QkNormArgs& a, const void* gqo, const void* gko
 }  // namespace
 
 size_t qknorm_backward_workspace_bytes(const QkNormArgs& a) {
-    const Shape s = shape_of(a, a.dtype == 0 ? 4 : 8);
+    const Shape s = shape_of(a, a.dtype == 0 ? 4 : 8, kBackwardCtas);
     return (static_cast<size_t>(s.grid) * 2 * a.D * sizeof(float) + 255) / 256 * 256;
 }
 
