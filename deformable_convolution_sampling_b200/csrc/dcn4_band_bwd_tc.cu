@@ -21,6 +21,11 @@
 // p and d go to the tensor cores as the I/O type (EXACT: as two numbers of it, see
 // kBandExactKeys), over the scores they came from in
 // tensor memory; the sums stay there in fp32 until they are rounded once.
+//
+// 2 x 4096 causal tokens, window 1024, 16 heads of 128 on 4: grad_q 119 us (its 90
+// GFLOP at 760 TFLOP/s), grad_kv 160 us (120 GFLOP), stats 20 us, bound by MMAs of
+// N = 64 from shared memory; 16 x 785 ragged tokens with a bias, 8 heads of 64: 65, 93
+// and 10 us, bound by the latency of a step's chain (products, exponentials, products).
 #include "dcn4_band_tc.cuh"
 
 namespace dcn4 {

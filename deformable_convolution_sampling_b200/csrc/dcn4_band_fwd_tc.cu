@@ -19,6 +19,13 @@
 // so that one tile's exponentials run under the other's products.  Of a key tile
 // only the 32-column chunks that some row may see are computed; only chunks on the
 // band's edge are masked element by element.
+//
+// Bound by MMAs of N = 64 from shared memory (49 cycles, not 32: its bandwidth) and by
+// exponentials in equal parts for heads of 128, by issue slots for heads of 32.  Tiles of
+// 128 keys would run the MMAs at their full rate, but leave tensor memory no room for a
+// second tile's scores: 203 us against 145 for 8192 causal tokens with a window of 2048
+// and 16 heads of 128 on 4 (831 TFLOP/s); 8 maps of 64 x 64, eight rows of pixels and a
+// bias, 8 heads of 32: 122 us.
 #include "dcn4_band_tc.cuh"
 
 namespace dcn4 {
