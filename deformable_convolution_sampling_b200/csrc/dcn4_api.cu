@@ -418,7 +418,8 @@ int make_qknorm(const dcn4_qknorm_params* p, dcn4::QkNormArgs* a) {
     if (p->D * static_cast<long long>(eb) % 16 != 0 || p->D > 256)
         return fail(DCN4_ERR_UNSUPPORTED, "D=%d: D*sizeof(dtype) must be a multiple of 16 and D <= 256", p->D);
     if (static_cast<long long>(p->Hq) + p->Hk > 65536) return fail(DCN4_ERR_UNSUPPORTED, "at most 65536 heads");
-    if (static_cast<long long>(p->N) * p->L > (1LL << 40)) return fail(DCN4_ERR_UNSUPPORTED, "N*L too large");
+    if (p->L >= (1 << 30) || static_cast<long long>(p->N) * p->L > (1LL << 40))
+        return fail(DCN4_ERR_UNSUPPORTED, "L must be < 2^30 and N*L <= 2^40");
     for (long long s : {p->q_batch, p->q_row, p->k_batch, p->k_row}) {
         if (s < 0 || s >= (1LL << 38)) return fail(DCN4_ERR_BAD_SHAPE, "strides must be >= 0 and < 2^38 elements");
         if (s * eb % 16 != 0) return fail(DCN4_ERR_UNSUPPORTED, "strides must be multiples of 16 bytes");

@@ -70,13 +70,18 @@ __global__ void __launch_bounds__(256) diag_sum_kernel(BandArgs a, int per, int 
     const int hk = h / a.G, g = h - hk * a.G;
     const long long all = (static_cast<long long>(a.N) * per) << shift, e0 = all * blockIdx.z / gridDim.z, e1 = all * (blockIdx.z + 1) / gridDim.z;
     float s = 0.f;
-    if (rel < len) {
-#pragma unroll 8
-        for (long long e = e0 + warp; e < e1; e += 8) {
-            const unsigned c = static_cast<unsigned>(e >> shift), n = c / per;  // N Hk per is a grid: 31 bits
+    constexpr int U = 8;  // loads at a time, also in the last batch
+    for (long long e = e0 + warp; e < e1; e += 8 * U) {
+        float v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const long long x = e + 8 * u;
+            const unsigned c = static_cast<unsigned>(x >> shift), n = c / per;  // N Hk per is a grid: 31 bits
             const long long cta = (static_cast<long long>(n) * a.Hk + hk) * per + c - n * per;
-            s += diag[(((cta << shift) + (e & ((1 << shift) - 1))) * a.G + g) * len + rel];
+            v[u] = x < e1 && rel < len ? __ldg(diag + (((cta << shift) + (x & ((1 << shift) - 1))) * a.G + g) * len + rel) : 0.f;
         }
+#pragma unroll
+        for (int u = 0; u < U; ++u) s += v[u];
     }
     s_part[warp][lane] = s;
     __syncthreads();
@@ -93,8 +98,13 @@ __global__ void __launch_bounds__(256) bucket_sum_kernel(BandArgs a, int parts, 
     const int h = blockIdx.x, len = 2 * a.M + 1, lane = threadIdx.x & 31;
     for (int r = threadIdx.x; r < len; r += 256) {
         float s = 0.f;
-#pragma unroll 8
-        for (int z = 0; z < parts; ++z) s += sums[(static_cast<long long>(z) * a.Hq + h) * len + r];
+        for (int z0 = 0; z0 < parts; z0 += 16) {
+            float v[16];
+#pragma unroll
+            for (int z = 0; z < 16; ++z) v[z] = z0 + z < parts ? __ldg(sums + (static_cast<long long>(z0 + z) * a.Hq + h) * len + r) : 0.f;
+#pragma unroll
+            for (int z = 0; z < 16; ++z) s += v[z];
+        }
         s_sum[r] = s;
     }
     __syncthreads();

@@ -300,12 +300,12 @@ __global__ void __launch_bounds__(QCfg<NB, BIAS>::threads, 1)
         };
         int nw = 0, ca, cb;
         bool ok = true;
-        for (int t = 0; t < cnt && ok; ++t) {
-            if (t == first && twice) {
+        for (int t = 0; t < cnt; ++t) {
+            if (t == first && twice) {  // (also by a warp whose wait gave up: the others' barrier counts it)
                 delta = both(off, true);
                 off = 0.f;
             }
-            if (!active(w, t, ca, cb)) continue;
+            if (!ok || !active(w, t, ca, cb)) continue;
             const int j = tile_at(t) + c * kTcChunk;
             const bool on = warp_live && c >= ca && c < cb;
             uint32_t x[32];
@@ -678,6 +678,11 @@ __global__ void __launch_bounds__(KvCfg<NB, BIAS>::threads, 1)
         const int kw = k0 + (warp & 3) * 32;  // this warp's keys
         Diagonals dg;
         int dg_head = -1;
+        float* diag_w = diag + (static_cast<long long>(blockIdx.x) * kDiagWarps + warp) * a.G * (2 * a.M + 1);
+        if (BIAS) {  // what no store below reaches is 0
+            for (int e = lane; e < a.G * (2 * a.M + 1); e += 32) diag_w[e] = 0.f;
+            __syncwarp();
+        }
         dg.M = a.M;
         dg.rel0 = kw - start;
         dg.buf = diag_s + warp * kDiagBuf;
@@ -690,7 +695,7 @@ __global__ void __launch_bounds__(KvCfg<NB, BIAS>::threads, 1)
             st_w.next();
             if (BIAS && warp_live && g != dg_head) {
                 if (dg_head >= 0) dg.finish(lane);
-                dg.start(diag + ((static_cast<long long>(blockIdx.x) * kDiagWarps + warp) * a.G + g) * (2 * a.M + 1));
+                dg.start(diag_w + g * (2 * a.M + 1));
                 dg_head = g;
             }
             chunks(i, ca, cb);
@@ -906,7 +911,6 @@ cudaError_t launch(const BandArgs& a, const void* out, const float* lse, const v
                  smem_kv = KvCfg<NB, BIAS>::smem + (BIAS ? static_cast<size_t>(a.G) * kv.floats * sizeof(float) : 0);
     cudaError_t e = allow_smem<grad_q_kernel<T, NB, BIAS, EXACT>>();
     if (e == cudaSuccess) e = allow_smem<grad_kv_kernel<T, NB, BIAS, EXACT>>();
-    if (e == cudaSuccess && BIAS) e = cudaMemsetAsync(diag, 0, diag_bytes(a, kv), stream);
     if (e != cudaSuccess) return e;
     CUtensorMap mq, mg, mk, mv, mq1, mg1, mk1, mv1;
     if (!make_map(&mq, a.dtype, a.q, a.N, a.Lq, a.Hq, a.D, a.q_batch, a.q_row, pack, tq) ||

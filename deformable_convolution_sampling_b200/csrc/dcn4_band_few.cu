@@ -19,8 +19,7 @@
 // 16384 tokens, 8 key heads of 128; 2 caches of 1000 tokens: 12.1 us, this one 8.7.)
 #include <cmath>
 
-#include "dcn4_band_parts.cuh"
-#include "dcn4_common.cuh"
+#include "dcn4_band_tc.cuh"
 
 namespace dcn4 {
 namespace {
@@ -290,11 +289,12 @@ cudaError_t launch(const BandArgs& a, void* out, float* lse, void* ws, cudaStrea
     const int splits = few_splits(a);
     const BandPart part = band_part(a, splits, ws);
     const unsigned grid = static_cast<unsigned>(static_cast<long long>(a.N) * a.Hk * splits);
-    const auto kernel = a.D > 64 ? few_kernel<T, 4> : few_kernel<T, 2>;
-    const int smem = a.D > 64 ? Cfg<4>::smem : Cfg<2>::smem;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = a.D > 64 ? tc::allow_smem<few_kernel<T, 4>>() : tc::allow_smem<few_kernel<T, 2>>();
     if (e != cudaSuccess) return e;
-    kernel<<<grid, kThreads, smem, stream>>>(a, splits, static_cast<T*>(out), lse, part);
+    if (a.D > 64)
+        few_kernel<T, 4><<<grid, kThreads, Cfg<4>::smem, stream>>>(a, splits, static_cast<T*>(out), lse, part);
+    else
+        few_kernel<T, 2><<<grid, kThreads, Cfg<2>::smem, stream>>>(a, splits, static_cast<T*>(out), lse, part);
     e = cudaGetLastError();
     if (e != cudaSuccess || splits == 1) return e;
     return launch_band_join(a, splits, part, out, lse, stream);

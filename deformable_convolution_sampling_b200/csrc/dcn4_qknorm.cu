@@ -417,8 +417,13 @@ __global__ void __launch_bounds__(kThreads) qknorm_weights_kernel(const float* _
     const int e = blockIdx.x * kWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (e >= 2 * D) return;
     float s = 0.f;
-#pragma unroll 8
-    for (int c = lane; c < ctas; c += 32) s += __ldg(part + static_cast<long long>(c) * 2 * D + e);
+    for (int c = lane; c < ctas; c += 32 * 16) {  // sixteen loads at a time: one batch mostly
+        float v[16];
+#pragma unroll
+        for (int u = 0; u < 16; ++u) v[u] = c + 32 * u < ctas ? __ldg(part + static_cast<long long>(c + 32 * u) * 2 * D + e) : 0.f;
+#pragma unroll
+        for (int u = 0; u < 16; ++u) s += v[u];
+    }
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     T* to = e < D ? gwq : gwk;
     if (lane == 0 && to) to[e < D ? e : e - D] = from_f32<T>(s);

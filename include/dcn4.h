@@ -537,7 +537,7 @@ int dcn4_band_status(int reset);
  * Hq or Hk may be 0 (its pointers are then not read).  Preconditions beyond those
  * of every call: D * sizeof(dtype) a multiple of 16 and D <= 256, R <= D a
  * multiple of 2 * axes, eps > 0, strides multiples of 16 bytes, heads at most
- * 65536 in all.
+ * 65536 in all, L below 2^30, N * L at most 2^40.
  * ------------------------------------------------------------------------- */
 typedef struct {
     int N, L;             /* images, tokens per image                                */

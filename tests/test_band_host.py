@@ -45,7 +45,7 @@ def test_band_refusals(dcn, field, value, status):
 @pytest.mark.parametrize("field,value,status", [
     ("dtype", -1, -8), ("N", -1, -2), ("L", -1, -2), ("Hq", -1, -2), ("D", 0, -2), ("D", 20, -5), ("D", 264, -5),
     ("R", 34, -2), ("R", 3, -2), ("R", -2, -2), ("axes", 3, -2), ("axes", 0, -2), ("interleaved", 2, -2), ("eps", 0.0, -2),
-    ("eps", math.nan, -2), ("Hq", 70000, -5), ("q_row", 32, -2), ("k_batch", 4, -5), ("q_batch", -8, -2),
+    ("eps", math.nan, -2), ("Hq", 70000, -5), ("L", 1 << 30, -5), ("q_row", 32, -2), ("k_batch", 4, -5), ("q_batch", -8, -2),
 ])
 def test_qknorm_refusals(dcn, field, value, status):
     p = dcn.make_qknorm_params(N=2, L=40, Hq=4, Hk=2, D=32, R=16)
