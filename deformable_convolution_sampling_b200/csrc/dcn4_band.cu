@@ -62,23 +62,24 @@ __global__ void __launch_bounds__(256) join_kernel(BandArgs a, int splits, BandP
     if (lane == 0) lse[r] = l == 0.f ? -INFINITY : m + logf(l);
 }
 
-// sums[z][h][rel] = the diagonal sums of head h, in a fixed order; a z-th of them a block.
-// 2^shift sums a CTA, `per` CTAs an image and key head.
-__global__ void __launch_bounds__(256) diag_sum_kernel(BandArgs a, int per, int shift, const float* __restrict__ diag, float* __restrict__ sums) {
+// sums[z][h][rel] = the diagonal sums of head h, in a fixed order; `chunk` CTAs' a block.
+// 2^shift sums a CTA, `per` CTAs an image and key head, `all` of them for a key head.
+__global__ void __launch_bounds__(256) diag_sum_kernel(BandArgs a, unsigned all, unsigned per, unsigned chunk, int shift,
+                                                       const float* __restrict__ diag, float* __restrict__ sums) {
     __shared__ float s_part[8][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.y, len = 2 * a.M + 1, rel = blockIdx.x * 32 + lane;
-    const int hk = h / a.G, g = h - hk * a.G;
-    const long long all = (static_cast<long long>(a.N) * per) << shift, e0 = all * blockIdx.z / gridDim.z, e1 = all * (blockIdx.z + 1) / gridDim.z;
-    float s = 0.f;
     constexpr int U = 8;  // loads at a time, also in the last batch
-    for (long long e = e0 + warp; e < e1; e += 8 * U) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.y, len = 2 * a.M + 1, rel = blockIdx.x * 32 + lane;
+    const unsigned hk = h / a.G, g = h - hk * a.G, c0 = blockIdx.z * chunk, c1 = min(all, c0 + chunk);
+    const long long row = static_cast<long long>(a.G) * len;
+    const float* from = diag + static_cast<long long>(g) * len + rel;
+    float s = 0.f;
+    for (unsigned c = c0; c < c1; c += (8 * U) >> shift) {
         float v[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const long long x = e + 8 * u;
-            const unsigned c = static_cast<unsigned>(x >> shift), n = c / per;  // N Hk per is a grid: 31 bits
-            const long long cta = (static_cast<long long>(n) * a.Hk + hk) * per + c - n * per;
-            v[u] = x < e1 && rel < len ? __ldg(diag + (((cta << shift) + (x & ((1 << shift) - 1))) * a.G + g) * len + rel) : 0.f;
+            const unsigned x = warp + 8 * u, q = c + (x >> shift), n = q / per;
+            const unsigned cta = (n * a.Hk + hk) * per + (q - n * per);  // a grid: 31 bits
+            v[u] = q < c1 && rel < len ? __ldg(from + ((static_cast<long long>(cta) << shift) + (x & ((1u << shift) - 1u))) * row) : 0.f;
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) s += v[u];
@@ -122,12 +123,9 @@ __global__ void __launch_bounds__(256) no_keys_kernel(float* __restrict__ lse, l
     if (r < rows) lse[r] = -INFINITY;
 }
 
-size_t round256(size_t b) { return (b + 255) / 256 * 256; }
+constexpr unsigned kSumParts = 32;  // blocks a diagonal's sum is shared by, at most
 
-// Blocks that share a diagonal's sum: some 64 sums each.
-int sum_parts(const BandArgs& a, int per, int each) {
-    return static_cast<int>(std::min<long long>(32, (static_cast<long long>(a.N) * per * each + 63) / 64));
-}
+size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
 }  // namespace
 
@@ -144,20 +142,22 @@ cudaError_t launch_band_join(const BandArgs& a, int splits, BandPart part, void*
 }
 
 size_t band_sum_bytes(const BandArgs& a) {
-    return static_cast<size_t>(32) * a.Hq * (2 * a.M + 1) * sizeof(float);
+    return static_cast<size_t>(kSumParts) * a.Hq * (2 * a.M + 1) * sizeof(float);
 }
 
 cudaError_t launch_band_bias_sum(const BandArgs& a, int per, int each, const float* diag, float* sums, void* gbias,
                                  cudaStream_t stream) {
-    const int zs = sum_parts(a, per, each), shift = each == 1 ? 0 : 4;  // one sum a CTA, or sixteen
-    diag_sum_kernel<<<dim3((2 * a.M + 32) / 32, a.Hq, zs), 256, 0, stream>>>(a, per, shift, diag, sums);
+    const int shift = each == 1 ? 0 : 4;  // one sum a CTA, or sixteen
+    const unsigned all = static_cast<unsigned>(a.N) * per, batch = 64u >> shift;
+    const unsigned chunk = std::max((all + kSumParts * batch - 1) / (kSumParts * batch), 1u) * batch, zs = (all + chunk - 1) / chunk;
+    diag_sum_kernel<<<dim3((2 * a.M + 32) / 32, a.Hq, zs), 256, 0, stream>>>(a, all, per, chunk, shift, diag, sums);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const dim3 grid(a.Hq, (a.nb + 63) / 64);
     switch (a.dtype) {
-        case 0: bucket_sum_kernel<float><<<grid, 256, 0, stream>>>(a, zs, sums, static_cast<float*>(gbias)); break;
-        case 1: bucket_sum_kernel<__half><<<grid, 256, 0, stream>>>(a, zs, sums, static_cast<__half*>(gbias)); break;
-        case 2: bucket_sum_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(a, zs, sums, static_cast<__nv_bfloat16*>(gbias)); break;
+        case 0: bucket_sum_kernel<float><<<grid, 256, 0, stream>>>(a, static_cast<int>(zs), sums, static_cast<float*>(gbias)); break;
+        case 1: bucket_sum_kernel<__half><<<grid, 256, 0, stream>>>(a, static_cast<int>(zs), sums, static_cast<__half*>(gbias)); break;
+        case 2: bucket_sum_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(a, static_cast<int>(zs), sums, static_cast<__nv_bfloat16*>(gbias)); break;
         default: return cudaErrorInvalidValue;
     }
     return cudaGetLastError();
