@@ -30,13 +30,19 @@ constexpr int kPL = kB + 4;   // row length of the probability tile
 // row's address, or NULL for a row of zeros.
 template <typename T, int DP, typename Row>
 __device__ __forceinline__ void load_tile(float* dst, int D, Row row) {
-    constexpr int E = Elem<T>::per16, C = DP / E;
-    for (int i = threadIdx.x; i < kB * C; i += kThreads) {
-        const int r = i / C, c = i - r * C;
+    constexpr int E = Elem<T>::per16, C = DP / E, N = kB * C / kThreads;
+    uint4 v[N];  // all loads before the first store: one latency a tile
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const int i = threadIdx.x + n * kThreads, r = i / C, c = i - r * C;
         const T* src = row(r);
-        const uint4 v = src && c * E < D ? __ldg(reinterpret_cast<const uint4*>(src + c * E)) : make_uint4(0u, 0u, 0u, 0u);
+        v[n] = src && c * E < D ? __ldg(reinterpret_cast<const uint4*>(src + c * E)) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const int i = threadIdx.x + n * kThreads, r = i / C, c = i - r * C;
         float2 f[E / 2];
-        unpack(v, f, T());
+        unpack(v[n], f, T());
         float* d = dst + r * (DP + 4) + c * E;
 #pragma unroll
         for (int e = 0; e < E / 4; ++e)
@@ -171,16 +177,16 @@ __device__ __forceinline__ float row_sum(float v) {
 }
 
 template <typename T, int DP>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
     simt_forward_kernel(BandArgs a, int blocks, int splits, int floats, T* __restrict__ out, float* __restrict__ lse, BandPart part) {
     constexpr int LD = DP + 4;
     extern __shared__ __align__(16) float smem[];
-    float *Qs = smem, *Ks = Qs + kB * LD, *Vs = Ks + kB * LD, *Ps = Vs + kB * LD;
+    float *Qs = smem, *Ks = Qs + kB * LD, *Vs = Ks + kB * LD, *Ps = Ks;  // P takes the place of K, which its product has read: two CTAs an SM
     const int sp = blockIdx.x % splits, blk = blockIdx.x / splits % blocks, nh = blockIdx.x / splits / blocks;
     const int n = nh / a.Hk, hk = nh - n * a.Hk;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int klen = band_klen(a, n), qlen = band_qlen(a, n), start = band_start(a, n);
-    const Bias<T> bias(a, Ps + kB * kPL, floats, hk * a.G);
+    const Bias<T> bias(a, Vs + kB * LD, floats, hk * a.G);
     const int rows = a.Lq * a.G, r0 = blk * kB;
     const int i0 = r0 / a.G, i1 = min((min(r0 + kB, rows) - 1) / a.G, qlen - 1);
     const T* q = static_cast<const T*>(a.q) + n * a.q_batch + static_cast<long long>(hk) * a.G * a.D;
@@ -216,6 +222,7 @@ __global__ void __launch_bounds__(kThreads)
             __syncthreads();
             float x[4][4];
             product<DP>(x, Qs, Ks, a.D, ty, tx);
+            __syncthreads();
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 float top = -INFINITY;
@@ -492,7 +499,7 @@ cudaError_t allow_smem(K kernel, size_t bytes) {
 template <typename T, int DP>
 cudaError_t forward_typed(const BandArgs& a, void* out, float* lse, void* ws, cudaStream_t stream) {
     const int blocks = simt_row_blocks(a), splits = simt_splits(a), floats = simt_table(a);
-    const size_t smem = tiles_smem<DP>(3, 1) + floats * sizeof(float);
+    const size_t smem = tiles_smem<DP>(3, 0) + floats * sizeof(float);
     cudaError_t e = allow_smem(simt_forward_kernel<T, DP>, smem);
     if (e != cudaSuccess) return e;
     const BandPart part = band_part(a, splits, ws);
