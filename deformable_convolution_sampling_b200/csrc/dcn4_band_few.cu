@@ -15,7 +15,7 @@
 // the kernel for many rows); p is rounded to the I/O type for its product, all sums
 // and statistics are fp32.  Four warps join in shared memory, CTAs through parts.
 // (Loads straight into registers left 6 KB a warp in flight: 3.7 TB/s.  The kernel for
-// many rows, which could take these calls too: 4.8 TB/s, this one 6.0, at 16 caches of
+// many rows, which could take these calls too: 4.8 TB/s, this one 5.9, at 16 caches of
 // 16384 tokens, 8 key heads of 128; 2 caches of 1000 tokens: 12.1 us, this one 8.7.)
 #include <cmath>
 

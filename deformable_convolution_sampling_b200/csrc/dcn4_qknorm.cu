@@ -18,7 +18,7 @@
 // pieces p and p + R / 2 of the "halves" form (any two where pairs are neighbours), so
 // that turning is arithmetic on registers; the sums are shuffles.  Only where R / 2 is
 // no whole number of pieces does a head go through shared memory.  4 x 4096 tokens, 20
-// heads of 128, bf16: 41 us forward (4.1 TB/s; a copy takes 28), 64 us backward.
+// heads of 128, bf16: 42 us forward (4.0 TB/s; a copy takes 28), 68 us backward.
 #include <algorithm>
 
 #include "dcn4_band.cuh"

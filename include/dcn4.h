@@ -453,9 +453,10 @@ int dcn4_attn_backward(const dcn4_attn_params* p, const void* value, const float
  * Precision: products accumulate in fp32, the softmax statistics are fp32.  For
  * fp16 / bf16 the products run on the tensor cores, whose second operands (the
  * probabilities e^{s - m} against a running maximum m, and in the backward the
- * probabilities and their gradients) are rounded to dtype; each output is then
- * rounded once.  fp32 stays fp32 throughout.  No atomics on sums: results are
- * the same from call to call.
+ * probabilities and their gradients) are rounded to dtype (kept as two numbers of
+ * dtype where rows see at most 64 keys); each output is then rounded once.  With
+ * fp16, gradients of scores below 2^-24 vanish: scale the loss as usual.  fp32 stays
+ * fp32 throughout.  No atomics on sums: results are the same from call to call.
  *
  * Preconditions beyond those of every call (16-byte aligned pointers, q_start,
  * q_len, k_len 4-byte aligned): Hq a multiple of Hk, Hq / Hk <= 128, D *
@@ -493,8 +494,9 @@ int dcn4_band_forward(const dcn4_band_params* p, const void* q, const void* k, c
                       const int* buckets, const int* q_start, const int* q_len, const int* k_len, void* out, float* lse,
                       void* workspace, size_t workspace_bytes, void* stream);
 
-/* Bytes of device workspace dcn4_band_backward needs (fp32: one number per query
- * and head, and with a bias the parts of its gradient); 0 if p is invalid. */
+/* Bytes of device workspace dcn4_band_backward needs (fp32: two numbers per query
+ * and head, partial gradients where few keys face many queries, and with a bias the
+ * sums of its gradient by relative position); 0 if p is invalid. */
 size_t dcn4_band_backward_workspace_size(const dcn4_band_params* p);
 
 /* Backward for grad_out, from the out and lse of the forward: with D_i = <grad_out_i, out_i>,
@@ -502,8 +504,8 @@ size_t dcn4_band_backward_workspace_size(const dcn4_band_params* p);
  *     grad_q_i = scale sum_j d_ij k_j,   grad_k_j = scale sum_i d_ij q_i,   grad_v_j = sum_i p_ij grad_out_i,
  *     grad_bias[b, h] = sum of d_ij over the pairs of bucket b and head h
  * (sums over the images too; grad_k and grad_v also over the query heads of a key
- * head).  All are overwritten.  grad_bias may be NULL (not wanted).  Launches on
- * `stream`: a kernel for grad_q, one for grad_k and grad_v, one for grad_bias. */
+ * head).  All are overwritten.  grad_bias may be NULL (not wanted).  A few kernels
+ * on `stream`. */
 int dcn4_band_backward(const dcn4_band_params* p, const void* q, const void* k, const void* v, const void* bias,
                        const int* buckets, const int* q_start, const int* q_len, const int* k_len, const void* out,
                        const float* lse, const void* grad_out, void* grad_q, void* grad_k, void* grad_v,

@@ -107,6 +107,10 @@ CASES = [
     case("bf16", 1, 160, 160, 24, 1, 64, right=0, nb=8, M=20),                              # many heads share a key head
     case("f16", 1, 9, 150, 256, 2, 16, right=0),                                            # a head group of 128
     case("f16", 70, 3, 20, 2, 2, 8, left=2, right=2),
+    case("bf16", 1, 700, 700, 2, 1, 64, left=5, right=0, sinks=600),                        # most keys are sinks
+    case("f16", 1, 1000, 1000, 2, 1, 32, left=40, right=0, sinks=3, nb=8, M=16),            # the sinks' tile is split
+    case("f32", 1, 300, 300, 2, 1, 24, left=9, right=0, sinks=130, nb=4, M=40),
+    case("bf16", 2, 30, 900, 6, 2, 72, nb=9, M=1000, left=800, right=100),
 ]
 
 
