@@ -625,7 +625,7 @@ def _heads_strides(name, t, dtype, device):
 def _int_vector(name, t, N, device):
     import torch
     if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != (N,) or not t.is_contiguous() or t.device != device):
-        raise ValueError(f"{name} must be a contiguous int32 tensor [N={N}] on q's device")
+        raise ValueError(f"{name} must be a contiguous int32 tensor [{N}] on q's device")
 
 
 def _dense(name, t, shape, dtype, device):
@@ -670,18 +670,24 @@ def _same(name, t, shape, dtype, batch, row):
         raise ValueError(f"{name} is not the tensor these parameters were made for")
 
 
-def _band_call(p, q, k, v):
+def _band_call(p, q, k, v, bias, buckets, *vectors):
     dt, keys = _torch_dtype(p.dtype), (p.N, p.Lk, p.Hk, p.D)
     _same("q", q, (p.N, p.Lq, p.Hq, p.D), dt, p.q_batch, p.q_row)
     _same("k", k, keys, dt, p.k_batch, p.k_row)
     _same("v", v, keys, dt, p.v_batch, p.v_row)
+    if bias is not None and buckets is not None:
+        _dense("bias", bias, (p.nb, p.Hq), dt, q.device)
+        _int_vector("buckets", buckets, 2 * p.M + 1, q.device)
+    for t in vectors:
+        if t is not None:
+            _int_vector("q_start, q_len or k_len", t, p.N, q.device)
 
 
 def band_forward(p: dcn4_band_params, q, k, v, bias=None, buckets=None, q_start=None, q_len=None, k_len=None, out=None):
     """(out [N, Lq, Hq, D], lse [N, Hq, Lq] fp32) of the dense attention over a band of keys,
     for CUDA tensors as band_params_for takes them."""
     import torch
-    _band_call(p, q, k, v)
+    _band_call(p, q, k, v, bias, buckets, q_start, q_len, k_len)
     shape = (p.N, p.Lq, p.Hq, p.D)
     if out is None:
         out = _dense_like(q, shape)
@@ -701,7 +707,7 @@ def band_backward(p: dcn4_band_params, q, k, v, out, lse, grad_out, bias=None, b
     grad_out [N, Lq, Hq, D] contiguous.  The gradients are dense."""
     import torch
     dev, dt = q.device, q.dtype
-    _band_call(p, q, k, v)
+    _band_call(p, q, k, v, bias, buckets, q_start, q_len, k_len)
     for name, t in (("out", out), ("grad_out", grad_out)):
         _dense(name, t, (p.N, p.Lq, p.Hq, p.D), dt, dev)
     _dense("lse", lse, (p.N, p.Hq, p.Lq), torch.float32, dev)
@@ -746,16 +752,19 @@ def qknorm_params_for(q, k, wq=None, wk=None, pos=None, inv_freq=None, *, interl
     return p
 
 
-def _qknorm_call(p, q, k):
+def _qknorm_call(p, q, k, wq, wk, pos, inv_freq):
     dt = _torch_dtype(p.dtype)
     _same("q", q, (p.N, p.L, p.Hq, p.D), dt, p.q_batch, p.q_row)
     _same("k", k, (p.N, p.L, p.Hk, p.D), dt, p.k_batch, p.k_row)
+    for t, n, of in ((wq, p.D, dt), (wk, p.D, dt), (pos, p.N * p.L * p.axes, None), (inv_freq, p.R // 2, None)):
+        if t is not None and (t.numel() != n or t.dtype != (of or _torch_dtype(DCN4_F32)) or not t.is_contiguous() or t.device != q.device):
+            raise ValueError("a weight, pos or inv_freq is not the tensor these parameters were made for")
 
 
 def qknorm_forward(p: dcn4_qknorm_params, q, k, wq=None, wk=None, pos=None, inv_freq=None):
     """(q_out [N, L, Hq, D], k_out [N, L, Hk, D]): the heads of q and k RMS-normed, weighted and
     rotated by their positions, for CUDA tensors as qknorm_params_for takes them."""
-    _qknorm_call(p, q, k)
+    _qknorm_call(p, q, k, wq, wk, pos, inv_freq)
     qo, ko = _dense_like(q, (p.N, p.L, p.Hq, p.D)), _dense_like(k, (p.N, p.L, p.Hk, p.D))
     _launch(q.device, dcn4_qknorm_forward, p, q.data_ptr(), k.data_ptr(), _ptr(wq), _ptr(wk), _ptr(pos), _ptr(inv_freq),
             qo.data_ptr(), ko.data_ptr())
@@ -767,7 +776,7 @@ def qknorm_backward(p: dcn4_qknorm_params, q, k, wq, wk, pos, inv_freq, grad_q_o
     gradients of its outputs; a weight that was None gets no gradient."""
     import torch
     dev, dt = q.device, q.dtype
-    _qknorm_call(p, q, k)
+    _qknorm_call(p, q, k, wq, wk, pos, inv_freq)
     _dense("grad_q_out", grad_q_out, (p.N, p.L, p.Hq, p.D), dt, dev)
     _dense("grad_k_out", grad_k_out, (p.N, p.L, p.Hk, p.D), dt, dev)
     gq, gk = torch.empty_like(grad_q_out), torch.empty_like(grad_k_out)

@@ -72,7 +72,7 @@ cudaError_t launch_band_bwd_tc(const BandArgs& a, const void* out, const float* 
                                void* gbias, void* ws, cudaStream_t stream);
 cudaError_t band_bwd_status(unsigned* status, bool reset);
 
-// Every type on the fp32 pipes (dcn4_band_simt.cu).
+// On the fp32 pipes (dcn4_band_simt.cu): fp32 forward, every type's backward.
 int simt_row_blocks(const BandArgs& a);
 int simt_splits(const BandArgs& a);
 cudaError_t launch_band_simt_forward(const BandArgs& a, void* out, float* lse, void* ws, cudaStream_t stream);

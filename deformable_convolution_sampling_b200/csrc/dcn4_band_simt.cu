@@ -1,5 +1,5 @@
-// dcn4_band_simt.cu — the band attention on the fp32 pipes, forward and
-// backward, in the form that is right for every type and shape.
+// dcn4_band_simt.cu — the band attention on the fp32 pipes: fp32, and the backward of
+// 16-bit types whose bias tables do not fit the tensor-core kernels.
 //
 // Forward, one pass over the visible keys with a running maximum m and sum l:
 //     s = scale q.k + b,  m' = max(m, s),  l = l e^(m-m') + e^(s-m'),  o likewise;  out = o / l,
@@ -589,13 +589,7 @@ size_t band_simt_backward_workspace(const BandArgs& a) {
 }
 
 cudaError_t launch_band_simt_forward(const BandArgs& a, void* out, float* lse, void* ws, cudaStream_t stream) {
-    const bool wide = a.D > 64;
-    switch (a.dtype) {
-        case 0: return wide ? forward_typed<float, 128>(a, out, lse, ws, stream) : forward_typed<float, 64>(a, out, lse, ws, stream);
-        case 1: return wide ? forward_typed<__half, 128>(a, out, lse, ws, stream) : forward_typed<__half, 64>(a, out, lse, ws, stream);
-        case 2: return wide ? forward_typed<__nv_bfloat16, 128>(a, out, lse, ws, stream) : forward_typed<__nv_bfloat16, 64>(a, out, lse, ws, stream);
-        default: return cudaErrorInvalidValue;
-    }
+    return a.D > 64 ? forward_typed<float, 128>(a, out, lse, ws, stream) : forward_typed<float, 64>(a, out, lse, ws, stream);
 }
 
 cudaError_t launch_band_simt_backward(const BandArgs& a, const void* out, const float* lse, const void* gout, void* gq,

@@ -128,6 +128,18 @@ def test_tensor_helpers_refuse_on_the_host(dcn):
     for t in (q[:, :3], q.float(), torch.zeros(2, 4, 4, 8).half()):
         with pytest.raises(ValueError, match="not the tensor"):
             dcn.band_forward(p, t, q, q)
+    b = dcn.make_band_params(N=2, Lq=4, Lk=4, Hq=2, D=8, nb=3, M=2)
+    five = torch.zeros(5, dtype=torch.int32)
+    for bias, buckets, vec in ((torch.zeros(4, 2).half(), five, None), (torch.zeros(3, 2).half(), five[:3].clone(), None),
+                               (torch.zeros(3, 2).half(), five, five[:1].clone()), (torch.zeros(3, 2).half(), five, torch.zeros(2))):
+        with pytest.raises(ValueError, match="must be a contiguous"):
+            dcn.band_forward(b, q, q, q, bias, buckets, k_len=vec)
+    r = dcn.make_qknorm_params(N=2, L=4, Hq=2, Hk=2, D=8, R=4)
+    f32 = torch.float32
+    ok = (torch.zeros(8).half(), None, torch.zeros(2, 4, dtype=f32), torch.zeros(2, dtype=f32))
+    for i, t in ((0, torch.zeros(7).half()), (0, torch.zeros(8)), (2, torch.zeros(2, 3)), (3, torch.zeros(3)), (3, torch.zeros(2).double())):
+        with pytest.raises(ValueError, match="made for"):
+            dcn.qknorm_forward(r, q, q, *(t if j == i else x for j, x in enumerate(ok)))
     s = dcn.make_band_params(N=2, Lq=4, Lk=4, Hq=2, D=8, k_row=32, k_batch=128)
     with pytest.raises(ValueError, match="not the tensor"):
         dcn.band_forward(s, q, q, q)
