@@ -15,16 +15,17 @@
 // sum of a row's d is that error (it is 0 otherwise), so grad_q corrects delta by it
 // for grad_kv, where it would add up: over the pairs of a bucket most of all.  For
 // gq the error weighs as the mean of a row's keys, that is with the root of their
-// number: where rows see about kFewKeys or fewer, grad_q goes over the keys twice and takes
-// delta = sum p E from the first pass (one more pass of two of its three products).
+// number: a CTA of grad_q whose rows see at most kFewKeys goes over them twice and takes
+// delta = sum p E from the first pass (one more pass of two of its three products; of
+// a long causal band the first CTAs only, whose rows hold half of gq's norm).
 //
 // p and d go to the tensor cores as the I/O type (EXACT: as two numbers of it, see
 // kBandExactKeys), over the scores they came from in
 // tensor memory; the sums stay there in fp32 until they are rounded once.
 //
-// 2 x 4096 causal tokens, window 1024, 16 heads of 128 on 4: grad_q 119 us (its 90
-// GFLOP at 760 TFLOP/s), grad_kv 160 us (120 GFLOP), stats 20 us, bound by MMAs of
-// N = 64 from shared memory; 16 x 785 ragged tokens with a bias, 8 heads of 64: 65, 93
+// 2 x 4096 causal tokens, window 1024, 16 heads of 128 on 4: grad_q 122 us (its 90
+// GFLOP at 740 TFLOP/s), grad_kv 160 us (120 GFLOP), stats 20 us, bound by MMAs of
+// N = 64 from shared memory; 16 x 785 ragged tokens with a bias, 8 heads of 64: 77, 93
 // and 10 us, bound by the latency of a step's chain (products, exponentials, products).
 #include "dcn4_band_tc.cuh"
 
@@ -115,7 +116,7 @@ template <typename T, int NB, bool BIAS, bool EXACT>
 __global__ void __launch_bounds__(QCfg<NB, BIAS>::threads, 1)
     grad_q_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_g,
                   const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, BandArgs a, int pack,
-                  int tq, int blocks, int floats, int twice, float2* __restrict__ stats, T* __restrict__ gq) {
+                  int tq, int blocks, int floats, float2* __restrict__ stats, T* __restrict__ gq) {
     constexpr int kSlots = QCfg<NB, BIAS>::slots;
     extern __shared__ __align__(1024) unsigned char band_smem[];
     __shared__ __align__(8) uint64_t full[kSlots], empty[kSlots], raw, rows_full, s_full[2], e_full[2], p_full[2], o_done[2];
@@ -165,7 +166,9 @@ __global__ void __launch_bounds__(QCfg<NB, BIAS>::threads, 1)
     BandTiles bt{0, 0, 0};
     if (i0 <= i1) bt = band_tiles(a, start + i0, start + i1, klen, kTile);
     // tiles to go over: with `twice`, first for delta alone
-    const int tiles = bt.count(), first = twice ? tiles : 0, cnt = first + tiles;
+    const int tiles = bt.count();
+    const bool twice = tiles * kTile <= kFewKeys;
+    const int first = twice ? tiles : 0, cnt = first + tiles;
     auto tile_at = [&](int t) { return bt.tile(t < first ? t : t - first) * kTile; };
     // what a half's rows see of key tile t: chunks [ca, cb)
     auto band_of = [&](int w, int& plo, int& phi) {
@@ -880,12 +883,6 @@ KvShape kv_shape(const BandArgs& a) {
     return s;
 }
 
-// Rows see few keys on the average (of a causal band's, the first ones see fewer than the most).
-bool few_keys(const BandArgs& a) {
-    const long long most = band_most_keys(a);
-    return (2LL * std::min(a.right, kBandMaxLen) < most ? most / 2 : most) <= kFewKeys;
-}
-
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 size_t stats_bytes(const BandArgs& a) { return up256(static_cast<size_t>(a.N) * a.Hq * padded_queries(a.Lq) * sizeof(float2)); }
 size_t part_bytes(const BandArgs& a, const KvShape& s) {
@@ -930,7 +927,7 @@ cudaError_t launch(const BandArgs& a, const void* out, const float* lse, const v
                                                                                       static_cast<const T*>(gout), stats);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     grad_q_kernel<T, NB, BIAS, EXACT><<<static_cast<unsigned>(static_cast<long long>(a.N) * (a.Hq / pack) * blocks), QCfg<NB, BIAS>::threads, smem_q, stream>>>(
-        mq, mg, mk, mv, a, pack, tq, blocks, kv.floats, few_keys(a), stats, static_cast<T*>(gq));
+        mq, mg, mk, mv, a, pack, tq, blocks, kv.floats, stats, static_cast<T*>(gq));
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     grad_kv_kernel<T, NB, BIAS, EXACT><<<static_cast<unsigned>(static_cast<long long>(a.N) * a.Hk * kv.items()), KvCfg<NB, BIAS>::threads, smem_kv, stream>>>(
         mq1, mg1, mk1, mv1, a, kv, stats, static_cast<T*>(gk), static_cast<T*>(gv), part, diag);
