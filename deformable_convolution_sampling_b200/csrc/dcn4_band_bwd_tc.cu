@@ -289,7 +289,8 @@ __global__ void __launch_bounds__(QCfg<NB, BIAS>::threads, 1)
         float delta = twice ? 0.f : st.y, off = 0.f;  // off: the sum of the row's d, or in the first pass of p E
         const float sc = BIAS ? a.scale : a.scale * kLog2e;
         const float* tab = table + g * floats + a.M + kTableExtra - pos;
-        // the row's sum over both chunks, for the first chunk's thread (and, with `back`, the second's)
+        // the row's sum over both chunks, for the first chunk's thread (and, with `back`, the second's).  Each
+        // word is read by the other chunk's thread only, before a barrier that its next writer passes later.
         auto both = [&](float v, bool back) {
             if (c) s_off[w][row] = v;
             asm volatile("bar.sync %0, 256;" ::"r"(1 + w) : "memory");
@@ -297,7 +298,7 @@ __global__ void __launch_bounds__(QCfg<NB, BIAS>::threads, 1)
             if (back) {
                 if (!c) s_off[w][row] = v;
                 asm volatile("bar.sync %0, 256;" ::"r"(1 + w) : "memory");
-                v = s_off[w][row];
+                if (c) v = s_off[w][row];
             }
             return v;
         };
