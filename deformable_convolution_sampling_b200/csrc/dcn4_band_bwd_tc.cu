@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(QCfg<NB, BIAS>::threads, 1)
                   int tq, int blocks, int floats, float2* __restrict__ stats, T* __restrict__ gq) {
     constexpr int kSlots = QCfg<NB, BIAS>::slots;
     extern __shared__ __align__(1024) unsigned char band_smem[];
-    __shared__ __align__(8) uint64_t full[kSlots], empty[kSlots], raw, rows_full, s_full[2], e_full[2], p_full[2], o_done[2];
+    __shared__ __align__(8) uint64_t full[kSlots], empty[kSlots], raw, rows_full, s_full[2], e_full[2], p_full[2], o_done[2], ahead;
     __shared__ uint32_t taddr_s;
     __shared__ int s_abort;
     __shared__ float s_off[2][kTcRows];  // the second chunk's part of a row's sum
@@ -143,6 +143,7 @@ __global__ void __launch_bounds__(QCfg<NB, BIAS>::threads, 1)
         }
         mbar_init(smem_u32(&raw), 1);
         mbar_init(smem_u32(&rows_full), 1);
+        mbar_init(smem_u32(&ahead), 8);
         for (int w = 0; w < 2; ++w) {
             mbar_init(smem_u32(&s_full[w]), 1);
             mbar_init(smem_u32(&e_full[w]), 1);
@@ -230,8 +231,9 @@ __global__ void __launch_bounds__(QCfg<NB, BIAS>::threads, 1)
             bool ok = warp_wait(&rows_full, 0u, abort), some = false;
             uint32_t p_phase = 0;
             // half a step behind the first half, so that one's products run under the other's exponentials
+            // (a barrier that completes once: p_full would go on without this warp, and its parity come round)
             int ca0, cb0;
-            if (w == 1 && active(0, 0, ca0, cb0)) ok = ok && warp_wait(&p_full[0], 0u, abort);
+            if (w == 1 && active(0, 0, ca0, cb0)) ok = ok && warp_wait(&ahead, 0u, abort);
             int s = 0;
             uint32_t ph = 0;
 #pragma unroll 1
@@ -370,7 +372,10 @@ __global__ void __launch_bounds__(QCfg<NB, BIAS>::threads, 1)
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&p_full[w]));
+            if (lane == 0) {
+                mbar_arrive(smem_u32(&p_full[w]));
+                if (w == 0 && t == 0) mbar_arrive(smem_u32(&ahead));
+            }
             ++nw;
         }
         off = both(off, false);

@@ -25,8 +25,16 @@ ONE_TILE = [
 ]
 
 
-@pytest.mark.parametrize("c", ONE_TILE, ids=str)
-def test_one_key_tile_in_the_second_pass(dcn, c):  # noqa: F811
+# Rings of two and three slots with many tiles behind them: grad_q's halves may be as far apart as the ring.
+RINGS = [
+    case("bf16", 1, 700, 700, 4, 2, 128, nb=8, M=16),
+    case("f16", 2, 300, 900, 4, 4, 72, left=500, right=0),
+]
+
+
+@pytest.mark.parametrize("c", ONE_TILE + RINGS, ids=str)
+def test_order_within_grad_q(dcn, c):  # noqa: F811
+    """Equal to the definition and the same from call to call."""
     t = make(c, 3)
     first = compare(dcn, c, t)
     for _ in range(20):
