@@ -662,25 +662,36 @@ def band_params_for(q, k, v, *, left=-1, right=-1, sinks=0, scale=None, bias=Non
     return p
 
 
-def _same(name, t, shape, dtype, batch, row):
-    """ValueError unless t is the tensor (its shape and strides, 0 for dense ones) that the parameters are for."""
-    sb, sl = t.stride()[:2]
-    if t.shape != shape or t.dtype != dtype or (batch and shape[0] > 1 and sb != batch) or (
-            row and shape[1] > 1 and sl != row):
+def _same(name, t, shape, dtype, device, batch, row):
+    """ValueError unless t is the tensor (its shape, device and all strides, 0 for dense ones) that the parameters
+    are for.  A dimension of length 1 has no stride that matters."""
+    ok = t.shape == shape and t.dtype == dtype and t.device == device
+    if ok and t.numel():
+        N, L, H, D = shape
+        sb, sl, sh, sd = t.stride()
+        row = row or H * D
+        ok = (N == 1 or sb == (batch or row * L)) and (L == 1 or sl == row) and (H == 1 or sh == D) and (D == 1 or sd == 1)
+    if not ok:
         raise ValueError(f"{name} is not the tensor these parameters were made for")
+
+
+def _on_gpu(q):
+    if not q.is_cuda:
+        raise ValueError("q and the other tensors must be on a CUDA device")
 
 
 def _band_call(p, q, k, v, bias, buckets, *vectors):
     dt, keys = _torch_dtype(p.dtype), (p.N, p.Lk, p.Hk, p.D)
-    _same("q", q, (p.N, p.Lq, p.Hq, p.D), dt, p.q_batch, p.q_row)
-    _same("k", k, keys, dt, p.k_batch, p.k_row)
-    _same("v", v, keys, dt, p.v_batch, p.v_row)
+    _same("q", q, (p.N, p.Lq, p.Hq, p.D), dt, q.device, p.q_batch, p.q_row)
+    _same("k", k, keys, dt, q.device, p.k_batch, p.k_row)
+    _same("v", v, keys, dt, q.device, p.v_batch, p.v_row)
     if bias is not None and buckets is not None:
         _dense("bias", bias, (p.nb, p.Hq), dt, q.device)
         _int_vector("buckets", buckets, 2 * p.M + 1, q.device)
     for t in vectors:
         if t is not None:
             _int_vector("q_start, q_len or k_len", t, p.N, q.device)
+    _on_gpu(q)
 
 
 def band_forward(p: dcn4_band_params, q, k, v, bias=None, buckets=None, q_start=None, q_len=None, k_len=None, out=None):
@@ -754,11 +765,12 @@ def qknorm_params_for(q, k, wq=None, wk=None, pos=None, inv_freq=None, *, interl
 
 def _qknorm_call(p, q, k, wq, wk, pos, inv_freq):
     dt = _torch_dtype(p.dtype)
-    _same("q", q, (p.N, p.L, p.Hq, p.D), dt, p.q_batch, p.q_row)
-    _same("k", k, (p.N, p.L, p.Hk, p.D), dt, p.k_batch, p.k_row)
+    _same("q", q, (p.N, p.L, p.Hq, p.D), dt, q.device, p.q_batch, p.q_row)
+    _same("k", k, (p.N, p.L, p.Hk, p.D), dt, q.device, p.k_batch, p.k_row)
     for t, n, of in ((wq, p.D, dt), (wk, p.D, dt), (pos, p.N * p.L * p.axes, None), (inv_freq, p.R // 2, None)):
         if t is not None and (t.numel() != n or t.dtype != (of or _torch_dtype(DCN4_F32)) or not t.is_contiguous() or t.device != q.device):
             raise ValueError("a weight, pos or inv_freq is not the tensor these parameters were made for")
+    _on_gpu(q)
 
 
 def qknorm_forward(p: dcn4_qknorm_params, q, k, wq=None, wk=None, pos=None, inv_freq=None):

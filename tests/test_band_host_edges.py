@@ -1,0 +1,49 @@
+"""Host side of the band attention and the query/key norm, beyond tests/test_band_host.py: tensors that
+parameters are not for, workspaces of calls that want less (CPU only: nothing is launched)."""
+import pytest
+
+from test_abi_host import dcn  # noqa: F401  (a fixture)
+
+
+def _views(shape):
+    """Tensors of `shape` that dense parameters are not for: expanded, with transposed heads, every second
+    entry of longer rows, tokens of a longer row, on another device (as q: not on a GPU)."""
+    import torch
+    N, L, H, D = shape
+    z = lambda *s: torch.zeros(*s).half()  # noqa: E731
+    return {"expanded images": z(1, L, H, D).expand(shape), "expanded tokens": z(N, 1, H, D).expand(shape),
+            "transposed heads": z(N, L, D, H).transpose(2, 3), "head by head": z(N, H, L, D).transpose(1, 2),
+            "every second entry": z(N, L, H, 2 * D)[..., ::2], "longer rows": z(N, L, H + 1, D)[:, :, :H],
+            "longer images": z(N, L + 1, H, D)[:, :L], "another device": torch.zeros(shape, dtype=torch.float16, device="meta")}
+
+
+@pytest.mark.parametrize("name", list(_views((2, 4, 2, 8))))
+@pytest.mark.parametrize("explicit", [False, True])
+def test_tensors_that_the_parameters_are_not_for(dcn, name, explicit):
+    """Shapes and types alone do not make a tensor the parameters' own (host checks: nothing is launched)."""
+    import torch
+    shape = (2, 4, 2, 8)
+    dense, other = torch.zeros(shape).half(), _views(shape)[name]
+    st = dict(q_batch=64, q_row=16, k_batch=64, k_row=16) if explicit else {}
+    b = dcn.make_band_params(N=2, Lq=4, Lk=4, Hq=2, D=8, **st, **(dict(v_batch=64, v_row=16) if explicit else {}))
+    r = dcn.make_qknorm_params(N=2, L=4, Hq=2, Hk=2, D=8, **st)
+    for i in range(3):
+        args = [other if i == j else dense for j in range(3)]
+        with pytest.raises(ValueError, match="not the tensor"):
+            dcn.band_forward(b, *args)
+        with pytest.raises(ValueError, match="not the tensor"):
+            dcn.band_backward(b, *args, dense, torch.zeros(2, 2, 4), dense)
+    for args in ((other, dense), (dense, other)):
+        with pytest.raises(ValueError, match="not the tensor"):
+            dcn.qknorm_forward(r, *args)
+        with pytest.raises(ValueError, match="not the tensor"):
+            dcn.qknorm_backward(r, *args, None, None, None, None, dense, dense)
+
+
+def test_parameters_of_dense_tensors_take_no_cpu_tensors(dcn):
+    import torch
+    t = torch.zeros(2, 4, 2, 8).half()
+    with pytest.raises(ValueError, match="CUDA"):
+        dcn.band_forward(dcn.make_band_params(N=2, Lq=4, Lk=4, Hq=2, D=8), t, t, t)
+    with pytest.raises(ValueError, match="CUDA"):
+        dcn.qknorm_forward(dcn.make_qknorm_params(N=2, L=4, Hq=2, Hk=2, D=8), t, t)
