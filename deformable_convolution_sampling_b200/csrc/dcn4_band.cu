@@ -9,9 +9,11 @@ namespace dcn4 {
 namespace {
 
 // out = (sum_s o_s e^(m_s - m)) / (sum_s l_s e^(m_s - m)), lse = m + log of that
-// sum: a warp per row.
+// sum: a warp per row.  The m_s come in the unit that their kernel holds scores in (`unit`
+// natural ones): a conversion would round each on its own, and where scores are of 10^6 the
+// parts' weights with it.
 template <typename T>
-__global__ void __launch_bounds__(256) join_kernel(BandArgs a, int splits, BandPart part, T* __restrict__ out,
+__global__ void __launch_bounds__(256) join_kernel(BandArgs a, int splits, BandPart part, float unit, T* __restrict__ out,
                                                    float* __restrict__ lse, long long rows) {
     const long long r = blockIdx.x * 8ll + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
@@ -38,7 +40,7 @@ __global__ void __launch_bounds__(256) join_kernel(BandArgs a, int splits, BandP
     float l = 0.f, o[4] = {};
     for (int s0 = 0; s0 < splits; s0 += 32) {
         if (s0) v = s0 + lane < splits ? __ldg(ml + s0 + lane) : make_float2(0.f, 0.f);
-        const float mine = v.y != 0.f ? expf(v.x - ref) : 0.f;  // a range may hold nothing the row sees
+        const float mine = v.y != 0.f ? expf((v.x - ref) * unit) : 0.f;  // a range may hold nothing the row sees
         l += v.y * mine;
         for (int s = s0; s < min(s0 + 32, splits); s += U) {
             if (s) fetch(s);
@@ -59,7 +61,7 @@ __global__ void __launch_bounds__(256) join_kernel(BandArgs a, int splits, BandP
 #pragma unroll
     for (int c = 0; c < 4; ++c)
         if (lane + 32 * c < a.D) to[lane + 32 * c] = from_f32<T>(o[c] * f);
-    if (lane == 0) lse[r] = l == 0.f ? -INFINITY : m + logf(l);
+    if (lane == 0) lse[r] = l == 0.f ? -INFINITY : m * unit + logf(l);
 }
 
 // sums[z][h][rel] = the diagonal sums of head h, in a fixed order; `chunk` CTAs' a block.
@@ -129,13 +131,13 @@ size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
 }  // namespace
 
-cudaError_t launch_band_join(const BandArgs& a, int splits, BandPart part, void* out, float* lse, cudaStream_t stream) {
+cudaError_t launch_band_join(const BandArgs& a, int splits, BandPart part, float unit, void* out, float* lse, cudaStream_t stream) {
     const long long rows = band_rows(a);
     const unsigned grid = static_cast<unsigned>((rows + 7) / 8);
     switch (a.dtype) {
-        case 0: join_kernel<float><<<grid, 256, 0, stream>>>(a, splits, part, static_cast<float*>(out), lse, rows); break;
-        case 1: join_kernel<__half><<<grid, 256, 0, stream>>>(a, splits, part, static_cast<__half*>(out), lse, rows); break;
-        case 2: join_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(a, splits, part, static_cast<__nv_bfloat16*>(out), lse, rows); break;
+        case 0: join_kernel<float><<<grid, 256, 0, stream>>>(a, splits, part, unit, static_cast<float*>(out), lse, rows); break;
+        case 1: join_kernel<__half><<<grid, 256, 0, stream>>>(a, splits, part, unit, static_cast<__half*>(out), lse, rows); break;
+        case 2: join_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(a, splits, part, unit, static_cast<__nv_bfloat16*>(out), lse, rows); break;
         default: return cudaErrorInvalidValue;
     }
     return cudaGetLastError();

@@ -297,7 +297,7 @@ cudaError_t launch(const BandArgs& a, void* out, float* lse, void* ws, cudaStrea
         few_kernel<T, 2><<<grid, kThreads, Cfg<2>::smem, stream>>>(a, splits, static_cast<T*>(out), lse, part);
     e = cudaGetLastError();
     if (e != cudaSuccess || splits == 1) return e;
-    return launch_band_join(a, splits, part, out, lse, stream);
+    return launch_band_join(a, splits, part, 1.f, out, lse, stream);
 }
 
 }  // namespace

@@ -454,7 +454,6 @@ __global__ void __launch_bounds__(Cfg<NB>::threads, Cfg<NB>::ctas)
                 l = l * f0 + l1 * f1;
                 second = t1 - t0 > 1 && __any_sync(0xffffffffu, l1 > 0.f);
             }
-            const float mn = BIAS ? m : m * kLn2;
             const long long at = (static_cast<long long>(n) * a.Hq + h0 + g) * a.Lq + i;
             const bool split = sh.splits > 1;
             const float inv = l > 0.f ? (split ? 1.f : 1.f / l) : 0.f;
@@ -462,9 +461,9 @@ __global__ void __launch_bounds__(Cfg<NB>::threads, Cfg<NB>::ctas)
             f1 *= inv;
             if (rows_here) {
                 if (split)
-                    part.ml[at * sh.splits + sp] = make_float2(l > 0.f ? mn : -INFINITY, l);
+                    part.ml[at * sh.splits + sp] = make_float2(l > 0.f ? m : -INFINITY, l);
                 else
-                    lse[at] = l > 0.f ? mn + logf(l) : -INFINITY;
+                    lse[at] = l > 0.f ? (BIAS ? m : m * kLn2) + logf(l) : -INFINITY;
             }
             T* to = out + ((static_cast<long long>(n) * a.Lq + i) * a.Hq + h0 + g) * a.D;
             float* po = part.o + (at * sh.splits + sp) * a.D;
@@ -539,7 +538,7 @@ cudaError_t launch(const BandArgs& a, const FwdShape& s, void* out, float* lse, 
     fwd_kernel<T, NB, BIAS, EXACT><<<static_cast<unsigned>(ctas), C::threads, smem, stream>>>(mq, mk, mv, a, s, static_cast<T*>(out), lse, part);
     e = cudaGetLastError();
     if (e != cudaSuccess || s.splits == 1) return e;
-    return launch_band_join(a, s.splits, part, out, lse, stream);
+    return launch_band_join(a, s.splits, part, BIAS ? 1.f : kLn2, out, lse, stream);
 }
 
 template <typename T, int NB>

@@ -47,8 +47,8 @@ inline long long band_most_keys(const BandArgs& a) {
     return std::min<long long>(a.Lk, static_cast<long long>(std::min(a.left, kBandMaxLen)) + std::min(a.right, kBandMaxLen) + 1 + a.sinks);
 }
 
-// out and lse of every row from its parts.
-cudaError_t launch_band_join(const BandArgs& a, int splits, BandPart part, void* out, float* lse, cudaStream_t stream);
+// out and lse of every row from its parts, whose maxima are in `unit` natural units (1, or ln 2 of base 2).
+cudaError_t launch_band_join(const BandArgs& a, int splits, BandPart part, float unit, void* out, float* lse, cudaStream_t stream);
 // gbias from sums of ds along diagonals: diag[((n Hk + hk) per + c) each + w][G][2 M + 1], c < per
 // CTAs of an image and key head, w < each sums a CTA.  Needs band_sum_bytes of scratch.
 size_t band_sum_bytes(const BandArgs& a);

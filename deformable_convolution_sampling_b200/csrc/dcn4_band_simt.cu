@@ -510,7 +510,7 @@ cudaError_t forward_typed(const BandArgs& a, void* out, float* lse, void* ws, cu
         a, blocks, splits, floats, static_cast<T*>(out), lse, part);
     e = cudaGetLastError();
     if (e != cudaSuccess || splits == 1) return e;
-    return launch_band_join(a, splits, part, out, lse, stream);
+    return launch_band_join(a, splits, part, 1.f, out, lse, stream);
 }
 
 // Ranges of the queries that see a key tile (splits of grad_kv).

@@ -5,7 +5,9 @@ derived where it is used."""
 import pytest
 import torch
 
-from test_gpu_band import DTYPES, case, compare, dcn, make, run  # noqa: F401  (dcn is a fixture)
+from _band import E32, check
+from _band_far import far_reference
+from test_gpu_band import case, compare, dcn, make, run  # noqa: F401  (dcn is a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -40,3 +42,62 @@ def test_order_within_grad_q(dcn, c):  # noqa: F811
     for _ in range(20):
         for x, y in zip(first, run(dcn, c, t)):
             assert x is y is None or torch.equal(x, y)
+
+
+def far_compare(dcn, c, t, s, es, names, loose=1.0):  # noqa: F811
+    """run(c, t) against far_reference; the bounds must be below the values, or they would say nothing."""
+    M = c.get("M", 0)
+    buckets = None
+    if c.get("nb"):
+        rel = torch.arange(c["Lk"])[None] - (c["Lk"] - c["Lq"] + torch.arange(c["Lq"])[:, None])
+        buckets = t["buckets"].long()[rel.clamp(-M, M) + M], c["nb"]
+    scale = c["D"] ** -0.5 if c.get("scale") is None else c["scale"]
+    r = far_reference(t["q"], t["k"], t["v"], t["g"], s, es, scale, c["dtype"], buckets)
+    got = dict(zip(("out", "lse", "gq", "gk", "gv", "gb"), run(dcn, c, t)))
+    for name in names:
+        part = r[name + "_tol"].median() / r[name].abs().mean()
+        assert part < loose, f"{name}: a bound of {float(part):.2f} of the values says nothing"
+        check(name, got[name], r[name], r[name + "_tol"])
+    return got
+
+
+def rel_of(c):
+    return torch.arange(c["Lk"])[None] - (c["Lk"] - c["Lq"] + torch.arange(c["Lq"])[:, None])
+
+
+# Scores of about 2^20 that differ by a few: products, scores and biases are exact in 32 bits (whole numbers and
+# quarters), so that only what is done with them is at stake.
+COMMON = [dict(Lq=150, Lk=150, Hq=2, Hk=1, D=64), dict(Lq=64, Lk=900, Hq=2, Hk=2, D=128), dict(Lq=40, Lk=60, Hq=4, Hk=2, D=32),
+          dict(Lq=300, Lk=300, Hq=2, Hk=1, D=64, nb=4, M=16), dict(Lq=130, Lk=130, Hq=24, Hk=1, D=40, nb=4, M=16)]
+
+
+def common_part(dtype, i, c=None):
+    """A case (of COMMON), its tensors and its scores."""
+    c = case(dtype, 1, scale=0.25, right=0, **(c or COMMON[i]))
+    t = make(c, i)
+    gen = torch.Generator().manual_seed(i)
+    for x in ("q", "k"):
+        t[x] = torch.randint(-1, 2, t[x].shape, generator=gen).to(t[x].dtype)
+        t[x][..., 0] = 2048.0
+    b = 0.0
+    if c.get("nb"):
+        t["bias"] = torch.randint(-8, 9, t["bias"].shape, generator=gen).to(t["bias"].dtype) / 4
+        b = t["bias"].double()[t["buckets"].long()[rel_of(c).clamp(-c["M"], c["M"]) + c["M"]]].permute(2, 0, 1)
+    kk = t["k"].double().repeat_interleave(c["Hq"] // c["Hk"], 2)
+    s = torch.einsum("nihd,njhd->nhij", t["q"].double(), kk) * 0.25 + b
+    return c, t, torch.where(rel_of(c) <= 0, s, torch.full_like(s, -torch.inf))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("i", range(len(COMMON)))
+def test_scores_with_a_large_common_part(dcn, dtype, i):  # noqa: F811
+    """Differences of scores are below 100, and formed to 32 bits."""
+    c, t, s = common_part(dtype, i)
+    far_compare(dcn, c, t, s, 100 * E32, ["out"])
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("c", [dict(Lq=1, Lk=3000, Hq=4, Hk=2, D=64), dict(Lq=2, Lk=200, Hq=4, Hk=1, D=128), dict(Lq=40, Lk=5000, Hq=2, Hk=2, D=64)], ids=str)
+def test_few_rows_with_scores_of_a_large_common_part(dcn, dtype, c):  # noqa: F811
+    c, t, s = common_part(dtype, 9, c)
+    far_compare(dcn, c, t, s, 100 * E32, ["out"])
