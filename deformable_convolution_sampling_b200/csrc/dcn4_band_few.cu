@@ -266,12 +266,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<KG>::ctas)
         const long long at = (static_cast<long long>(n) * a.Hq + hq) * a.Lq + i;
         if (splits > 1) {
             *reinterpret_cast<float4*>(part.o + (at * splits + sp) * a.D + d) = s;
-            if (d == 0) part.ml[at * splits + sp] = make_float2(ll > 0.f ? mm : -INFINITY, ll);
+            if (d == 0) part.ml[at * splits + sp] = make_float2(ll != 0.f ? mm : -INFINITY, ll);
         } else {
-            const float inv = ll > 0.f ? 1.f / ll : 0.f;
+            const float inv = ll != 0.f ? 1.f / ll : 0.f;  // (a sum of NaN stays one)
             T* to = out + ((static_cast<long long>(n) * a.Lq + i) * a.Hq + hq) * a.D + d;
             *reinterpret_cast<uint2*>(to) = make_uint2(pair_of<T>(s.x * inv, s.y * inv), pair_of<T>(s.z * inv, s.w * inv));
-            if (d == 0) lse[at] = ll > 0.f ? mm + logf(ll) : -INFINITY;
+            if (d == 0) lse[at] = ll != 0.f ? mm + logf(ll) : -INFINITY;
         }
     }
 }

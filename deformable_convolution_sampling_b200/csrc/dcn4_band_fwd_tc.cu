@@ -442,28 +442,29 @@ __global__ void __launch_bounds__(Cfg<NB>::threads, Cfg<NB>::ctas)
         }
         const bool rows_here = ql < sh.tq && i < a.Lq;
         if (ok && !(sh.alt && w == 1) && __any_sync(0xffffffffu, rows_here)) {
+            // (a sum is 0 where a row sees nothing, and NaN, which must stay, where it sees one)
             float f0 = 1.f, f1 = 0.f, m = rm, l = live ? rl : 0.f;
             bool first = nw > 0, second = false;
             if (sh.alt) {
                 const float2 other = s_ml[row];
                 const float l1 = live ? other.y : 0.f;
-                m = fmaxf(rm, l1 > 0.f ? other.x : -INFINITY);
+                m = fmaxf(rm, l1 != 0.f ? other.x : -INFINITY);
                 const float ref = m == -INFINITY ? 0.f : m;
-                f0 = l > 0.f ? ex2((rm - ref) * unit) : 0.f;
-                f1 = l1 > 0.f ? ex2((other.x - ref) * unit) : 0.f;
+                f0 = l != 0.f ? ex2((rm - ref) * unit) : 0.f;
+                f1 = l1 != 0.f ? ex2((other.x - ref) * unit) : 0.f;
                 l = l * f0 + l1 * f1;
-                second = t1 - t0 > 1 && __any_sync(0xffffffffu, l1 > 0.f);
+                second = t1 - t0 > 1 && __any_sync(0xffffffffu, l1 != 0.f);
             }
             const long long at = (static_cast<long long>(n) * a.Hq + h0 + g) * a.Lq + i;
             const bool split = sh.splits > 1;
-            const float inv = l > 0.f ? (split ? 1.f : 1.f / l) : 0.f;
-            f0 = l > 0.f ? f0 * inv : 0.f;
+            const float inv = l != 0.f ? (split ? 1.f : 1.f / l) : 0.f;
+            f0 = l != 0.f ? f0 * inv : 0.f;
             f1 *= inv;
             if (rows_here) {
                 if (split)
-                    part.ml[at * sh.splits + sp] = make_float2(l > 0.f ? m : -INFINITY, l);
+                    part.ml[at * sh.splits + sp] = make_float2(l != 0.f ? m : -INFINITY, l);
                 else
-                    lse[at] = l > 0.f ? (BIAS ? m : m * kLn2) + logf(l) : -INFINITY;
+                    lse[at] = l != 0.f ? (BIAS ? m : m * kLn2) + logf(l) : -INFINITY;
             }
             T* to = out + ((static_cast<long long>(n) * a.Lq + i) * a.Hq + h0 + g) * a.D;
             float* po = part.o + (at * sh.splits + sp) * a.D;

@@ -446,9 +446,11 @@ int dcn4_attn_backward(const dcn4_attn_params* p, const void* value, const float
  *   grad_bias        [nb, Hq]        dtype
  *
  * Keys and values at j >= k_len[n] and queries (and grad_out) at i >= q_len[n]
- * may hold anything, infinities and NaN too.  A non-finite key or value at j <
- * k_len[n] reaches the queries that see it, and may reach any that share a tile
- * of 128 with one that does.
+ * may hold anything, infinities and NaN too.  A NaN in a query reaches its rows.  A
+ * non-finite key or value at j < k_len[n] reaches the queries that see it, and may
+ * reach others, as a probability of 0 times an infinity is a NaN: any that share a
+ * tile of 128 rows with one that sees it, or whose own keys share a tile of 64 (128
+ * in the backward) with it.  A cache whose end holds none needs k_len, not right = 0.
  *
  * Precision: products accumulate in fp32, the softmax statistics are fp32.  For
  * fp16 / bf16 the products run on the tensor cores, whose second operands (the

@@ -101,3 +101,37 @@ def test_scores_with_a_large_common_part(dcn, dtype, i):  # noqa: F811
 def test_few_rows_with_scores_of_a_large_common_part(dcn, dtype, c):  # noqa: F811
     c, t, s = common_part(dtype, 9, c)
     far_compare(dcn, c, t, s, 100 * E32, ["out"])
+
+
+# Many rows with and without split keys, both halves on the same rows, few rows with and without split keys, fp32.
+NAN = [case("bf16", 1, 300, 300, 2, 1, 64), case("f16", 1, 40, 2000, 2, 2, 128), case("f16", 1, 60, 60, 2, 1, 32),
+       case("bf16", 2, 1, 3000, 4, 2, 64), case("f16", 1, 2, 100, 4, 2, 128), case("f16", 600, 1, 70, 2, 2, 64), case("f32", 1, 70, 100, 2, 2, 32),
+       case("bf16", 1, 200, 200, 2, 1, 64, nb=4, M=8)]
+
+
+@pytest.mark.parametrize("c", NAN, ids=str)
+def test_nan_reaches_the_rows_that_see_it(dcn, c):  # noqa: F811
+    """A NaN in a query reaches its rows, one in a key that everybody sees everything, of its heads."""
+    t = make(c)
+    t["q"][0, 0, 0, 3] = torch.nan
+    out, lse, gq = run(dcn, c, t)[:3]
+    for x in (out[0, 0, 0], lse[0, 0, 0], gq[0, 0, 0]):
+        assert x.isnan().all()
+    assert c["Lq"] == 1 or not lse[0, 0, 1:].isnan().any()
+    assert not out[:, :, 1].isnan().any() and not lse[:, 1].isnan().any()
+    t = make(c)
+    t["k"][0, c["Lk"] // 2, 0, 1] = torch.nan
+    out, lse, gq = run(dcn, c, t)[:3]
+    for x in (out[0, :, 0], lse[0, 0], gq[0, :, 0]):
+        assert x.isnan().all()
+    assert c["Hk"] == 1 or not lse[:, -1].isnan().any()
+    t = make(c)
+    t["v"][0, c["Lk"] - 1, 0, 2] = torch.inf
+    out, lse = run(dcn, c, t)[:2]
+    assert not out[0, :, 0, 2].isfinite().any() and lse.isfinite().all()
+
+
+def test_a_value_that_no_query_sees_may_not_be_finite_behind_k_len(dcn):  # noqa: F811
+    """Infinities ahead of a token are kept out by k_len."""
+    c = case("bf16", 2, 1, 200, 4, 2, 64, right=0, k_len=[150, 77], q_start=[149, 76], poison=True)
+    compare(dcn, c, backward=False)
