@@ -51,6 +51,13 @@ __device__ __forceinline__ bool band_sees(const BandArgs& a, int p, int j, int k
 // What the backward subtracts from a row's scores.  A row whose log sum is -infinity
 // has probabilities of 0, also where a bias of -infinity makes s - lse a NaN.
 __device__ __forceinline__ float band_lse_ref(float lse) { return lse == -INFINITY ? INFINITY : lse; }
+// One number in 32 bits holds a row's log sum to 2^-24 of itself.  Where that is far from
+// zero (a row that sees only keys of the type's lowest bias keeps nothing of its log l),
+// e^(s - lse) is off by a factor, and the backward takes the row's maximum m and sum l
+// anew: p = e^(s - m) / l.  Up to 512 the factor is within 2^-15 of 1, a sixteenth of
+// fp16's half step and no more than the rounding of such a score itself.
+constexpr float kBandFarLse = 512.f;
+__device__ __forceinline__ bool band_far(float ref) { return fabsf(ref) > kBandFarLse && fabsf(ref) < INFINITY; }
 
 // The tiles of `bn` keys that positions p_lo..p_hi (all of them queries) have to
 // visit: the tiles of the sinks, then those of the window.

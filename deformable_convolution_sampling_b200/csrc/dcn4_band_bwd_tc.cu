@@ -63,12 +63,12 @@ __device__ __forceinline__ void fill_table(const BandArgs& a, float* table, int 
     }
 }
 
-// (lse, delta) of every row, [N][Hq][padded Lq].  Without a bias lse is in log2
-// units, as the scores are formed there.  `lanes` lanes a row, four rows a thread:
-// bound by HBM.
+// (lse, delta) of every row, [N][Hq][padded Lq], and the weight of its probabilities
+// (1; grad_q changes those of far rows).  Without a bias lse is in log2 units, as the
+// scores are formed there.  `lanes` lanes a row, four rows a thread: bound by HBM.
 template <typename T>
 __global__ void __launch_bounds__(256) stats_kernel(BandArgs a, int lanes, const T* __restrict__ out, const float* __restrict__ lse,
-                                                    const T* __restrict__ gout, float2* __restrict__ stats) {
+                                                    const T* __restrict__ gout, float2* __restrict__ stats, float* __restrict__ weights) {
     constexpr int U = 4;
     const int LP = padded_queries(a.Lq), groups = 256 / lanes, blocks = (LP + groups * U - 1) / (groups * U);
     const int nh = blockIdx.x / blocks, n = nh / a.Hq, h = nh - n * a.Hq, i0 = (blockIdx.x - nh * blocks) * groups * U + threadIdx.x / lanes;
@@ -98,7 +98,10 @@ __global__ void __launch_bounds__(256) stats_kernel(BandArgs a, int lanes, const
         for (int e = 0; e < 4; ++e) d = fmaf(p[e].x, q[e].x, fmaf(p[e].y, q[e].y, d));
         for (int o = lanes >> 1; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
         const int i = i0 + u * groups;
-        if (i < LP && piece == 0) stats[static_cast<long long>(nh) * LP + i] = make_float2(a.nb ? l[u] : l[u] * kLog2e, d);
+        if (i < LP && piece == 0) {
+            stats[static_cast<long long>(nh) * LP + i] = make_float2(a.nb ? l[u] : l[u] * kLog2e, d);
+            weights[static_cast<long long>(nh) * LP + i] = 1.f;
+        }
     }
 }
 
@@ -116,7 +119,8 @@ template <typename T, int NB, bool BIAS, bool EXACT>
 __global__ void __launch_bounds__(QCfg<NB, BIAS>::threads, 1)
     grad_q_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_g,
                   const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, BandArgs a, int pack,
-                  int tq, int blocks, int floats, float2* __restrict__ stats, T* __restrict__ gq) {
+                  int tq, int blocks, int floats, float2* __restrict__ stats, float* __restrict__ weights,
+                  int* __restrict__ far_blocks, T* __restrict__ gq) {
     constexpr int kSlots = QCfg<NB, BIAS>::slots;
     extern __shared__ __align__(1024) unsigned char band_smem[];
     __shared__ __align__(8) uint64_t full[kSlots], empty[kSlots], raw, rows_full, s_full[2], e_full[2], p_full[2], o_done[2], ahead;
@@ -135,6 +139,11 @@ __global__ void __launch_bounds__(QCfg<NB, BIAS>::threads, 1)
     const int klen = static_cast<int>(uniform(band_klen(a, n))), qlen = static_cast<int>(uniform(band_qlen(a, n))),
               start = static_cast<int>(uniform(band_start(a, n)));
     const int i0 = blk * 2 * tq, i1 = min(i0 + 2 * tq, qlen) - 1;
+    // the row of a softmax thread: of half w, and the chunk c of its columns
+    const int w = (warp >> 2) & 1, c = warp >> 3, row = tid & 127, ql = row / pack, g = row - ql * pack, i = i0 + w * tq + ql;
+    const bool live = warp < kProducer && ql < tq && i < qlen;
+    const long long stat_of = (static_cast<long long>(n) * a.Hq + h0 + g) * padded_queries(a.Lq) + i;
+    const float2 st = live ? stats[stat_of] : make_float2(INFINITY, 0.f);
 
     if (tid == 0) {
         for (int s = 0; s < kSlots; ++s) {
@@ -159,16 +168,17 @@ __global__ void __launch_bounds__(QCfg<NB, BIAS>::threads, 1)
     }
     if (BIAS) fill_table<T>(a, table, floats, h0, pack, QCfg<NB, BIAS>::threads);
     tc_fence_before();
-    __syncthreads();
+    const bool far = uniform(__syncthreads_or(band_far(st.x))) != 0;  // some row's sum is not in its lse
     tc_fence_after();
     const uint32_t tmem = uniform(taddr_s);
     volatile int* abort = &s_abort;
 
     BandTiles bt{0, 0, 0};
     if (i0 <= i1) bt = band_tiles(a, start + i0, start + i1, klen, kTile);
-    // tiles to go over: with `twice`, first for delta alone
+    if (tid == 0) far_blocks[(n * groups + h0 / pack) * blocks + blk] = far;
+    // tiles to go over: with `twice`, first for delta alone (and for the rows' maxima and sums, where `far`)
     const int tiles = bt.count();
-    const bool twice = tiles * kTile <= kFewKeys;
+    const bool twice = tiles * kTile <= kFewKeys || far;
     const int first = twice ? tiles : 0, cnt = first + tiles;
     auto tile_at = [&](int t) { return bt.tile(t < first ? t : t - first) * kTile; };
     // what a half's rows see of key tile t: chunks [ca, cb)
@@ -276,27 +286,23 @@ __global__ void __launch_bounds__(QCfg<NB, BIAS>::threads, 1)
         }
         __syncwarp();
     } else if (warp < kProducer) {
-        const int w = (warp >> 2) & 1, c = warp >> 3, row = tid & 127;  // a half's rows, the chunk c of its columns
         const uint32_t at_h = tmem + w * 256 + (static_cast<uint32_t>((warp & 3) * 32) << 16), at_s = at_h + c * kTcChunk, at_o = at_h + 128;
-        const int ql = row / pack, g = row - ql * pack, i = i0 + w * tq + ql;
-        const bool live = ql < tq && i < qlen;
         const bool warp_live = __any_sync(0xffffffffu, live);
         int plo, phi;
         band_of(w, plo, phi);
         const int pos = start + i;
         const int jlo = max(0, pos - a.left), jhi = min(klen, pos + a.right + 1), jsink = min(a.sinks, jhi);
         const int all_lo = phi - a.left, all_hi = min(klen, plo + a.right + 1) - kTcChunk;  // keys that all rows of the tile see
-        float2* stat = stats + (static_cast<long long>(n) * a.Hq + h0 + g) * padded_queries(a.Lq) + i;
-        const float2 st = live ? *stat : make_float2(INFINITY, 0.f);
-        float delta = twice ? 0.f : st.y, off = 0.f;  // off: the sum of the row's d, or in the first pass of p E
+        // p = 2^(score - ref) * weight; off: the sum of the row's d, or in the first pass of p E
+        float ref = st.x, weight = 1.f, delta = twice ? 0.f : st.y, shift = -delta, off = 0.f;
         const float sc = BIAS ? a.scale : a.scale * kLog2e;
         const float* tab = table + g * floats + a.M + kTableExtra - pos;
-        // the row's sum over both chunks, for the first chunk's thread (and, with `back`, the second's).  Each
-        // word is read by the other chunk's thread only, before a barrier that its next writer passes later.
-        auto both = [&](float v, bool back) {
+        // the row's sum (or maximum) over both chunks, for the first chunk's thread (and, with `back`, the second's).
+        // Each word is read by the other chunk's thread only, before a barrier that its next writer passes later.
+        auto both = [&](float v, bool back, bool largest = false) {
             if (c) s_off[w][row] = v;
             asm volatile("bar.sync %0, 256;" ::"r"(1 + w) : "memory");
-            if (!c) v += s_off[w][row];
+            if (!c) v = largest ? fmaxf(v, s_off[w][row]) : v + s_off[w][row];
             if (back) {
                 if (!c) s_off[w][row] = v;
                 asm volatile("bar.sync %0, 256;" ::"r"(1 + w) : "memory");
@@ -306,9 +312,63 @@ __global__ void __launch_bounds__(QCfg<NB, BIAS>::threads, 1)
         };
         int nw = 0, ca, cb;
         bool ok = true;
-        for (int t = 0; t < cnt; ++t) {
+        int t = 0;
+        if (far) {
+            // The first pass of a CTA with far rows: their maxima, sums and delta, as the forward forms them.  (In
+            // sixteen columns at a time and beside the loop below, whose registers it would not leave alone.)
+            float top = -INFINITY, sum = 0.f;
+            constexpr float unit = BIAS ? kLog2e : 1.f;
+            for (; t < first && ok; ++t) {
+                if (!active(w, t, ca, cb)) continue;
+                const int j = tile_at(t) + c * kTcChunk;
+                ok = warp_wait(&s_full[w], nw & 1, abort) && warp_wait(&e_full[w], nw & 1, abort);
+                tc_fence_after();
+                if (ok && warp_live && c >= ca && c < cb) {
+                    const uint32_t see = (low_bits(jhi - j) & ~low_bits(jlo - j)) | low_bits(jsink - j);
+#pragma unroll 1
+                    for (int h = 0; h < kTcChunk; h += 16) {
+                        uint32_t x[16], y[16];
+                        tmem_ld16(at_s + h, x);
+                        tmem_ld16(at_s + 64 + h, y);
+                        float most = top;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float s = __uint_as_float(x[e]);
+                            if (BIAS) x[e] = __float_as_uint(fmaf(s, sc, tab[max(pos - a.M, min(j + h + e, pos + a.M))]));
+                            if (see >> (h + e) & 1u) most = fmaxf(most, BIAS ? __uint_as_float(x[e]) : s * sc);
+                        }
+                        const float f = top == -INFINITY ? 0.f : ex2((top - most) * unit);
+                        sum *= f;
+                        off *= f;
+                        top = most;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            if (!(see >> (h + e) & 1u)) continue;
+                            const float s = __uint_as_float(x[e]), p = top == -INFINITY ? 0.f : ex2(BIAS ? (s - top) * unit : fmaf(s, sc, -top));
+                            sum += p;
+                            off = fmaf(p, __uint_as_float(y[e]), off);
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&p_full[w]));
+                    if (w == 0 && t == 0) mbar_arrive(smem_u32(&ahead));
+                }
+                ++nw;
+            }
+            t = first;
+            ref = both(top, true, true);
+            const float f = top == -INFINITY ? 0.f : ex2((top - ref) * unit), l = both(sum * f, true);
+            off *= f;
+            weight = l != 0.f ? 1.f / l : 1.f;
+            ref = l != 0.f ? ref : INFINITY;
+        }
+        for (; t < cnt; ++t) {
             if (t == first && twice) {  // (also by a warp whose wait gave up: the others' barrier counts it)
-                delta = both(off, true);
+                delta = both(off, true) * weight;
+                shift = -delta * weight;
                 off = 0.f;
             }
             if (!ok || !active(w, t, ca, cb)) continue;
@@ -330,11 +390,13 @@ __global__ void __launch_bounds__(QCfg<NB, BIAS>::threads, 1)
 #pragma unroll
                         for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(fmaf(__uint_as_float(x[e]), sc, tab[j + e]));
                     }
+                }
+                if (BIAS) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) sub_mul2(x[e], x[e + 1], st.x, kLog2e);
+                    for (int e = 0; e < 32; e += 2) sub_mul2(x[e], x[e + 1], ref, kLog2e);
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) fma2(x[e], x[e + 1], sc, -st.x);
+                    for (int e = 0; e < 32; e += 2) fma2(x[e], x[e + 1], sc, -ref);
                 }
 #pragma unroll
                 for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(ex2(__uint_as_float(x[e])));
@@ -346,7 +408,7 @@ __global__ void __launch_bounds__(QCfg<NB, BIAS>::threads, 1)
                 tmem_ld32_async(at_s + 64, y);
                 tmem_ld_wait(y);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * (__uint_as_float(y[e]) - delta));
+                for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * fmaf(__uint_as_float(y[e]), weight, shift));
                 if (j < all_lo || j > all_hi) {
                     const uint32_t see = (low_bits(jhi - j) & ~low_bits(jlo - j)) | low_bits(jsink - j);
 #pragma unroll
@@ -379,7 +441,10 @@ __global__ void __launch_bounds__(QCfg<NB, BIAS>::threads, 1)
             ++nw;
         }
         off = both(off, false);
-        if (ok && live && !c) stat->y = delta + off;
+        if (ok && live && !c) {
+            stats[stat_of] = make_float2(ref, delta + off);
+            if (far) weights[stat_of] = weight;
+        }
         if (ok && cnt) ok = warp_wait(&o_done[w], 0u, abort);
         tc_fence_after();
         const bool rows_here = ql < tq && i < a.Lq;
@@ -497,8 +562,9 @@ template <typename T, int NB, bool BIAS, bool EXACT>
 __global__ void __launch_bounds__(KvCfg<NB, BIAS>::threads, 1)
     grad_kv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_g,
                    const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, BandArgs a, KvShape sh,
-                   const float2* __restrict__ stats, T* __restrict__ gk, T* __restrict__ gv, float* __restrict__ part,
-                   float* __restrict__ diag) {
+                   const float2* __restrict__ stats, const float* __restrict__ weights, const int* __restrict__ far_blocks,
+                   int blocks, T* __restrict__ gk, T* __restrict__ gv,
+                   float* __restrict__ part, float* __restrict__ diag) {
     using C = KvCfg<NB, BIAS>;
     constexpr int kSlots = C::slots;
     extern __shared__ __align__(1024) unsigned char band_smem[];
@@ -684,6 +750,10 @@ __global__ void __launch_bounds__(KvCfg<NB, BIAS>::threads, 1)
         // queries that see every key of the tile (with a bias a dead key's d must be 0, so its tile is masked)
         const int all_lo = BIAS && k1 - k0 < kTcRows ? kBandFar : k1 - 1 - a.right - start, all_hi = (k1 <= a.sinks ? qlen : min(qlen, k0 + a.left - start + 1)) - kTcChunk;
         const float sc = BIAS ? a.scale : a.scale * kLog2e;
+        // whether some row of this key head is far (`blocks` of grad_q's CTAs went over them)
+        int some = 0;
+        for (int e = lane; e < blocks; e += 32) some |= far_blocks[nh * blocks + e];
+        const bool far = __any_sync(0xffffffffu, some);
         const int kw = k0 + (warp & 3) * 32;  // this warp's keys
         Diagonals dg;
         int dg_head = -1;
@@ -708,12 +778,12 @@ __global__ void __launch_bounds__(KvCfg<NB, BIAS>::threads, 1)
                 dg_head = g;
             }
             chunks(i, ca, cb);
+            const bool on = warp_live && c >= ca && c < cb;
             // the scores, and (the loads' own barrier) the queries' stats
             ok = warp_wait(&full[s], (t / kSlots) & 1, abort) && warp_wait(&s_full[w], (t >> 1) & 1, abort);
             if (!ok) break;
             tc_fence_after();
             uint32_t x[32], y[32];
-            const bool on = warp_live && c >= ca && c < cb;
             if (on) {
                 const float4* st = stat_s + s * (C::stat / 16) + c * (kTcChunk / 2);  // lse, delta of two queries each
                 tmem_ld32_async(at_s, x);
@@ -742,6 +812,11 @@ __global__ void __launch_bounds__(KvCfg<NB, BIAS>::threads, 1)
                         x[e] = __float_as_uint(ex2(fmaf(__uint_as_float(x[e]), sc, -u.x)));
                         x[e + 1] = __float_as_uint(ex2(fmaf(__uint_as_float(x[e + 1]), sc, -u.z)));
                     }
+                }
+                if (far) {
+                    const float weight = weights[(static_cast<long long>(n) * a.Hq + hk * a.G + g) * padded_queries(a.Lq) + ic + lane];  // of query ic + lane
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * __shfl_sync(0xffffffffu, weight, e));
                 }
             }
             if (!(ok = warp_wait(&e_full[w], (t >> 1) & 1, abort))) break;
@@ -891,6 +966,19 @@ KvShape kv_shape(const BandArgs& a) {
 
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 size_t stats_bytes(const BandArgs& a) { return up256(static_cast<size_t>(a.N) * a.Hq * padded_queries(a.Lq) * sizeof(float2)); }
+// How the rows of grad_q map to its CTAs: two tiles of `tq` queries of `pack` heads each.
+struct RowShape {
+    int pack, tq, blocks;
+};
+RowShape row_shape(const BandArgs& a) {
+    const int tq = kTcRows / a.G;
+    return {a.G, tq, (a.Lq + 2 * tq - 1) / (2 * tq)};
+}
+size_t far_bytes(const BandArgs& a) {
+    const RowShape r = row_shape(a);
+    return up256(static_cast<size_t>(a.N) * (a.Hq / r.pack) * r.blocks * sizeof(int));
+}
+size_t weights_bytes(const BandArgs& a) { return up256(static_cast<size_t>(a.N) * a.Hq * padded_queries(a.Lq) * sizeof(float)); }
 size_t part_bytes(const BandArgs& a, const KvShape& s) {
     return s.split() ? up256(static_cast<size_t>(a.N) * a.Hk * s.items() * 2 * kTcRows * a.D * sizeof(float)) : 0;
 }
@@ -905,10 +993,12 @@ cudaError_t launch(const BandArgs& a, const void* out, const float* lse, const v
     char* at = static_cast<char*>(ws);
     const KvShape kv = kv_shape(a);
     float2* stats = reinterpret_cast<float2*>(at);
-    float* part = reinterpret_cast<float*>(at += stats_bytes(a));
+    float* weights = reinterpret_cast<float*>(at += stats_bytes(a));
+    int* far_blocks = reinterpret_cast<int*>(at += weights_bytes(a));
+    float* part = reinterpret_cast<float*>(at += far_bytes(a));
     float* diag = reinterpret_cast<float*>(at += part_bytes(a, kv));
     float* sums = reinterpret_cast<float*>(at += diag_bytes(a, kv));
-    const int pack = a.G, tq = kTcRows / pack, blocks = (a.Lq + 2 * tq - 1) / (2 * tq);
+    const auto [pack, tq, blocks] = row_shape(a);
     const long long dense = static_cast<long long>(a.Hq) * a.D;
     const size_t smem_q = QCfg<NB, BIAS>::smem + (BIAS ? static_cast<size_t>(a.G) * kv.floats * sizeof(float) : 0),
                  smem_kv = KvCfg<NB, BIAS>::smem + (BIAS ? static_cast<size_t>(a.G) * kv.floats * sizeof(float) : 0);
@@ -930,13 +1020,13 @@ cudaError_t launch(const BandArgs& a, const void* out, const float* lse, const v
     const int each = 4 * 256 / lanes;
     const long long row_blocks = static_cast<long long>(a.N) * a.Hq * ((padded_queries(a.Lq) + each - 1) / each);
     stats_kernel<T><<<static_cast<unsigned>(row_blocks), 256, 0, stream>>>(a, lanes, static_cast<const T*>(out), lse,
-                                                                                      static_cast<const T*>(gout), stats);
+                                                                                      static_cast<const T*>(gout), stats, weights);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     grad_q_kernel<T, NB, BIAS, EXACT><<<static_cast<unsigned>(static_cast<long long>(a.N) * (a.Hq / pack) * blocks), QCfg<NB, BIAS>::threads, smem_q, stream>>>(
-        mq, mg, mk, mv, a, pack, tq, blocks, kv.floats, stats, static_cast<T*>(gq));
+        mq, mg, mk, mv, a, pack, tq, blocks, kv.floats, stats, weights, far_blocks, static_cast<T*>(gq));
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     grad_kv_kernel<T, NB, BIAS, EXACT><<<static_cast<unsigned>(static_cast<long long>(a.N) * a.Hk * kv.items()), KvCfg<NB, BIAS>::threads, smem_kv, stream>>>(
-        mq1, mg1, mk1, mv1, a, kv, stats, static_cast<T*>(gk), static_cast<T*>(gv), part, diag);
+        mq1, mg1, mk1, mv1, a, kv, stats, weights, far_blocks, blocks * (a.G / pack), static_cast<T*>(gk), static_cast<T*>(gv), part, diag);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (kv.split()) {
         const int tiles = kv.other_parts > 1 ? kv.tiles : kv.sink_tiles;
@@ -956,7 +1046,7 @@ bool band_bwd_tc_fits(const BandArgs& a) {
 
 size_t band_bwd_tc_workspace(const BandArgs& a) {
     const KvShape kv = kv_shape(a);
-    return stats_bytes(a) + part_bytes(a, kv) + diag_bytes(a, kv) + sums_bytes(a);
+    return stats_bytes(a) + weights_bytes(a) + far_bytes(a) + part_bytes(a, kv) + diag_bytes(a, kv) + sums_bytes(a);
 }
 
 cudaError_t launch_band_bwd_tc(const BandArgs& a, const void* out, const float* lse, const void* gout, void* gq, void* gk, void* gv,

@@ -272,12 +272,14 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
 }
 
-// gq of 64 rows over a range of their keys, their D (into delta) and, with a bias, the
-// sums of ds along diagonals: diag[CTA][G][2 M + 1], of relative position -M .. M (the ends: and beyond).
+// gq of 64 rows over a range of their keys, their D (into delta), what a probability is formed
+// from (refs: e^(s - x) y; lse and 1, or a far row's maximum and the inverse of its sum) and, with a
+// bias, the sums of ds along diagonals: diag[CTA][G][2 M + 1], of relative position -M .. M (the ends:
+// and beyond).
 template <typename T, int DP>
 __global__ void __launch_bounds__(kThreads)
     simt_grad_q_kernel(BandArgs a, int blocks, int splits, int floats, const T* __restrict__ out, const float* __restrict__ lse,
-                       const T* __restrict__ gout, T* __restrict__ gq, float* __restrict__ delta,
+                       const T* __restrict__ gout, T* __restrict__ gq, float* __restrict__ delta, float2* __restrict__ refs,
                        float* __restrict__ part, float* __restrict__ diag) {
     constexpr int LD = DP + 4;
     extern __shared__ __align__(16) float smem[];
@@ -303,7 +305,8 @@ __global__ void __launch_bounds__(kThreads)
     __syncthreads();
     int pos[4], head[4];
     bool live[4];
-    float le[4], de[4], o[4][DP / 16];
+    float le[4], weight[4], de[4], o[4][DP / 16];
+    bool far = false;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
         const int row = r0 + 4 * ty + r;
@@ -312,6 +315,8 @@ __global__ void __launch_bounds__(kThreads)
         head[r] = hk * a.G + row % a.G;
         const long long at = (static_cast<long long>(n) * a.Hq + head[r]) * a.Lq + row / a.G;
         le[r] = live[r] ? band_lse_ref(lse[at]) : 0.f;
+        weight[r] = 1.f;
+        far |= band_far(le[r]);
         float d = 0.f;
         for (int e = tx; e < DP; e += 16) d = fmaf(Gs[(4 * ty + r) * LD + e], Ks[(4 * ty + r) * LD + e], d);
         de[r] = row_sum(d);
@@ -322,8 +327,44 @@ __global__ void __launch_bounds__(kThreads)
     float* mine = diag + static_cast<long long>(blockIdx.x) * a.G * (2 * a.M + 1);
     if (a.nb)
         for (int e = threadIdx.x; e < a.G * (2 * a.M + 1); e += kThreads) mine[e] = 0.f;
+    far = __syncthreads_or(far);
     if (i0 <= i1) {
         const BandTiles bt = band_tiles(a, start + i0, start + i1, klen, kB);
+        if (far) {  // the rows' maxima and sums over all of their keys, in every CTA of a split row
+            float l[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) le[r] = -INFINITY, l[r] = 0.f;
+            for (int t = 0; t < bt.count(); ++t) {
+                const int j0 = bt.tile(t) * kB;
+                __syncthreads();
+                load_tile<T, DP>(Ks, a.D, [&](int j) -> const T* { return j0 + j < klen ? k + (j0 + j) * a.k_row : nullptr; });
+                __syncthreads();
+                float x[4][4];
+                product<DP>(x, Qs, Ks, a.D, ty, tx);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const int j = j0 + tx + 16 * c;
+                        const bool see = live[r] && band_sees(a, pos[r], j, klen);
+                        x[r][c] = see ? x[r][c] * a.scale + bias.at(a, j - pos[r], head[r] - hk * a.G, hk * a.G) : -INFINITY;
+                        top = fmaxf(top, x[r][c]);
+                    }
+                    const float to = fmaxf(le[r], row_max(top)), ref = to == -INFINITY ? 0.f : to;
+                    float sum = 0.f;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) sum += expf(x[r][c] - ref);
+                    l[r] = l[r] * expf(le[r] - ref) + row_sum(sum);
+                    le[r] = to;
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                le[r] = l[r] != 0.f ? le[r] : INFINITY;
+                weight[r] = l[r] != 0.f ? 1.f / l[r] : 1.f;
+            }
+        }
         const int cnt = bt.count(), t0 = static_cast<int>(static_cast<long long>(cnt) * sp / splits),
                   t1 = static_cast<int>(static_cast<long long>(cnt) * (sp + 1) / splits);
         for (int t = t0; t < t1; ++t) {
@@ -343,7 +384,7 @@ __global__ void __launch_bounds__(kThreads)
                     float ds = 0.f;
                     if (live[r] && band_sees(a, pos[r], j, klen)) {
                         const float s = x[r][c] * a.scale + bias.at(a, j - pos[r], head[r] - hk * a.G, hk * a.G);
-                        ds = expf(s - le[r]) * (y[r][c] - de[r]);
+                        ds = expf(s - le[r]) * weight[r] * (y[r][c] - de[r]);
                     }
                     Ps[(4 * ty + r) * kPL + tx + 16 * c] = ds;
                 }
@@ -381,6 +422,7 @@ __global__ void __launch_bounds__(kThreads)
     for (int r = 0; r < 4; ++r) {
         const int row = r0 + 4 * ty + r;
         if (row >= rows) continue;
+        if (tx == 0 && sp == 0) refs[(static_cast<long long>(n) * a.Hq + head[r]) * a.Lq + row / a.G] = make_float2(le[r], weight[r]);
         if (splits > 1)
             store_rows<float, DP>(part + sp * band_rows(a) * a.D + dense(row), a.D, o, r, tx, a.scale);
         else
@@ -391,7 +433,7 @@ __global__ void __launch_bounds__(kThreads)
 // gk and gv of 64 keys over a range of the queries that see them.
 template <typename T, int DP>
 __global__ void __launch_bounds__(kThreads)
-    simt_grad_kv_kernel(BandArgs a, int blocks, int splits, int floats, const float* __restrict__ lse, const T* __restrict__ gout,
+    simt_grad_kv_kernel(BandArgs a, int blocks, int splits, int floats, const float2* __restrict__ refs, const T* __restrict__ gout,
                         const float* __restrict__ delta, T* __restrict__ gk, T* __restrict__ gv, float* __restrict__ part) {
     constexpr int LD = DP + 4;
     extern __shared__ __align__(16) float smem[];
@@ -434,13 +476,14 @@ __global__ void __launch_bounds__(kThreads)
             const int row = r0 + 4 * ty + r, i = row / a.G, h = hk * a.G + row % a.G, pos = start + i;
             const bool live = row < rhi;
             const long long at = (static_cast<long long>(n) * a.Hq + h) * a.Lq + i;
-            const float le = live ? band_lse_ref(lse[at]) : 0.f, de = live ? delta[at] : 0.f;
+            const float2 ref = live ? refs[at] : make_float2(0.f, 1.f);
+            const float de = live ? delta[at] : 0.f;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const int j = j0 + tx + 16 * c;
                 float p = 0.f;
                 if (live && band_sees(a, pos, j, klen))
-                    p = expf(x[r][c] * a.scale + bias.at(a, j - pos, h - hk * a.G, hk * a.G) - le);
+                    p = expf(x[r][c] * a.scale + bias.at(a, j - pos, h - hk * a.G, hk * a.G) - ref.x) * ref.y;
                 Ps[(4 * ty + r) * kPL + tx + 16 * c] = p;
                 Ds[(4 * ty + r) * kPL + tx + 16 * c] = p == 0.f ? 0.f : p * (y[r][c] - de);
             }
@@ -520,13 +563,14 @@ int kv_splits(const BandArgs& a) {
     return split_count(ctas, ((a.sinks ? static_cast<long long>(a.Lq) : reach) * a.G + kB - 1) / kB);
 }
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
-// Workspace of the backward: delta, parts (grad_q's, then grad_kv's in the same place), diagonal sums, their sums by head.
+// Workspace of the backward: delta, refs, parts (grad_q's, then grad_kv's in the same place), diagonal sums, their sums by head.
 struct Workspace {
-    size_t delta, part, diag, sums;
+    size_t delta, refs, part, diag, sums;
     explicit Workspace(const BandArgs& a) {
         const int sq = simt_splits(a), sk = kv_splits(a);
         const size_t nq = static_cast<size_t>(band_rows(a)) * a.D, nk = static_cast<size_t>(a.N) * a.Lk * a.Hk * a.D;
         delta = up256(static_cast<size_t>(band_rows(a)) * sizeof(float));
+        refs = up256(static_cast<size_t>(band_rows(a)) * sizeof(float2));
         part = up256(std::max(sq > 1 ? nq * sq : 0, sk > 1 ? 2 * nk * sk : 0) * sizeof(float));
         const size_t ctas = static_cast<size_t>(a.N) * a.Hk * simt_row_blocks(a) * sq;
         diag = a.nb ? up256(ctas * a.G * (2 * a.M + 1) * sizeof(float)) : 0;
@@ -546,7 +590,8 @@ cudaError_t backward_typed(const BandArgs& a, const void* out, const float* lse,
     const Workspace w(a);
     char* at = static_cast<char*>(ws);
     float* delta = reinterpret_cast<float*>(at);
-    float* part = reinterpret_cast<float*>(at += w.delta);
+    float2* refs = reinterpret_cast<float2*>(at += w.delta);
+    float* part = reinterpret_cast<float*>(at += w.refs);
     float* diag = reinterpret_cast<float*>(at += w.part);
     float* sums = reinterpret_cast<float*>(at += w.diag);
     const int blocks = simt_row_blocks(a), sq = simt_splits(a), sk = kv_splits(a), floats = simt_table(a);
@@ -558,13 +603,13 @@ cudaError_t backward_typed(const BandArgs& a, const void* out, const float* lse,
     if (e != cudaSuccess) return e;
     const long long ctas = static_cast<long long>(a.N) * a.Hk * blocks * sq;
     simt_grad_q_kernel<T, DP><<<static_cast<unsigned>(ctas), kThreads, smem_q, stream>>>(
-        a, blocks, sq, floats, static_cast<const T*>(out), lse, static_cast<const T*>(gout), static_cast<T*>(gq), delta, part, diag);
+        a, blocks, sq, floats, static_cast<const T*>(out), lse, static_cast<const T*>(gout), static_cast<T*>(gq), delta, refs, part, diag);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const long long nq = band_rows(a) * a.D, nk = static_cast<long long>(a.N) * a.Lk * a.Hk * a.D;
     if (sq > 1 && (e = launch_sum_parts<T>(part, sq, nq, nq, gq, stream)) != cudaSuccess) return e;
     const int kblocks = (a.Lk + kB - 1) / kB;
     simt_grad_kv_kernel<T, DP><<<static_cast<unsigned>(static_cast<long long>(a.N) * a.Hk * kblocks * sk), kThreads, smem_kv, stream>>>(
-        a, kblocks, sk, floats, lse, static_cast<const T*>(gout), delta, static_cast<T*>(gk), static_cast<T*>(gv), part);
+        a, kblocks, sk, floats, refs, static_cast<const T*>(gout), delta, static_cast<T*>(gk), static_cast<T*>(gv), part);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (sk > 1) {
         if ((e = launch_sum_parts<T>(part, sk, 2 * nk, nk, gk, stream)) != cudaSuccess) return e;
@@ -585,7 +630,7 @@ int simt_splits(const BandArgs& a) {
 }
 size_t band_simt_backward_workspace(const BandArgs& a) {
     const Workspace w(a);
-    return w.delta + w.part + w.diag + w.sums;
+    return w.delta + w.refs + w.part + w.diag + w.sums;
 }
 
 cudaError_t launch_band_simt_forward(const BandArgs& a, void* out, float* lse, void* ws, cudaStream_t stream) {

@@ -496,12 +496,14 @@ int dcn4_band_forward(const dcn4_band_params* p, const void* q, const void* k, c
                       const int* buckets, const int* q_start, const int* q_len, const int* k_len, void* out, float* lse,
                       void* workspace, size_t workspace_bytes, void* stream);
 
-/* Bytes of device workspace dcn4_band_backward needs (fp32: two numbers per query
+/* Bytes of device workspace dcn4_band_backward needs (fp32: three numbers per query
  * and head, partial gradients where few keys face many queries, and with a bias the
  * sums of its gradient by relative position); 0 if p is invalid. */
 size_t dcn4_band_backward_workspace_size(const dcn4_band_params* p);
 
-/* Backward for grad_out, from the out and lse of the forward: with D_i = <grad_out_i, out_i>,
+/* Backward for grad_out, from the out and lse of the forward (where |lse_i| is above
+ * 512, too far from 0 to keep the log of a sum in 32 bits, the row's maximum and sum are
+ * taken anew): with D_i = <grad_out_i, out_i>,
  * p_ij = e^{s_ij - lse_i} and d_ij = p_ij (<grad_out_i, v_j> - D_i),
  *     grad_q_i = scale sum_j d_ij k_j,   grad_k_j = scale sum_i d_ij q_i,   grad_v_j = sum_i p_ij grad_out_i,
  *     grad_bias[b, h] = sum of d_ij over the pairs of bucket b and head h

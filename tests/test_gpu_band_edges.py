@@ -7,7 +7,7 @@ import torch
 
 from _band import E32, check
 from _band_far import far_reference
-from test_gpu_band import case, compare, dcn, make, run  # noqa: F401  (dcn is a fixture)
+from test_gpu_band import DTYPES, case, compare, dcn, make, run  # noqa: F401  (dcn is a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -58,7 +58,7 @@ def far_compare(dcn, c, t, s, es, names, loose=1.0):  # noqa: F811
         part = r[name + "_tol"].median() / r[name].abs().mean()
         assert part < loose, f"{name}: a bound of {float(part):.2f} of the values says nothing"
         check(name, got[name], r[name], r[name + "_tol"])
-    return got
+    return got, r
 
 
 def rel_of(c):
@@ -71,20 +71,20 @@ COMMON = [dict(Lq=150, Lk=150, Hq=2, Hk=1, D=64), dict(Lq=64, Lk=900, Hq=2, Hk=2
           dict(Lq=300, Lk=300, Hq=2, Hk=1, D=64, nb=4, M=16), dict(Lq=130, Lk=130, Hq=24, Hk=1, D=40, nb=4, M=16)]
 
 
-def common_part(dtype, i, c=None):
+def common_part(dtype, i, c=None, sign=1):
     """A case (of COMMON), its tensors and its scores."""
-    c = case(dtype, 1, scale=0.25, right=0, **(c or COMMON[i]))
+    c = case(dtype, 1, scale=0.25 * sign, right=0, **(c or COMMON[i]))
     t = make(c, i)
     gen = torch.Generator().manual_seed(i)
     for x in ("q", "k"):
         t[x] = torch.randint(-1, 2, t[x].shape, generator=gen).to(t[x].dtype)
-        t[x][..., 0] = 2048.0
+        t[x][..., 0] = 2048.0 if x == "q" else 2048.0 * sign
     b = 0.0
     if c.get("nb"):
         t["bias"] = torch.randint(-8, 9, t["bias"].shape, generator=gen).to(t["bias"].dtype) / 4
         b = t["bias"].double()[t["buckets"].long()[rel_of(c).clamp(-c["M"], c["M"]) + c["M"]]].permute(2, 0, 1)
     kk = t["k"].double().repeat_interleave(c["Hq"] // c["Hk"], 2)
-    s = torch.einsum("nihd,njhd->nhij", t["q"].double(), kk) * 0.25 + b
+    s = torch.einsum("nihd,njhd->nhij", t["q"].double(), kk) * c["scale"] + b
     return c, t, torch.where(rel_of(c) <= 0, s, torch.full_like(s, -torch.inf))
 
 
@@ -94,6 +94,19 @@ def test_scores_with_a_large_common_part(dcn, dtype, i):  # noqa: F811
     """Differences of scores are below 100, and formed to 32 bits."""
     c, t, s = common_part(dtype, i)
     far_compare(dcn, c, t, s, 100 * E32, ["out"])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("i,sign", [(i, 1) for i in range(len(COMMON))] + [(0, -1), (3, -1)])
+def test_gradients_of_scores_with_a_large_common_part(dcn, dtype, i, sign):  # noqa: F811
+    """One log sum in 32 bits is off by 0.06 at 2^20.  (The first entries of q and k, 2048, have their gradients
+    from sums that cancel: bounds above the values, as they are 2048 times the rest's.)"""
+    c, t, s = common_part(dtype, i, sign=sign)
+    got, r = far_compare(dcn, c, t, s, 100 * E32, ["gv"] + (["gb"] if c.get("nb") and c["Hq"] < 24 else []))
+    for name in ("gq", "gk"):
+        tol, ref = r[name + "_tol"], r[name]
+        assert tol[..., 1:].median() < ref[..., 1:].abs().mean()
+        check(name, got[name], ref, tol)
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
@@ -135,3 +148,42 @@ def test_a_value_that_no_query_sees_may_not_be_finite_behind_k_len(dcn):  # noqa
     """Infinities ahead of a token are kept out by k_len."""
     c = case("bf16", 2, 1, 200, 4, 2, 64, right=0, k_len=[150, 77], q_start=[149, 76], poison=True)
     compare(dcn, c, backward=False)
+
+
+# Rows that see only keys with the type's lowest bias: uniform over them.  Few keys and many (grad_q goes over the
+# keys once or twice), heads of up to 64 and up to 128, a head group of 24.
+LOWEST = [dict(Lq=150, Lk=150, Hq=2, Hk=1, D=64, left=60, right=60), dict(Lq=900, Lk=900, Hq=2, Hk=2, D=32),
+          dict(Lq=70, Lk=700, Hq=2, Hk=1, D=128), dict(Lq=130, Lk=130, Hq=24, Hk=1, D=40)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("i", range(len(LOWEST)))
+def test_rows_of_lowest_biases(dcn, dtype, i):  # noqa: F811
+    c = case(dtype, 1, nb=4, M=100, **LOWEST[i])
+    t = make(c, i)
+    low = torch.finfo(DTYPES[dtype]).min
+    t["bias"] = torch.full((4, c["Hq"]), low, dtype=DTYPES[dtype])
+    t["bias"][3] = 0.5
+    t["buckets"] = torch.zeros(201, dtype=torch.int32)
+    t["buckets"][130:140] = 3
+    rel = rel_of(c)
+    seen = (-rel <= c.get("left", 10**9)) & (rel <= c.get("right", 10**9))
+    normal = seen & (rel >= 30) & (rel < 40)
+    D = c["D"]
+    kk = t["k"].double().repeat_interleave(c["Hq"] // c["Hk"], 2)
+    x = torch.einsum("nihd,njhd->nhij", t["q"].double(), kk) * D ** -0.5
+    # beside a key of another bucket the lowest ones vanish; on their own, fp16's keep their scores (2^-9 of
+    # rounding each at 65504, and the products'), the other types' scores all are the lowest value itself
+    flat = torch.zeros_like(x) if dtype != "f16" else x
+    s = torch.where(normal, x, torch.where(normal.any(-1, keepdim=True), torch.full_like(x, -torch.inf), flat))
+    s = torch.where(seen, s, torch.full_like(x, -torch.inf))
+    es = (D + 4) * E32 * 60 + (2.0 ** -9 if dtype == "f16" else 0.0)  # sum |q k| / sqrt(D) is below 60 here
+    assert float(torch.einsum("nihd,njhd->nhij", t["q"].double().abs(), kk.abs()).amax()) * D ** -0.5 < 60
+    got, r = far_compare(dcn, c, t, s, es, ["out", "gq", "gk", "gv"])
+    if c["Hq"] < 24:  # 0 but for rounding: all keys that count in a row are of one bucket
+        check("gb", got["gb"], r["gb"], r["gb_tol"])
+    last = got["out"][0, -1, 0].double().cpu()  # sees no key of bucket 3
+    if dtype != "f16":
+        mean = t["v"][0, seen[-1], 0].double().mean(0)
+        # |out| is below 1, and a probability off by half a step, of |v| below 5
+        assert float(mean.abs().max()) < 1 and ((last - mean).abs() <= 4 * torch.finfo(DTYPES[dtype]).eps).all()
