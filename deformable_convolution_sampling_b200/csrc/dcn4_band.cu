@@ -186,8 +186,7 @@ cudaError_t band_status(unsigned* status, bool reset) {
 }
 
 size_t band_backward_workspace_bytes(const BandArgs& a) {
-    if (band_bwd_tc_fits(a)) return band_bwd_tc_workspace(a);
-    return band_simt_backward_workspace(a);
+    return a.dtype == 0 ? band_simt_backward_workspace(a) : band_bwd_tc_workspace(a);
 }
 
 cudaError_t launch_band_forward(const BandArgs& a, void* out, float* lse, void* ws, cudaStream_t stream) {
@@ -197,7 +196,7 @@ cudaError_t launch_band_forward(const BandArgs& a, void* out, float* lse, void* 
 
 cudaError_t launch_band_backward(const BandArgs& a, const void* out, const float* lse, const void* gout, void* gq,
                                  void* gk, void* gv, void* gbias, void* ws, cudaStream_t stream) {
-    if (band_bwd_tc_fits(a)) return launch_band_bwd_tc(a, out, lse, gout, gq, gk, gv, gbias, ws, stream);
+    if (a.dtype != 0) return launch_band_bwd_tc(a, out, lse, gout, gq, gk, gv, gbias, ws, stream);
     return launch_band_simt_backward(a, out, lse, gout, gq, gk, gv, gbias, ws, stream);
 }
 

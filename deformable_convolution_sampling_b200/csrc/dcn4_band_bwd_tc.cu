@@ -52,10 +52,10 @@ __device__ unsigned g_band_bwd_status;
 __host__ __device__ inline int table_floats(int M) { return 2 * (M + kTableExtra) + 1; }
 __host__ __device__ inline int padded_queries(int Lq) { return (Lq + kTile - 1) / kTile * kTile; }
 
-// Bias of `heads` heads from h0 on by relative position, clamped.
+// Bias of `heads` heads from h0 on by relative position, clamped; thread `at` of `threads`.
 template <typename T>
-__device__ __forceinline__ void fill_table(const BandArgs& a, float* table, int floats, int h0, int heads, int threads) {
-    for (int e = threadIdx.x; e < heads * floats; e += threads) {
+__device__ __forceinline__ void fill_table(const BandArgs& a, float* table, int floats, int h0, int heads, int at, int threads) {
+    for (int e = at; e < heads * floats; e += threads) {
         const int g = e / floats, rel = e - g * floats - a.M - kTableExtra;
         const int bk = __ldg(a.buckets + max(-a.M, min(rel, a.M)) + a.M);
         table[e] = static_cast<unsigned>(bk) < static_cast<unsigned>(a.nb)
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(QCfg<NB, BIAS>::threads, 1)
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&taddr_s)), "r"(kTmem));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
-    if (BIAS) fill_table<T>(a, table, floats, h0, pack, QCfg<NB, BIAS>::threads);
+    if (BIAS) fill_table<T>(a, table, floats, h0, pack, tid, QCfg<NB, BIAS>::threads);
     tc_fence_before();
     const bool far = uniform(__syncthreads_or(band_far(st.x))) != 0;  // some row's sum is not in its lse
     tc_fence_after();
@@ -558,7 +558,9 @@ struct KvCfg {
     static constexpr size_t smem = 1024 + 2 * NB * kTcBlock + slots * (stage + stat) + (BIAS ? kDiagWarps * kDiagBuf * sizeof(float) : 0);
 };
 
-template <typename T, int NB, bool BIAS, bool EXACT>
+// WHOLE: the bias tables of all heads that share the key head are held at once; otherwise each parity holds its
+// present head's and reloads it at the next (as a branch in one kernel that cost the others 18 %).
+template <typename T, int NB, bool BIAS, bool EXACT, bool WHOLE>
 __global__ void __launch_bounds__(KvCfg<NB, BIAS>::threads, 1)
     grad_kv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_g,
                    const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, BandArgs a, KvShape sh,
@@ -614,7 +616,7 @@ __global__ void __launch_bounds__(KvCfg<NB, BIAS>::threads, 1)
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&taddr_s)), "r"(kTmem));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
-    if (BIAS) fill_table<T>(a, table, sh.floats, hk * a.G, a.G, C::threads);
+    if (BIAS && WHOLE) fill_table<T>(a, table, sh.floats, hk * a.G, a.G, tid, C::threads);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -756,7 +758,7 @@ __global__ void __launch_bounds__(KvCfg<NB, BIAS>::threads, 1)
         const bool far = __any_sync(0xffffffffu, some);
         const int kw = k0 + (warp & 3) * 32;  // this warp's keys
         Diagonals dg;
-        int dg_head = -1;
+        int dg_head = -1, tab_head = -1;
         float* diag_w = diag + (static_cast<long long>(blockIdx.x) * kDiagWarps + warp) * a.G * (2 * a.M + 1);
         if (BIAS) {  // what no store below reaches is 0
             for (int e = lane; e < a.G * (2 * a.M + 1); e += 32) diag_w[e] = 0.f;
@@ -772,6 +774,13 @@ __global__ void __launch_bounds__(KvCfg<NB, BIAS>::threads, 1)
             int ca, cb;
             const int g = st_w.g, i = (q0 + st_w.r) * kTile, ic = i + c * kTcChunk;
             st_w.next();
+            if (!WHOLE && g != tab_head) {  // (also by a warp whose wait gave up: the others' barriers count it)
+                asm volatile("bar.sync %0, 256;" ::"r"(1 + w) : "memory");  // the last head's reads are done
+                fill_table<T>(a, table + w * sh.floats, sh.floats, hk * a.G + g, 1, c * kTcRows + row, 256);
+                asm volatile("bar.sync %0, 256;" ::"r"(1 + w) : "memory");
+                tab_head = g;
+            }
+            if (!WHOLE && !ok) continue;
             if (BIAS && warp_live && g != dg_head) {
                 if (dg_head >= 0) dg.finish(lane);
                 dg.start(diag_w + g * (2 * a.M + 1));
@@ -781,7 +790,10 @@ __global__ void __launch_bounds__(KvCfg<NB, BIAS>::threads, 1)
             const bool on = warp_live && c >= ca && c < cb;
             // the scores, and (the loads' own barrier) the queries' stats
             ok = warp_wait(&full[s], (t / kSlots) & 1, abort) && warp_wait(&s_full[w], (t >> 1) & 1, abort);
-            if (!ok) break;
+            if (!ok) {
+                if (WHOLE) break;
+                continue;
+            }
             tc_fence_after();
             uint32_t x[32], y[32];
             if (on) {
@@ -791,7 +803,7 @@ __global__ void __launch_bounds__(KvCfg<NB, BIAS>::threads, 1)
                 if (BIAS) {
                     // relative positions k0 - (start + ic + 31) ... k1 - 1 - (start + ic)
                     const int side = k0 - (start + ic + kTcChunk - 1) >= a.M ? 1 : k1 - 1 - (start + ic) <= -a.M ? -1 : 0;
-                    const float* tab = table + g * sh.floats;
+                    const float* tab = table + (WHOLE ? g : w) * sh.floats;
                     if (side) {
                         const float bb = tab[side > 0 ? sh.floats - 1 : 0];
 #pragma unroll
@@ -819,7 +831,10 @@ __global__ void __launch_bounds__(KvCfg<NB, BIAS>::threads, 1)
                     for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * __shfl_sync(0xffffffffu, weight, e));
                 }
             }
-            if (!(ok = warp_wait(&e_full[w], (t >> 1) & 1, abort))) break;
+            if (!(ok = warp_wait(&e_full[w], (t >> 1) & 1, abort))) {
+                if (WHOLE) break;
+                continue;
+            }
             tc_fence_after();
             if (on) {
                 const float4* st = stat_s + s * (C::stat / 16) + c * (kTcChunk / 2);
@@ -944,6 +959,20 @@ __global__ void __launch_bounds__(256) kv_join_kernel(BandArgs a, KvShape sh, in
     *reinterpret_cast<uint2*>(to) = make_uint2(pack2<T>(s.x, s.y), pack2<T>(s.z, s.w));
 }
 
+// How the rows of grad_q map to its CTAs: two tiles of `tq` queries of `pack` heads each.
+struct RowShape {
+    int pack, tq, blocks;
+};
+// Whether the bias tables of all heads that share a key head fit shared memory beside the tiles.  If not,
+// grad_q's tiles are of one head, and grad_kv, which goes head by head, reloads its table at each.
+bool whole_tables(const BandArgs& a) {
+    return !a.nb || static_cast<size_t>(a.G) * table_floats(a.M) * sizeof(float) <= kTableBytes;
+}
+RowShape row_shape(const BandArgs& a) {
+    const int pack = whole_tables(a) ? a.G : 1, tq = kTcRows / pack;
+    return {pack, tq, (a.Lq + 2 * tq - 1) / (2 * tq)};
+}
+
 KvShape kv_shape(const BandArgs& a) {
     KvShape s;
     s.floats = a.nb ? table_floats(a.M) : 0;
@@ -966,14 +995,6 @@ KvShape kv_shape(const BandArgs& a) {
 
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 size_t stats_bytes(const BandArgs& a) { return up256(static_cast<size_t>(a.N) * a.Hq * padded_queries(a.Lq) * sizeof(float2)); }
-// How the rows of grad_q map to its CTAs: two tiles of `tq` queries of `pack` heads each.
-struct RowShape {
-    int pack, tq, blocks;
-};
-RowShape row_shape(const BandArgs& a) {
-    const int tq = kTcRows / a.G;
-    return {a.G, tq, (a.Lq + 2 * tq - 1) / (2 * tq)};
-}
 size_t far_bytes(const BandArgs& a) {
     const RowShape r = row_shape(a);
     return up256(static_cast<size_t>(a.N) * (a.Hq / r.pack) * r.blocks * sizeof(int));
@@ -999,11 +1020,12 @@ cudaError_t launch(const BandArgs& a, const void* out, const float* lse, const v
     float* diag = reinterpret_cast<float*>(at += part_bytes(a, kv));
     float* sums = reinterpret_cast<float*>(at += diag_bytes(a, kv));
     const auto [pack, tq, blocks] = row_shape(a);
+    const bool whole = !BIAS || whole_tables(a);
     const long long dense = static_cast<long long>(a.Hq) * a.D;
-    const size_t smem_q = QCfg<NB, BIAS>::smem + (BIAS ? static_cast<size_t>(a.G) * kv.floats * sizeof(float) : 0),
-                 smem_kv = KvCfg<NB, BIAS>::smem + (BIAS ? static_cast<size_t>(a.G) * kv.floats * sizeof(float) : 0);
+    const size_t smem_q = QCfg<NB, BIAS>::smem + (BIAS ? static_cast<size_t>(pack) * kv.floats * sizeof(float) : 0),
+                 smem_kv = KvCfg<NB, BIAS>::smem + (BIAS ? static_cast<size_t>(whole ? a.G : 2) * kv.floats * sizeof(float) : 0);
     cudaError_t e = allow_smem<grad_q_kernel<T, NB, BIAS, EXACT>>();
-    if (e == cudaSuccess) e = allow_smem<grad_kv_kernel<T, NB, BIAS, EXACT>>();
+    if (e == cudaSuccess) e = whole ? allow_smem<grad_kv_kernel<T, NB, BIAS, EXACT, true>>() : allow_smem<grad_kv_kernel<T, NB, BIAS, EXACT, !BIAS>>();
     if (e != cudaSuccess) return e;
     CUtensorMap mq, mg, mk, mv, mq1, mg1, mk1, mv1;
     if (!make_map(&mq, a.dtype, a.q, a.N, a.Lq, a.Hq, a.D, a.q_batch, a.q_row, pack, tq) ||
@@ -1025,7 +1047,8 @@ cudaError_t launch(const BandArgs& a, const void* out, const float* lse, const v
     grad_q_kernel<T, NB, BIAS, EXACT><<<static_cast<unsigned>(static_cast<long long>(a.N) * (a.Hq / pack) * blocks), QCfg<NB, BIAS>::threads, smem_q, stream>>>(
         mq, mg, mk, mv, a, pack, tq, blocks, kv.floats, stats, weights, far_blocks, static_cast<T*>(gq));
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    grad_kv_kernel<T, NB, BIAS, EXACT><<<static_cast<unsigned>(static_cast<long long>(a.N) * a.Hk * kv.items()), KvCfg<NB, BIAS>::threads, smem_kv, stream>>>(
+    const auto kv_kernel = whole ? grad_kv_kernel<T, NB, BIAS, EXACT, true> : grad_kv_kernel<T, NB, BIAS, EXACT, !BIAS>;
+    kv_kernel<<<static_cast<unsigned>(static_cast<long long>(a.N) * a.Hk * kv.items()), KvCfg<NB, BIAS>::threads, smem_kv, stream>>>(
         mq1, mg1, mk1, mv1, a, kv, stats, weights, far_blocks, blocks * (a.G / pack), static_cast<T*>(gk), static_cast<T*>(gv), part, diag);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (kv.split()) {
@@ -1038,11 +1061,6 @@ cudaError_t launch(const BandArgs& a, const void* out, const float* lse, const v
 }
 
 }  // namespace
-
-// The bias tables of all heads that share a key head have to fit shared memory.
-bool band_bwd_tc_fits(const BandArgs& a) {
-    return a.dtype != 0 && (!a.nb || static_cast<size_t>(a.G) * table_floats(a.M) * sizeof(float) <= kTableBytes);
-}
 
 size_t band_bwd_tc_workspace(const BandArgs& a) {
     const KvShape kv = kv_shape(a);

@@ -65,14 +65,13 @@ bool band_few_fits(const BandArgs& a);
 size_t band_few_part_bytes(const BandArgs& a);
 cudaError_t launch_band_few(const BandArgs& a, void* out, float* lse, void* ws, cudaStream_t stream);
 
-// 16-bit backward on the tensor cores (dcn4_band_bwd_tc.cu), where it fits.
-bool band_bwd_tc_fits(const BandArgs& a);
+// 16-bit backward on the tensor cores (dcn4_band_bwd_tc.cu).
 size_t band_bwd_tc_workspace(const BandArgs& a);
 cudaError_t launch_band_bwd_tc(const BandArgs& a, const void* out, const float* lse, const void* gout, void* gq, void* gk, void* gv,
                                void* gbias, void* ws, cudaStream_t stream);
 cudaError_t band_bwd_status(unsigned* status, bool reset);
 
-// On the fp32 pipes (dcn4_band_simt.cu): fp32 forward, every type's backward.
+// fp32, on the fp32 pipes (dcn4_band_simt.cu).
 int simt_row_blocks(const BandArgs& a);
 int simt_splits(const BandArgs& a);
 cudaError_t launch_band_simt_forward(const BandArgs& a, void* out, float* lse, void* ws, cudaStream_t stream);

@@ -1,5 +1,4 @@
-// dcn4_band_simt.cu — the band attention on the fp32 pipes: fp32, and the backward of
-// 16-bit types whose bias tables do not fit the tensor-core kernels.
+// dcn4_band_simt.cu — the band attention in fp32, on the fp32 pipes.
 //
 // Forward, one pass over the visible keys with a running maximum m and sum l:
 //     s = scale q.k + b,  m' = max(m, s),  l = l e^(m-m') + e^(s-m'),  o likewise;  out = o / l,
@@ -639,17 +638,8 @@ cudaError_t launch_band_simt_forward(const BandArgs& a, void* out, float* lse, v
 
 cudaError_t launch_band_simt_backward(const BandArgs& a, const void* out, const float* lse, const void* gout, void* gq,
                                       void* gk, void* gv, void* gbias, void* ws, cudaStream_t stream) {
-    const bool wide = a.D > 64;
-#define DCN4_BAND_BWD(T)                                                                                             \
-    (wide ? backward_typed<T, 128>(a, out, lse, gout, gq, gk, gv, gbias, ws, stream)                                 \
-          : backward_typed<T, 64>(a, out, lse, gout, gq, gk, gv, gbias, ws, stream))
-    switch (a.dtype) {
-        case 0: return DCN4_BAND_BWD(float);
-        case 1: return DCN4_BAND_BWD(__half);
-        case 2: return DCN4_BAND_BWD(__nv_bfloat16);
-        default: return cudaErrorInvalidValue;
-    }
-#undef DCN4_BAND_BWD
+    return a.D > 64 ? backward_typed<float, 128>(a, out, lse, gout, gq, gk, gv, gbias, ws, stream)
+                    : backward_typed<float, 64>(a, out, lse, gout, gq, gk, gv, gbias, ws, stream);
 }
 
 }  // namespace dcn4

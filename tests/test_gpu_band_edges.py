@@ -102,7 +102,7 @@ def test_gradients_of_scores_with_a_large_common_part(dcn, dtype, i, sign):  # n
     """One log sum in 32 bits is off by 0.06 at 2^20.  (The first entries of q and k, 2048, have their gradients
     from sums that cancel: bounds above the values, as they are 2048 times the rest's.)"""
     c, t, s = common_part(dtype, i, sign=sign)
-    got, r = far_compare(dcn, c, t, s, 100 * E32, ["gv"] + (["gb"] if c.get("nb") and c["Hq"] < 24 else []))
+    got, r = far_compare(dcn, c, t, s, 100 * E32, ["gv"] + (["gb"] if c.get("nb") else []))
     for name in ("gq", "gk"):
         tol, ref = r[name + "_tol"], r[name]
         assert tol[..., 1:].median() < ref[..., 1:].abs().mean()
@@ -180,10 +180,48 @@ def test_rows_of_lowest_biases(dcn, dtype, i):  # noqa: F811
     es = (D + 4) * E32 * 60 + (2.0 ** -9 if dtype == "f16" else 0.0)  # sum |q k| / sqrt(D) is below 60 here
     assert float(torch.einsum("nihd,njhd->nhij", t["q"].double().abs(), kk.abs()).amax()) * D ** -0.5 < 60
     got, r = far_compare(dcn, c, t, s, es, ["out", "gq", "gk", "gv"])
-    if c["Hq"] < 24:  # 0 but for rounding: all keys that count in a row are of one bucket
-        check("gb", got["gb"], r["gb"], r["gb_tol"])
+    # 0 but for rounding: all keys that count in a row are of one bucket
+    check("gb", got["gb"], r["gb"], r["gb_tol"])
     last = got["out"][0, -1, 0].double().cpu()  # sees no key of bucket 3
     if dtype != "f16":
         mean = t["v"][0, seen[-1], 0].double().mean(0)
         # |out| is below 1, and a probability off by half a step, of |v| below 5
         assert float(mean.abs().max()) < 1 and ((last - mean).abs() <= 4 * torch.finfo(DTYPES[dtype]).eps).all()
+
+
+# Groups whose heads' bias tables fit shared memory together, and groups whose do not.
+GROUPS = [dict(Hq=2, Hk=1, M=32), dict(Hq=16, Hk=1, M=128), dict(Hq=16, Hk=2, M=512), dict(Hq=4, Hk=1, M=1024), dict(Hq=128, Hk=1, M=64)]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("i", range(len(GROUPS)))
+def test_bias_gradient_does_not_take_up_the_rounding_of_out(dcn, dtype, i):  # noqa: F811
+    """Values of 1 and the next number above it, a quarter of them the latter, and uniform probabilities: out
+    rounds down by a quarter of a step in every row, and delta from it would be off by the same amount in all of
+    them: a sum of over a hundred times what the bias gradient may be off by."""
+    # (few keys for fp16, whose steps are near those of fp32 sums over many)
+    c = case(dtype, 1, 600, 150 if dtype == "f16" else 600, D=64, nb=4, **GROUPS[i])
+    t = make(c, i)
+    t["q"].zero_()
+    t["bias"].zero_()
+    t["v"][:] = 1.0
+    t["v"][:, ::4] = 1 + torch.finfo(DTYPES[dtype]).eps
+    t["g"][:] = 1.0
+    s = torch.zeros(1, c["Hq"], c["Lq"], c["Lk"], dtype=torch.float64)
+    which = t["buckets"].long()[rel_of(c).clamp(-c["M"], c["M"]) + c["M"]]
+    r = far_reference(t["q"], t["k"], t["v"], t["g"], s, 0.0, 64 ** -0.5, dtype, (which, c["nb"]))
+    share = torch.bincount(which.reshape(-1), minlength=c["nb"]) / c["Lk"]  # rows' probabilities in each bucket
+    off = 64 * torch.finfo(DTYPES[dtype]).eps / 4 * share[:, None]  # what a rounded out would add, about
+    assert (r["gb_tol"] < off / 2).all()
+    check("gb", run(dcn, c, t)[5], r["gb"], r["gb_tol"])
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("c", [dict(Lq=300, Lk=300, Hq=16, Hk=1, D=64, M=128, right=0), dict(Lq=200, Lk=333, Hq=16, Hk=2, D=80, M=512, left=100, right=50, sinks=3),
+                               dict(Lq=700, Lk=130, Hq=6, Hk=1, D=128, M=1024, q_len=[700, 333], k_len=[130, 97], poison=True),
+                               dict(Lq=9, Lk=70, Hq=128, Hk=1, D=16, M=100), dict(Lq=65, Lk=40, Hq=25, Hk=1, D=32, M=100)], ids=str)
+def test_large_groups_with_a_bias(dcn, dtype, c):  # noqa: F811
+    c = case(dtype, 2, nb=12, **c)
+    a, b = compare(dcn, c), run(dcn, c, make(c))
+    for x, y in zip(a, b):
+        assert torch.equal(x, y)
