@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(256) diag_sum_kernel(BandArgs a, unsigned all,
                                                        const float* __restrict__ diag, float* __restrict__ sums) {
     __shared__ float s_part[8][32];
     constexpr int U = 8;  // loads at a time, also in the last batch
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.y, len = 2 * a.M + 1, rel = blockIdx.x * 32 + lane;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.x, len = 2 * a.M + 1, rel = blockIdx.y * 32 + lane;
     const unsigned hk = h / a.G, g = h - hk * a.G, c0 = blockIdx.z * chunk, c1 = min(all, c0 + chunk);
     const long long row = static_cast<long long>(a.G) * len;
     const float* from = diag + static_cast<long long>(g) * len + rel;
@@ -152,7 +152,8 @@ cudaError_t launch_band_bias_sum(const BandArgs& a, int per, int each, const flo
     const int shift = each == 1 ? 0 : 4;  // one sum a CTA, or sixteen
     const unsigned all = static_cast<unsigned>(a.N) * per, batch = 64u >> shift;
     const unsigned chunk = std::max((all + kSumParts * batch - 1) / (kSumParts * batch), 1u) * batch, zs = (all + chunk - 1) / chunk;
-    diag_sum_kernel<<<dim3((2 * a.M + 32) / 32, a.Hq, zs), 256, 0, stream>>>(a, all, per, chunk, shift, diag, sums);
+    // (heads along x: the other dimensions of a grid end at 65535)
+    diag_sum_kernel<<<dim3(a.Hq, (2 * a.M + 32) / 32, zs), 256, 0, stream>>>(a, all, per, chunk, shift, diag, sums);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const dim3 grid(a.Hq, (a.nb + 63) / 64);

@@ -225,3 +225,7 @@ def test_large_groups_with_a_bias(dcn, dtype, c):  # noqa: F811
     a, b = compare(dcn, c), run(dcn, c, make(c))
     for x, y in zip(a, b):
         assert torch.equal(x, y)
+
+
+def test_more_heads_than_a_grid_has_rows(dcn):  # noqa: F811
+    compare(dcn, case("f16", 1, 2, 3, 70000, 70000, 8, nb=2, M=1))
