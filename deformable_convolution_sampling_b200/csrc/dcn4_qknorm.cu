@@ -8,8 +8,9 @@
 //     gw = sum g s x,     gx = s (g w - x s^2 mean(g w x)).
 // The angle is formed and reduced to [-pi, pi] in 64 bits (a position of 10^5
 // times a frequency of 1 leaves 2^-7 of a radian in 32 bits), once per token
-// and pair into shared memory; all heads of the token use it.  Everything else
-// is 32 bits, rounded once.
+// and pair into shared memory; all heads of the token use it.  Its sine and cosine
+// are those of its 32 leading bits and a first-order term of the rest.  Everything
+// else is 32 bits, rounded once.
 //
 // Bound by HBM: x (and g) read once, out (or gx) written once.  A warp takes a few
 // tokens (or some heads of one, where tokens are few) on its own: its lanes form the
@@ -156,7 +157,12 @@ struct Warp {
             const float pos = __ldg(a.pos + (tok + t) * a.axes + (i >= per ? 1 : 0));
             double f = static_cast<double>(pos) * static_cast<double>(__ldg(a.inv_freq + i));
             f -= kTwoPi * rint(f * kInvTwoPi);
-            sincosf(static_cast<float>(f), sn + e, cs + e);
+            // 32 bits of an angle near pi leave up to 2^-23 of it: the rest turns sin and cos to first order
+            const float lead = static_cast<float>(f), rest = static_cast<float>(f - lead);
+            float sine, cosine;
+            sincosf(lead, &sine, &cosine);
+            sn[e] = fmaf(cosine, rest, sine);
+            cs[e] = fmaf(-sine, rest, cosine);
         }
         __syncwarp();
     }

@@ -229,3 +229,23 @@ def test_large_groups_with_a_bias(dcn, dtype, c):  # noqa: F811
 
 def test_more_heads_than_a_grid_has_rows(dcn):  # noqa: F811
     compare(dcn, case("f16", 1, 2, 3, 70000, 70000, 8, nb=2, M=1))
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rotation_keeps_the_angle_beyond_32_bits(dcn, interleaved):  # noqa: F811
+    """A head (2, 0, 0, 0) has a norm of 1 and comes out as 2 cos f and 2 sin f, f near +-pi.  sincosf is good to
+    2 steps (2^-22 of a value at most) and a sum behind it to half of one: 2.5 * 2^-23.  An angle held in 32 bits
+    alone is off by up to 2^-23, which is 2^-23 / sin f of the sine: up to ten times as much here."""
+    pos = torch.arange(100000, dtype=torch.float64)
+    f = torch.remainder(pos + torch.pi, 2 * torch.pi) - torch.pi
+    pos = pos[(f.abs() > 2.9) & (f.abs() < 3.1)].float().cuda()[None]
+    L = pos.shape[1]
+    x = torch.zeros(1, L, 2, 4, device="cuda")
+    x[..., 0] = 2.0
+    inv = torch.tensor([1.0, 0.5], device="cuda")
+    a = (x, x[:, :, :1].contiguous(), None, None, pos, inv)
+    p = dcn.qknorm_params_for(*a, interleaved=interleaved, eps=1e-30)
+    out, _ = dcn.qknorm_forward(p, *a)
+    angle = pos[0].double()
+    for got, ref in ((out[0, :, :, 0], 2 * angle.cos()), (out[0, :, :, 1 if interleaved else 2], 2 * angle.sin())):
+        assert ((got.double() - ref[:, None]).abs() <= 2.5 * 2.0 ** -23 * ref.abs()[:, None]).all()
