@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, kForwardCtas) qknorm_forward_kernel(
 template <typename T, int MODE>
 __global__ void __launch_bounds__(kThreads, kBackwardCtas)
     qknorm_backward_kernel(QkNormArgs a, Shape sh, const T* __restrict__ gqo, const T* __restrict__ gko,
-                           T* __restrict__ gq, T* __restrict__ gk, float* __restrict__ part) {
+                           T* __restrict__ gq, T* __restrict__ gk, double* __restrict__ part) {
     constexpr int E = Elem<T>::per16;
     extern __shared__ __align__(16) float qk_smem[];
     Warp<T, MODE> wp(a, sh, qk_smem);
@@ -396,7 +396,8 @@ __global__ void __launch_bounds__(kThreads, kBackwardCtas)
             }
         }
     }
-    // the CTA's sums: lane groups and warps in a fixed order
+    // the CTA's sums: lane groups and warps in a fixed order, in 64 bits, as the sum of the CTAs' (in 32 bits an fp32
+    // gradient was off by 2.1 times what its rounding alone leaves; what a lane adds up stays in 32)
     if (!part) return;
     float* bufs = qk_smem + kWarps * kMaxPairs * 2;
 #pragma unroll
@@ -409,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, kBackwardCtas)
                 for (int e = 0; e < E / 2; ++e) *reinterpret_cast<float2*>(wp.buf + wp.at[c] * E + 2 * e) = unf2(acc[side][c][e]);
         __syncthreads();
         for (int d = threadIdx.x; d < a.D; d += kThreads) {
-            float s = 0.f;
+            double s = 0.0;
             for (int w = 0; w < kWarps * wp.hpw; ++w) s += bufs[w * a.D + d];
             part[(static_cast<long long>(blockIdx.x) * 2 + side) * a.D + d] = s;
         }
@@ -418,21 +419,21 @@ __global__ void __launch_bounds__(kThreads, kBackwardCtas)
 
 // gw[d] = the sum of the CTAs' parts: a warp per entry.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) qknorm_weights_kernel(const float* __restrict__ part, int ctas, int D,
+__global__ void __launch_bounds__(kThreads) qknorm_weights_kernel(const double* __restrict__ part, int ctas, int D,
                                                                   T* __restrict__ gwq, T* __restrict__ gwk) {
     const int e = blockIdx.x * kWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (e >= 2 * D) return;
-    float s = 0.f;
+    double s = 0.0;
     for (int c = lane; c < ctas; c += 32 * 16) {  // sixteen loads at a time: one batch mostly
-        float v[16];
+        double v[16];
 #pragma unroll
-        for (int u = 0; u < 16; ++u) v[u] = c + 32 * u < ctas ? __ldg(part + static_cast<long long>(c + 32 * u) * 2 * D + e) : 0.f;
+        for (int u = 0; u < 16; ++u) v[u] = c + 32 * u < ctas ? __ldg(part + static_cast<long long>(c + 32 * u) * 2 * D + e) : 0.0;
 #pragma unroll
         for (int u = 0; u < 16; ++u) s += v[u];
     }
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     T* to = e < D ? gwq : gwk;
-    if (lane == 0 && to) to[e < D ? e : e - D] = from_f32<T>(s);
+    if (lane == 0 && to) to[e < D ? e : e - D] = from_f32<T>(static_cast<float>(s));
 }
 
 Shape shape_of(const QkNormArgs& a, int elems, int ctas) {
@@ -476,7 +477,7 @@ template <typename T>
 cudaError_t backward_typed(const QkNormArgs& a, const void* gqo, const void* gko, void* gq, void* gk, void* gwq,
                            void* gwk, void* ws, cudaStream_t stream) {
     const Shape s = shape_of(a, Elem<T>::per16, kBackwardCtas);
-    float* part = (gwq || gwk) ? static_cast<float*>(ws) : nullptr;
+    double* part = (gwq || gwk) ? static_cast<double*>(ws) : nullptr;
     const auto kernel = s.mode == kNone ? qknorm_backward_kernel<T, kNone> : s.mode == kHalves ? qknorm_backward_kernel<T, kHalves>
                         : s.mode == kNeighbours ? qknorm_backward_kernel<T, kNeighbours> : qknorm_backward_kernel<T, kExchange>;
     kernel<<<s.grid, kThreads, smem_bytes(a, s), stream>>>(a, s, static_cast<const T*>(gqo), static_cast<const T*>(gko),
@@ -492,7 +493,7 @@ cudaError_t backward_typed(const QkNormArgs& a, const void* gqo, const void* gko
 
 size_t qknorm_backward_workspace_bytes(const QkNormArgs& a) {
     const Shape s = shape_of(a, a.dtype == 0 ? 4 : 8, kBackwardCtas);
-    return (static_cast<size_t>(s.grid) * 2 * a.D * sizeof(float) + 255) / 256 * 256;
+    return (static_cast<size_t>(s.grid) * 2 * a.D * sizeof(double) + 255) / 256 * 256;
 }
 
 cudaError_t launch_qknorm_forward(const QkNormArgs& a, void* qo, void* ko, cudaStream_t stream) {

@@ -564,7 +564,7 @@ int dcn4_qknorm_forward(const dcn4_qknorm_params* p, const void* q, const void* 
                         const float* pos, const float* inv_freq, void* q_out, void* k_out, void* stream);
 
 /* Bytes of device workspace dcn4_qknorm_backward needs when a weight's gradient is
- * wanted (fp32 sums of each CTA); 0 if p is invalid. */
+ * wanted (64-bit sums of each CTA); 0 if p is invalid. */
 size_t dcn4_qknorm_backward_workspace_size(const dcn4_qknorm_params* p);
 
 /* Backward: grad_q and grad_k from the gradients of q_out and k_out (the inputs are

@@ -249,3 +249,20 @@ def test_rotation_keeps_the_angle_beyond_32_bits(dcn, interleaved):  # noqa: F81
     angle = pos[0].double()
     for got, ref in ((out[0, :, :, 0], 2 * angle.cos()), (out[0, :, :, 1 if interleaved else 2], 2 * angle.sin())):
         assert ((got.double() - ref[:, None]).abs() <= 2.5 * 2.0 ** -23 * ref.abs()[:, None]).all()
+
+
+def test_weight_gradients_are_rounded_once(dcn):  # noqa: F811
+    """Heads of +-1 have a norm of 1, so that a weight's gradient is a sum of 888 given numbers.  With two heads a token
+    that is a head for each of the backward's 1776 warps: no lane adds two of them, and the rest is 64 bits, so that
+    the result is off by half a step of 2^-23 at most."""
+    gen = torch.Generator().manual_seed(11)
+    N, L, D = 3, 296, 256
+    x = torch.randint(0, 2, (N, L, 1, D), generator=gen).float() * 2 - 1
+    gq, gk = torch.randn(x.shape, generator=gen), torch.randn(x.shape, generator=gen)
+    one = torch.ones(D).cuda()
+    a = (x.cuda(), x.cuda(), one, one, None, None)
+    p = dcn.qknorm_params_for(*a, eps=1e-30)
+    got = dcn.qknorm_backward(p, *a, gq.cuda(), gk.cuda())[2:]
+    for gw, g in zip(got, (gq, gk)):
+        ref = (x.double() * g.double()).sum((0, 1, 2))
+        assert ((gw.cpu().double() - ref).abs() <= 2.0 ** -24 * 1.0001 * ref.abs()).all()
