@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, kBackwardCtas)
                         }
                     const float2 sq = unf2(ss), sg = unf2(gx);
                     const float s = rsqrtf(fmaf(group_sum(sq.x + sq.y, sh.lph), inv_d, a.eps));
-                    const float back = s * s * (group_sum(sg.x + sg.y, sh.lph) * inv_d);
+                    const float back = s * (s * (group_sum(sg.x + sg.y, sh.lph) * inv_d));  // (s^2 may pass the largest number)
                     const F2 s2 = f2(s, s), back2 = f2(-back, -back);
 #pragma unroll
                     for (int c = 0; c < 2; ++c)

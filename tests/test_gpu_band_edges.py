@@ -266,3 +266,11 @@ def test_weight_gradients_are_rounded_once(dcn):  # noqa: F811
     for gw, g in zip(got, (gq, gk)):
         ref = (x.double() * g.double()).sum((0, 1, 2))
         assert ((gw.cpu().double() - ref).abs() <= 2.0 ** -24 * 1.0001 * ref.abs()).all()
+
+
+def test_norm_of_zeros_with_a_tiny_eps(dcn):  # noqa: F811
+    """1 / eps beyond the type's largest number: the gradient at zero is g w / sqrt(eps), a number."""
+    x, g = torch.zeros(1, 5, 2, 16).cuda(), torch.ones(1, 5, 2, 16).cuda()
+    p = dcn.qknorm_params_for(x, x, eps=1e-40)
+    gx = dcn.qknorm_backward(p, x, x, None, None, None, None, g, g)[0]
+    assert ((gx * 1e-20 - 1).abs() < 1e-4).all()  # eps is a subnormal: 1e-40 to 17 bits
