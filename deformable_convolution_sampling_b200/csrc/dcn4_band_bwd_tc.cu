@@ -115,6 +115,21 @@ struct QCfg {
     static constexpr size_t smem = 1024 + 4 * NB * kTcBlock + slots * 2 * NB * kTileBlock;
 };
 
+// After a wait that gave up: the block's results are NaN (and through delta its rows' part in grad_kv), and the
+// status word says so.  (A call, with nothing of the kernel's own, so that its registers are those of the way
+// without it: as part of grad_kv it cost 5 %.)
+template <typename T>
+__device__ __noinline__ void q_gave_up(BandArgs a, int pack, int tq, int blocks, float2* stats, T* gq) {
+    if (threadIdx.x == 0) atomicOr(&g_band_bwd_status, 1u);
+    const int blk = blocks - 1 - blockIdx.x % blocks, b = blockIdx.x / blocks, groups = a.Hq / pack, n = b / groups, h0 = (b - n * groups) * pack;
+    const int i0 = blk * 2 * tq, rows = max(min(i0 + 2 * tq, a.Lq) - i0, 0) * pack;
+    for (int r = threadIdx.x; r < rows; r += blockDim.x) {
+        const int i = i0 + r / pack, h = h0 + r % pack;
+        fill_nan(&stats[(static_cast<long long>(n) * a.Hq + h) * padded_queries(a.Lq) + i].y, 1);
+        fill_nan(gq + ((static_cast<long long>(n) * a.Lq + i) * a.Hq + h) * a.D, a.D);
+    }
+}
+
 template <typename T, int NB, bool BIAS, bool EXACT>
 __global__ void __launch_bounds__(QCfg<NB, BIAS>::threads, 1)
     grad_q_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_g,
@@ -472,7 +487,7 @@ __global__ void __launch_bounds__(QCfg<NB, BIAS>::threads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (tid == 0 && *abort) atomicOr(&g_band_bwd_status, 1u);
+    if (*abort) q_gave_up<T>(a, pack, tq, blocks, stats, gq);
     if (warp == kMma) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmem));
 }
 
@@ -557,6 +572,25 @@ struct KvCfg {
     static constexpr int stat = kTile * sizeof(float2);
     static constexpr size_t smem = 1024 + 2 * NB * kTcBlock + slots * (stage + stat) + (BIAS ? kDiagWarps * kDiagBuf * sizeof(float) : 0);
 };
+
+// As q_gave_up.
+template <typename T>
+__device__ __noinline__ void kv_gave_up(BandArgs a, KvShape sh, T* gk, T* gv, float* part, float* diag) {
+    if (threadIdx.x == 0) atomicOr(&g_band_bwd_status, 1u);
+    const int items = sh.items(), nh = blockIdx.x / items, item = blockIdx.x - nh * items, n = nh / a.Hk, hk = nh - n * a.Hk;
+    const int sink_items = sh.sink_tiles * sh.sink_parts;
+    const bool is_sink = item < sink_items;
+    const int parts = is_sink ? sh.sink_parts : sh.other_parts;
+    const int k0 = (is_sink ? item / parts : sh.sink_tiles + (item - sink_items) / parts) * kTcRows;
+    for (int r = threadIdx.x; r < kTcRows; r += blockDim.x) {
+        for (int w = 0; w < 2 && parts > 1; ++w) fill_nan(part + ((static_cast<long long>(blockIdx.x) * 2 + w) * kTcRows + r) * a.D, a.D);
+        if (parts > 1 || k0 + r >= a.Lk) continue;
+        const long long at = ((static_cast<long long>(n) * a.Lk + k0 + r) * a.Hk + hk) * a.D;
+        fill_nan(gk + at, a.D);
+        fill_nan(gv + at, a.D);
+    }
+    if (diag && threadIdx.x == 0) fill_nan(diag + static_cast<long long>(blockIdx.x) * kDiagWarps * a.G * (2 * a.M + 1), a.G * (2 * a.M + 1));
+}
 
 // WHOLE: the bias tables of all heads that share the key head are held at once; otherwise each parity holds its
 // present head's and reloads it at the next (as a branch in one kernel that cost the others 18 %).
@@ -924,7 +958,7 @@ __global__ void __launch_bounds__(KvCfg<NB, BIAS>::threads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (tid == 0 && *abort) atomicOr(&g_band_bwd_status, 1u);
+    if (*abort) kv_gave_up<T>(a, sh, gk, gv, part, BIAS ? diag : nullptr);
     if (warp == kMma) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmem));
 }
 

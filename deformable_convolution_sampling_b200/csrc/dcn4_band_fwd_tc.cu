@@ -97,6 +97,30 @@ __device__ __forceinline__ bool chunks_of(const RowBand& b, int j0, int& ca, int
     return b.any && lo < hi;
 }
 
+// After a wait that gave up: the block's results are NaN, and the status word says so.  (A call, with nothing of the
+// kernel's own, so that its registers are those of the way without it: as part of the kernel it cost 2 %.)
+template <typename T>
+__device__ __noinline__ void fwd_gave_up(BandArgs a, FwdShape sh, T* out, float* lse, BandPart part) {
+    if (threadIdx.x == 0) atomicOr(&g_band_status, 1u);
+    int b = blockIdx.x;
+    const int sp = b % sh.splits;
+    b /= sh.splits;
+    const int blk = sh.blocks - 1 - b % sh.blocks;
+    b /= sh.blocks;
+    const int groups = a.Hq / sh.pack, n = b / groups, h0 = (b - n * groups) * sh.pack, queries = (sh.alt ? 1 : 2) * sh.tq;
+    const int i0 = blk * queries, rows = max(min(i0 + queries, a.Lq) - i0, 0) * sh.pack;
+    for (int r = threadIdx.x; r < rows; r += blockDim.x) {
+        const int i = i0 + r / sh.pack, h = h0 + r % sh.pack;
+        const long long at = (static_cast<long long>(n) * a.Hq + h) * a.Lq + i;
+        if (sh.splits > 1) {
+            fill_nan(&part.ml[at * sh.splits + sp].y, 1);
+        } else {
+            fill_nan(lse + at, 1);
+            fill_nan(out + ((static_cast<long long>(n) * a.Lq + i) * a.Hq + h) * a.D, a.D);
+        }
+    }
+}
+
 // EXACT: p as two numbers (kBandExactKeys)
 template <typename T, int NB, bool BIAS, bool EXACT>
 __global__ void __launch_bounds__(Cfg<NB>::threads, Cfg<NB>::ctas)
@@ -504,7 +528,7 @@ __global__ void __launch_bounds__(Cfg<NB>::threads, Cfg<NB>::ctas)
     }
     tc_fence_before();
     __syncthreads();
-    if (tid == 0 && *abort) atomicOr(&g_band_status, 1u);
+    if (*abort) fwd_gave_up<T>(a, sh, out, lse, part);
     if (warp == kMma) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::tmem));
 }
 

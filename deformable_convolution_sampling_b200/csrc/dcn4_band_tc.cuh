@@ -128,6 +128,13 @@ __device__ __forceinline__ bool warp_wait(uint64_t* mbar, uint32_t parity, volat
     return false;
 }
 
+// What a block whose wait gave up leaves of a row (its copies have long landed: a wait's limit is far longer than
+// they take, and without the wait's progress the ring holds back further ones).
+template <typename T>
+__device__ __forceinline__ void fill_nan(T* row, int n) {
+    for (int d = 0; d < n; ++d) row[d] = from_f32<T>(__int_as_float(0x7fffffff));
+}
+
 // x * m + c of two values at once.
 __device__ __forceinline__ void fma2(uint32_t& x, uint32_t& y, float m, float c) {
     asm("{\n\t.reg .b64 v, w, z;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 w, {%2, %2};\n\tmov.b64 z, {%3, %3};\n\t"

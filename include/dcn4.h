@@ -517,7 +517,7 @@ int dcn4_band_backward(const dcn4_band_params* p, const void* q, const void* k, 
 
 /* The status word of the band attention's tensor-core kernels: 0 while every wait
  * on the tensor cores has completed, nonzero once one gave up (that block's results
- * are then not written).  Synchronous (waits for the device); reset != 0 clears it.
+ * are then NaN).  Synchronous (waits for the device); reset != 0 clears it.
  * Returns the word, or a negative DCN4_ERR_* status if it cannot be read. */
 int dcn4_band_status(int reset);
 
