@@ -500,6 +500,7 @@ struct KvShape {
     int tiles, sink_tiles;
     int sink_parts, other_parts;
     int floats;             // of a head's bias table
+    int whole;              // items of a key head that leave no parts, its last ones: all but the sinks', or none
     __host__ __device__ int items() const { return sink_tiles * sink_parts + (tiles - sink_tiles) * other_parts; }
     __host__ __device__ bool split() const { return sink_parts > 1 || other_parts > 1; }
 };
@@ -583,7 +584,7 @@ __device__ __noinline__ void kv_gave_up(BandArgs a, KvShape sh, T* gk, T* gv, fl
     const int parts = is_sink ? sh.sink_parts : sh.other_parts;
     const int k0 = (is_sink ? item / parts : sh.sink_tiles + (item - sink_items) / parts) * kTcRows;
     for (int r = threadIdx.x; r < kTcRows; r += blockDim.x) {
-        for (int w = 0; w < 2 && parts > 1; ++w) fill_nan(part + ((static_cast<long long>(blockIdx.x) * 2 + w) * kTcRows + r) * a.D, a.D);
+        for (int w = 0; w < 2 && parts > 1; ++w) fill_nan(part + ((static_cast<long long>(blockIdx.x - nh * sh.whole) * 2 + w) * kTcRows + r) * a.D, a.D);
         if (parts > 1 || k0 + r >= a.Lk) continue;
         const long long at = ((static_cast<long long>(n) * a.Lk + k0 + r) * a.Hk + hk) * a.D;
         fill_nan(gk + at, a.D);
@@ -606,7 +607,7 @@ __global__ void __launch_bounds__(KvCfg<NB, BIAS>::threads, 1)
     extern __shared__ __align__(1024) unsigned char band_smem[];
     __shared__ __align__(8) uint64_t full[kSlots], empty[kSlots], raw, keys_full, s_full[2], e_full[2], p_full[2], done;
     __shared__ uint32_t taddr_s;
-    __shared__ int s_abort;
+    __shared__ int s_abort, s_part;  // s_part: this block's place among those that leave parts (formed where it is used it cost 3 %)
     const int tid = threadIdx.x, warp = static_cast<int>(uniform(tid >> 5)), lane = tid & 31;
     const uint32_t base = (smem_u32(band_smem) + 1023u) & ~1023u;
     const uint32_t ks = base, ring = base + 2 * NB * kTcBlock, stat_at = ring + kSlots * C::stage;
@@ -638,6 +639,7 @@ __global__ void __launch_bounds__(KvCfg<NB, BIAS>::threads, 1)
         mbar_init(smem_u32(&raw), 1);
         mbar_init(smem_u32(&keys_full), 1);
         mbar_init(smem_u32(&done), 1);
+        s_part = blockIdx.x - nh * sh.whole;
         for (int w = 0; w < 2; ++w) {
             mbar_init(smem_u32(&s_full[w]), 1);
             mbar_init(smem_u32(&e_full[w]), 1);
@@ -931,7 +933,7 @@ __global__ void __launch_bounds__(KvCfg<NB, BIAS>::threads, 1)
         const float f = w ? a.scale : 1.f;
         const bool zero = !cnt || j >= klen;
         T* to = (w ? gk : gv) + ((static_cast<long long>(n) * a.Lk + j) * a.Hk + hk) * a.D;
-        float* po = part + ((static_cast<long long>(blockIdx.x) * 2 + w) * kTcRows + row) * a.D;
+        float* po = part + ((static_cast<long long>(s_part) * 2 + w) * kTcRows + row) * a.D;
         for (int d = 32 * c; d < a.D && ok; d += 64) {
             uint32_t x[32];
             if (cnt) {
@@ -981,7 +983,7 @@ __global__ void __launch_bounds__(256) kv_join_kernel(BandArgs a, KvShape sh, in
     const int parts = sink ? sh.sink_parts : sh.other_parts;
     if (parts == 1) return;
     const int first = sink ? kt * parts : sh.sink_tiles * sh.sink_parts + (kt - sh.sink_tiles) * parts;
-    const float* p = part + (((nh * sh.items() + first) * 2 + side) * kTcRows + row) * a.D + d;
+    const float* p = part + (((nh * (sh.items() - sh.whole) + first) * 2 + side) * kTcRows + row) * a.D + d;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int i = 0; i < parts; ++i) {
@@ -1024,6 +1026,7 @@ KvShape kv_shape(const BandArgs& a) {
         const long long each = static_cast<long long>(a.N) * a.Hk * s.sink_tiles, most = (4 * kBandSms + each - 1) / each;
         s.sink_parts = static_cast<int>(std::max<long long>(s.other_parts, std::min<long long>(static_cast<long long>(s.other_parts) * ((wide + narrow - 1) / narrow), most)));
     }
+    s.whole = s.other_parts > 1 ? 0 : s.items() - s.sink_tiles * s.sink_parts;
     return s;
 }
 
@@ -1035,7 +1038,7 @@ size_t far_bytes(const BandArgs& a) {
 }
 size_t weights_bytes(const BandArgs& a) { return up256(static_cast<size_t>(a.N) * a.Hq * padded_queries(a.Lq) * sizeof(float)); }
 size_t part_bytes(const BandArgs& a, const KvShape& s) {
-    return s.split() ? up256(static_cast<size_t>(a.N) * a.Hk * s.items() * 2 * kTcRows * a.D * sizeof(float)) : 0;
+    return s.split() ? up256(static_cast<size_t>(a.N) * a.Hk * (s.items() - s.whole) * 2 * kTcRows * a.D * sizeof(float)) : 0;
 }
 size_t diag_bytes(const BandArgs& a, const KvShape& s) {
     return a.nb ? up256(static_cast<size_t>(a.N) * a.Hq * s.items() * kDiagWarps * (2 * a.M + 1) * sizeof(float)) : 0;

@@ -47,3 +47,11 @@ def test_parameters_of_dense_tensors_take_no_cpu_tensors(dcn):
         dcn.band_forward(dcn.make_band_params(N=2, Lq=4, Lk=4, Hq=2, D=8), t, t, t)
     with pytest.raises(ValueError, match="CUDA"):
         dcn.qknorm_forward(dcn.make_qknorm_params(N=2, L=4, Hq=2, Hk=2, D=8), t, t)
+
+
+def test_workspaces_hold_what_is_used(dcn):  # noqa: F811
+    """A long window with sinks: only the sinks' tile of keys is split, and only its parts are held."""
+    p = dcn.make_band_params(N=1, Lq=131072, Lk=131072, Hq=8, D=128, left=4095, right=0, sinks=4, dtype="bf16")
+    rows = 8 * 131072
+    parts = 2 * 128 * 128 * 4 * (4 * 148)  # fp32 gradients of 128 keys, of four items an SM at most
+    assert dcn.dcn4_band_backward_workspace_size(p) < rows * 16 + parts
