@@ -178,6 +178,7 @@ def _load() -> ctypes.CDLL:
         "dcn4_band_forward_workspace_size": ([BP], ctypes.c_size_t),
         "dcn4_band_forward": ([BP] + [vp] * 11 + [ctypes.c_size_t, vp], ctypes.c_int),
         "dcn4_band_backward_workspace_size": ([BP], ctypes.c_size_t),
+        "dcn4_band_backward_frozen_workspace_size": ([BP], ctypes.c_size_t),
         "dcn4_band_backward": ([BP] + [vp] * 16 + [ctypes.c_size_t, vp], ctypes.c_int),
         "dcn4_band_status": ([ctypes.c_int], ctypes.c_int),
         "dcn4_qknorm_check_params": ([QP], ctypes.c_int),
@@ -332,6 +333,10 @@ def dcn4_band_forward(p: dcn4_band_params, q, k, v, bias, buckets, q_start, q_le
 
 def dcn4_band_backward_workspace_size(p: dcn4_band_params) -> int:
     return lib.dcn4_band_backward_workspace_size(ctypes.byref(p))
+
+
+def dcn4_band_backward_frozen_workspace_size(p: dcn4_band_params) -> int:
+    return lib.dcn4_band_backward_frozen_workspace_size(ctypes.byref(p))
 
 
 def dcn4_band_backward(p: dcn4_band_params, q, k, v, bias, buckets, q_start, q_len, k_len, out, lse, grad_out, grad_q,
@@ -726,7 +731,7 @@ def band_backward(p: dcn4_band_params, q, k, v, out, lse, grad_out, bias=None, b
     keys = (p.N, p.Lk, p.Hk, p.D)
     gk, gv = _dense_like(k, keys), _dense_like(v, keys)
     gb = torch.empty_like(bias) if bias is not None and want_bias else None
-    need = dcn4_band_backward_workspace_size(p)
+    need = dcn4_band_backward_workspace_size(p) if gb is not None else dcn4_band_backward_frozen_workspace_size(p)
     ws = _workspace(need, q)
     _launch(dev, dcn4_band_backward, p, q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(bias), _ptr(buckets), _ptr(q_start),
             _ptr(q_len), _ptr(k_len), out.data_ptr(), lse.data_ptr(), grad_out.data_ptr(), gq.data_ptr(), gk.data_ptr(),
@@ -783,18 +788,19 @@ def qknorm_forward(p: dcn4_qknorm_params, q, k, wq=None, wk=None, pos=None, inv_
     return qo, ko
 
 
-def qknorm_backward(p: dcn4_qknorm_params, q, k, wq, wk, pos, inv_freq, grad_q_out, grad_k_out):
+def qknorm_backward(p: dcn4_qknorm_params, q, k, wq, wk, pos, inv_freq, grad_q_out, grad_k_out,
+                    want_wq: bool = True, want_wk: bool = True):
     """(grad_q, grad_k, grad_wq or None, grad_wk or None) of qknorm_forward for contiguous
-    gradients of its outputs; a weight that was None gets no gradient."""
+    gradients of its outputs; a weight that was None, or is not wanted, gets no gradient."""
     import torch
     dev, dt = q.device, q.dtype
     _qknorm_call(p, q, k, wq, wk, pos, inv_freq)
     _dense("grad_q_out", grad_q_out, (p.N, p.L, p.Hq, p.D), dt, dev)
     _dense("grad_k_out", grad_k_out, (p.N, p.L, p.Hk, p.D), dt, dev)
     gq, gk = torch.empty_like(grad_q_out), torch.empty_like(grad_k_out)
-    gwq = torch.empty_like(wq) if wq is not None else None
-    gwk = torch.empty_like(wk) if wk is not None else None
-    need = dcn4_qknorm_backward_workspace_size(p) if wq is not None or wk is not None else 0
+    gwq = torch.empty_like(wq) if wq is not None and want_wq else None
+    gwk = torch.empty_like(wk) if wk is not None and want_wk else None
+    need = dcn4_qknorm_backward_workspace_size(p) if gwq is not None or gwk is not None else 0
     ws = _workspace(need, q)
     _launch(dev, dcn4_qknorm_backward, p, q.data_ptr(), k.data_ptr(), _ptr(wq), _ptr(wk), _ptr(pos), _ptr(inv_freq),
             grad_q_out.data_ptr(), grad_k_out.data_ptr(), gq.data_ptr(), gk.data_ptr(), _ptr(gwq), _ptr(gwk), _ptr(ws), need)
@@ -998,7 +1004,7 @@ def _autograd_function_qknorm():
         def backward(ctx, grad_q_out, grad_k_out):
             q, k, wq, wk, pos, inv_freq = ctx.saved_tensors
             grads = qknorm_backward(ctx.p, q, k, wq, wk, pos, inv_freq, grad_q_out.contiguous(),
-                                    grad_k_out.contiguous())
+                                    grad_k_out.contiguous(), *ctx.needs_input_grad[2:4])
             return grads + (None,) * 3
 
     return QkNorm

@@ -867,7 +867,13 @@ int dcn4_band_forward(const dcn4_band_params* p, const void* q, const void* k, c
 size_t dcn4_band_backward_workspace_size(const dcn4_band_params* p) {
     dcn4::BandArgs a;
     if (make_band(p, &a) != DCN4_OK || !a.N || !a.Lq || !a.Lk) return 0;
-    return dcn4::band_backward_workspace_bytes(a);
+    return dcn4::band_backward_workspace_bytes(a, a.nb > 0);
+}
+
+size_t dcn4_band_backward_frozen_workspace_size(const dcn4_band_params* p) {
+    dcn4::BandArgs a;
+    if (make_band(p, &a) != DCN4_OK || !a.N || !a.Lq || !a.Lk) return 0;
+    return dcn4::band_backward_workspace_bytes(a, false);
 }
 
 int dcn4_band_backward(const dcn4_band_params* p, const void* q, const void* k, const void* v, const void* bias,
@@ -897,7 +903,7 @@ int dcn4_band_backward(const dcn4_band_params* p, const void* q, const void* k, 
     if (!aligned16(out) || !aligned16(lse) || !aligned16(grad_out))
         return fail(DCN4_ERR_MISALIGNED, "every pointer must be 16-byte aligned");
     st = band_pointers(&a, q, k, v, bias, buckets, q_start, q_len, k_len);
-    if (st == DCN4_OK) st = check_workspace(dcn4::band_backward_workspace_bytes(a), workspace, workspace_bytes);
+    if (st == DCN4_OK) st = check_workspace(dcn4::band_backward_workspace_bytes(a, grad_bias != nullptr), workspace, workspace_bytes);
     if (st != DCN4_OK) return st;
     e = dcn4::launch_band_backward(a, out, lse, grad_out, grad_q, grad_k, grad_v, grad_bias, workspace, s);
     if (e != cudaSuccess) return fail(DCN4_ERR_LAUNCH, "band backward launch: %s", cudaGetErrorString(e));

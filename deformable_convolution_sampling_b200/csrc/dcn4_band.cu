@@ -186,8 +186,8 @@ cudaError_t band_status(unsigned* status, bool reset) {
     return e;
 }
 
-size_t band_backward_workspace_bytes(const BandArgs& a) {
-    return a.dtype == 0 ? band_simt_backward_workspace(a) : band_bwd_tc_workspace(a);
+size_t band_backward_workspace_bytes(const BandArgs& a, bool want_bias) {
+    return a.dtype == 0 ? band_simt_backward_workspace(a, want_bias) : band_bwd_tc_workspace(a, want_bias);
 }
 
 cudaError_t launch_band_forward(const BandArgs& a, void* out, float* lse, void* ws, cudaStream_t stream) {

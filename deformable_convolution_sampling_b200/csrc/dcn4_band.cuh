@@ -90,7 +90,7 @@ __device__ __forceinline__ void band_queries(const BandArgs& a, int start, int q
 
 // Bytes of scratch (see the C ABI), each a multiple of 256.
 size_t band_forward_workspace_bytes(const BandArgs& a);
-size_t band_backward_workspace_bytes(const BandArgs& a);
+size_t band_backward_workspace_bytes(const BandArgs& a, bool want_bias);
 // The status words of the kernels with bounded waits, or-ed.
 cudaError_t band_status(unsigned* status, bool reset);
 // out = 0 and lse = -infinity (no keys at all).

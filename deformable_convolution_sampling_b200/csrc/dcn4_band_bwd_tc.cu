@@ -796,7 +796,8 @@ __global__ void __launch_bounds__(KvCfg<NB, BIAS>::threads, 1)
         Diagonals dg;
         int dg_head = -1, tab_head = -1;
         float* diag_w = diag + (static_cast<long long>(blockIdx.x) * kDiagWarps + warp) * a.G * (2 * a.M + 1);
-        if (BIAS) {  // what no store below reaches is 0
+        const bool sums = BIAS && diag;
+        if (sums) {  // what no store below reaches is 0
             for (int e = lane; e < a.G * (2 * a.M + 1); e += 32) diag_w[e] = 0.f;
             __syncwarp();
         }
@@ -817,7 +818,7 @@ __global__ void __launch_bounds__(KvCfg<NB, BIAS>::threads, 1)
                 tab_head = g;
             }
             if (!WHOLE && !ok) continue;
-            if (BIAS && warp_live && g != dg_head) {
+            if (sums && warp_live && g != dg_head) {
                 if (dg_head >= 0) dg.finish(lane);
                 dg.start(diag_w + g * (2 * a.M + 1));
                 dg_head = g;
@@ -910,7 +911,7 @@ __global__ void __launch_bounds__(KvCfg<NB, BIAS>::threads, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&p_full[w]));
-            if (BIAS && on) {  // under the products that p and d go into
+            if (sums && on) {  // under the products that p and d go into
                 const bool above = kw - (start + ic + kTcChunk - 1) >= a.M, below = kw + 31 - (start + ic) <= -a.M;
                 if (above || below) {
                     float2 sum[2] = {};
@@ -924,7 +925,7 @@ __global__ void __launch_bounds__(KvCfg<NB, BIAS>::threads, 1)
             s += 2;
             if (s >= kSlots) s -= kSlots;
         }
-        if (BIAS && dg_head >= 0) dg.finish(lane);
+        if (sums && dg_head >= 0) dg.finish(lane);
         if (ok && cnt) ok = warp_wait(&done, 0u, abort);
         tc_fence_after();
         // parity 0 stores gv, 1 gk, each chunk's warps every second 32 columns
@@ -1054,8 +1055,8 @@ cudaError_t launch(const BandArgs& a, const void* out, const float* lse, const v
     float* weights = reinterpret_cast<float*>(at += stats_bytes(a));
     int* far_blocks = reinterpret_cast<int*>(at += weights_bytes(a));
     float* part = reinterpret_cast<float*>(at += far_bytes(a));
-    float* diag = reinterpret_cast<float*>(at += part_bytes(a, kv));
-    float* sums = reinterpret_cast<float*>(at += diag_bytes(a, kv));
+    float* diag = BIAS && gbias ? reinterpret_cast<float*>(at += part_bytes(a, kv)) : nullptr;
+    float* sums = diag ? reinterpret_cast<float*>(at += diag_bytes(a, kv)) : nullptr;
     const auto [pack, tq, blocks] = row_shape(a);
     const bool whole = !BIAS || whole_tables(a);
     const long long dense = static_cast<long long>(a.Hq) * a.D;
@@ -1094,14 +1095,14 @@ cudaError_t launch(const BandArgs& a, const void* out, const float* lse, const v
         kv_join_kernel<T><<<static_cast<unsigned>((n4 + 255) / 256), 256, 0, stream>>>(a, kv, tiles, part, static_cast<T*>(gk), static_cast<T*>(gv));
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
-    return BIAS && gbias ? launch_band_bias_sum(a, kv.items(), kDiagWarps, diag, sums, gbias, stream) : cudaSuccess;
+    return diag ? launch_band_bias_sum(a, kv.items(), kDiagWarps, diag, sums, gbias, stream) : cudaSuccess;
 }
 
 }  // namespace
 
-size_t band_bwd_tc_workspace(const BandArgs& a) {
+size_t band_bwd_tc_workspace(const BandArgs& a, bool want_bias) {
     const KvShape kv = kv_shape(a);
-    return stats_bytes(a) + weights_bytes(a) + far_bytes(a) + part_bytes(a, kv) + diag_bytes(a, kv) + sums_bytes(a);
+    return stats_bytes(a) + weights_bytes(a) + far_bytes(a) + part_bytes(a, kv) + (want_bias ? diag_bytes(a, kv) + sums_bytes(a) : 0);
 }
 
 cudaError_t launch_band_bwd_tc(const BandArgs& a, const void* out, const float* lse, const void* gout, void* gq, void* gk, void* gv,

@@ -66,7 +66,7 @@ size_t band_few_part_bytes(const BandArgs& a);
 cudaError_t launch_band_few(const BandArgs& a, void* out, float* lse, void* ws, cudaStream_t stream);
 
 // 16-bit backward on the tensor cores (dcn4_band_bwd_tc.cu).
-size_t band_bwd_tc_workspace(const BandArgs& a);
+size_t band_bwd_tc_workspace(const BandArgs& a, bool want_bias);
 cudaError_t launch_band_bwd_tc(const BandArgs& a, const void* out, const float* lse, const void* gout, void* gq, void* gk, void* gv,
                                void* gbias, void* ws, cudaStream_t stream);
 cudaError_t band_bwd_status(unsigned* status, bool reset);
@@ -77,6 +77,6 @@ int simt_splits(const BandArgs& a);
 cudaError_t launch_band_simt_forward(const BandArgs& a, void* out, float* lse, void* ws, cudaStream_t stream);
 cudaError_t launch_band_simt_backward(const BandArgs& a, const void* out, const float* lse, const void* gout, void* gq,
                                       void* gk, void* gv, void* gbias, void* ws, cudaStream_t stream);
-size_t band_simt_backward_workspace(const BandArgs& a);
+size_t band_simt_backward_workspace(const BandArgs& a, bool want_bias);
 
 }  // namespace dcn4

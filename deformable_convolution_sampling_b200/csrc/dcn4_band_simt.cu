@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 // gq of 64 rows over a range of their keys, their D (into delta), what a probability is formed
 // from (refs: e^(s - x) y; lse and 1, or a far row's maximum and the inverse of its sum) and, with a
-// bias, the sums of ds along diagonals: diag[CTA][G][2 M + 1], of relative position -M .. M (the ends:
+// bias whose gradient is wanted, the sums of ds along diagonals: diag[CTA][G][2 M + 1], of relative position -M .. M (the ends:
 // and beyond).
 template <typename T, int DP>
 __global__ void __launch_bounds__(kThreads)
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(kThreads)
         for (int c = 0; c < DP / 16; ++c) o[r][c] = 0.f;
     }
     float* mine = diag + static_cast<long long>(blockIdx.x) * a.G * (2 * a.M + 1);
-    if (a.nb)
+    if (diag)
         for (int e = threadIdx.x; e < a.G * (2 * a.M + 1); e += kThreads) mine[e] = 0.f;
     far = __syncthreads_or(far);
     if (i0 <= i1) {
@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(kThreads)
                 }
             __syncthreads();
             accumulate_rows<DP>(o, Ps, Ks, ty, tx);
-            if (a.nb) {
+            if (diag) {
                 // the tile's sums along each head's diagonals (all pairs of one relative position): one thread
                 // adds a diagonal's to its place, one warp those of a head beyond M
                 const int nd = ilast - i0 + kB;  // relative positions j0 - (start + ilast) ...
@@ -591,8 +591,8 @@ cudaError_t backward_typed(const BandArgs& a, const void* out, const float* lse,
     float* delta = reinterpret_cast<float*>(at);
     float2* refs = reinterpret_cast<float2*>(at += w.delta);
     float* part = reinterpret_cast<float*>(at += w.refs);
-    float* diag = reinterpret_cast<float*>(at += w.part);
-    float* sums = reinterpret_cast<float*>(at += w.diag);
+    float* diag = a.nb && gbias ? reinterpret_cast<float*>(at += w.part) : nullptr;
+    float* sums = diag ? reinterpret_cast<float*>(at += w.diag) : nullptr;
     const int blocks = simt_row_blocks(a), sq = simt_splits(a), sk = kv_splits(a), floats = simt_table(a);
     const int spread = (kB + a.G - 1) / a.G + 1 + kB;  // relative positions of one tile and head at most
     const size_t smem_q = tiles_smem<DP>(4, 1) + (a.nb ? (static_cast<size_t>(spread) * a.G + floats) * sizeof(float) : 0),
@@ -614,7 +614,7 @@ cudaError_t backward_typed(const BandArgs& a, const void* out, const float* lse,
         if ((e = launch_sum_parts<T>(part, sk, 2 * nk, nk, gk, stream)) != cudaSuccess) return e;
         if ((e = launch_sum_parts<T>(part + nk, sk, 2 * nk, nk, gv, stream)) != cudaSuccess) return e;
     }
-    return a.nb && gbias ? launch_band_bias_sum(a, blocks * sq, 1, diag, sums, gbias, stream) : cudaSuccess;
+    return diag ? launch_band_bias_sum(a, blocks * sq, 1, diag, sums, gbias, stream) : cudaSuccess;
 }
 
 }  // namespace
@@ -627,9 +627,9 @@ int simt_splits(const BandArgs& a) {
                                                          std::min(a.right, kBandMaxLen) + std::min(a.Lq, kB / a.G + 2) + a.sinks);
     return split_count(static_cast<long long>(a.N) * a.Hk * simt_row_blocks(a), (span + kB - 1) / kB);
 }
-size_t band_simt_backward_workspace(const BandArgs& a) {
+size_t band_simt_backward_workspace(const BandArgs& a, bool want_bias) {
     const Workspace w(a);
-    return w.delta + w.refs + w.part + w.diag + w.sums;
+    return w.delta + w.refs + w.part + (want_bias ? w.diag + w.sums : 0);
 }
 
 cudaError_t launch_band_simt_forward(const BandArgs& a, void* out, float* lse, void* ws, cudaStream_t stream) {

@@ -498,8 +498,13 @@ int dcn4_band_forward(const dcn4_band_params* p, const void* q, const void* k, c
 
 /* Bytes of device workspace dcn4_band_backward needs (fp32: three numbers per query
  * and head, partial gradients where few keys face many queries, and with a bias the
- * sums of its gradient by relative position); 0 if p is invalid. */
+ * sums of its gradient by relative position: 64 (2 M + 1) bytes and more for every
+ * 128 keys and query head); 0 if p is invalid. */
 size_t dcn4_band_backward_workspace_size(const dcn4_band_params* p);
+
+/* The same where grad_bias is NULL (a frozen bias): without those sums, which are
+ * then not formed. */
+size_t dcn4_band_backward_frozen_workspace_size(const dcn4_band_params* p);
 
 /* Backward for grad_out, from the out and lse of the forward (where |lse_i| is above
  * 512, too far from 0 to keep the log of a sum in 32 bits, the row's maximum and sum are

@@ -2,7 +2,7 @@
 parameters are not for, workspaces of calls that want less (CPU only: nothing is launched)."""
 import pytest
 
-from test_abi_host import dcn  # noqa: F401  (a fixture)
+from test_abi_host import dcn, run_without_gpu  # noqa: F401  (dcn is a fixture)
 
 
 def _views(shape):
@@ -55,3 +55,24 @@ def test_workspaces_hold_what_is_used(dcn):  # noqa: F811
     rows = 8 * 131072
     parts = 2 * 128 * 128 * 4 * (4 * 148)  # fp32 gradients of 128 keys, of four items an SM at most
     assert dcn.dcn4_band_backward_workspace_size(p) < rows * 16 + parts
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+def test_a_frozen_bias_needs_no_memory_for_its_gradient(dcn, dtype):  # noqa: F811
+    """The size that the call itself asks for (made-up addresses, no GPU in sight)."""
+    p = dcn.make_band_params(N=4, Lq=1024, Lk=1024, Hq=16, D=64, nb=32, M=512, dtype=dtype)
+    rows = 4 * 16 * 1024
+    whole, frozen = dcn.dcn4_band_backward_workspace_size(p), dcn.dcn4_band_backward_frozen_workspace_size(p)
+    assert frozen <= rows * 16 + 4096 and whole > 5 * frozen
+    plain = dcn.make_band_params(N=4, Lq=1024, Lk=1024, Hq=16, D=64, dtype=dtype)
+    assert dcn.dcn4_band_backward_workspace_size(plain) == dcn.dcn4_band_backward_frozen_workspace_size(plain) == frozen
+    p.D = 3
+    assert dcn.dcn4_band_backward_frozen_workspace_size(p) == 0
+    run_without_gpu(f"""
+p = dcn.make_band_params(N=4, Lq=1024, Lk=1024, Hq=16, D=64, nb=32, M=512, dtype="{dtype}")
+a = [16 * (i + 1) for i in range(14)]
+frozen = dcn.dcn4_band_backward_frozen_workspace_size(p)
+assert dcn.dcn4_band_backward(p, *a, 4096, 4096, frozen) == -6           # a gradient wanted
+assert dcn.dcn4_band_backward(p, *a, None, 4096, frozen - 1) == -6
+assert dcn.dcn4_band_backward(p, *a, None, 4096, frozen) not in (0, -6)  # as far as the launch, which has no GPU
+""")

@@ -274,3 +274,37 @@ def test_norm_of_zeros_with_a_tiny_eps(dcn):  # noqa: F811
     p = dcn.qknorm_params_for(x, x, eps=1e-40)
     gx = dcn.qknorm_backward(p, x, x, None, None, None, None, g, g)[0]
     assert ((gx * 1e-20 - 1).abs() < 1e-4).all()  # eps is a subnormal: 1e-40 to 17 bits
+
+
+@pytest.mark.parametrize("c", [case("f16", 1, 300, 300, 4, 2, 64, nb=8, M=16), case("f32", 1, 100, 100, 4, 2, 64, nb=8, M=16),
+                               case("bf16", 1, 200, 200, 16, 1, 64, nb=8, M=128)], ids=str)
+def test_a_frozen_bias_changes_nothing_else(dcn, c):  # noqa: F811
+    t = make(c)
+    cu = {k: None if v is None else v.cuda() for k, v in t.items()}
+    a = (cu["q"], cu["k"], cu["v"])
+    more = dict(bias=cu["bias"], buckets=cu["buckets"])
+    p = dcn.band_params_for(*a, **more)
+    out, lse = dcn.band_forward(p, *a, **more)
+    full = dcn.band_backward(p, *a, out, lse, cu["g"], **more)
+    part = dcn.band_backward(p, *a, out, lse, cu["g"], **more, want_bias=False)
+    assert part[3] is None and full[3] is not None
+    for x, y in zip(full[:3], part):
+        assert torch.equal(x, y)
+    q, k, v = (x.clone().requires_grad_(True) for x in a)
+    grads = torch.autograd.grad(dcn.band_attention(q, k, v, **more), (q, k, v), cu["g"])
+    for x, y in zip(full, grads):
+        assert torch.equal(x, y)
+
+
+def test_frozen_norm_weights_change_nothing_else(dcn):  # noqa: F811
+    gen = torch.Generator().manual_seed(3)
+    q, k, w = (torch.randn(*s, generator=gen).half().cuda() for s in ((2, 9, 4, 32), (2, 9, 2, 32), (32,)))
+    p = dcn.qknorm_params_for(q, k, w, w)
+    full = dcn.qknorm_backward(p, q, k, w, w, None, None, q, k)
+    for wants in ((False, False), (True, False), (False, True)):
+        part = dcn.qknorm_backward(p, q, k, w, w, None, None, q, k, *wants)
+        for x, y, want in zip(full, part, (True, True) + wants):
+            assert torch.equal(x, y) if want else y is None
+    a, b = q.clone().requires_grad_(True), k.clone().requires_grad_(True)
+    grads = torch.autograd.grad(dcn.qk_norm_rotate(a, b, w, w), (a, b), (q, k))
+    assert torch.equal(grads[0], full[0]) and torch.equal(grads[1], full[1])
