@@ -574,6 +574,12 @@ struct KvCfg {
     static constexpr size_t smem = 1024 + 2 * NB * kTcBlock + slots * (stage + stat) + (BIAS ? kDiagWarps * kDiagBuf * sizeof(float) : 0);
 };
 
+// fill_table of one head by 256 threads (a call: its loop would take registers of the loop around it).
+template <typename T>
+__device__ __noinline__ void fill_head(BandArgs a, float* table, int floats, int h, int at) {
+    fill_table<T>(a, table, floats, h, 1, at, 256);
+}
+
 // As q_gave_up.
 template <typename T>
 __device__ __noinline__ void kv_gave_up(BandArgs a, KvShape sh, T* gk, T* gv, float* part, float* diag) {
@@ -813,7 +819,7 @@ __global__ void __launch_bounds__(KvCfg<NB, BIAS>::threads, 1)
             st_w.next();
             if (!WHOLE && g != tab_head) {  // (also by a warp whose wait gave up: the others' barriers count it)
                 asm volatile("bar.sync %0, 256;" ::"r"(1 + w) : "memory");  // the last head's reads are done
-                fill_table<T>(a, table + w * sh.floats, sh.floats, hk * a.G + g, 1, c * kTcRows + row, 256);
+                fill_head<T>(a, table + w * sh.floats, sh.floats, hk * a.G + g, c * kTcRows + row);
                 asm volatile("bar.sync %0, 256;" ::"r"(1 + w) : "memory");
                 tab_head = g;
             }
