@@ -598,6 +598,12 @@ def _dense_like(t, shape):
     return torch.empty_like(t) if t.shape == shape and t.is_contiguous() else t.new_empty(shape)
 
 
+def _upstream(t):
+    """An upstream gradient as the kernels take it: contiguous and from a 16-byte boundary on."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 def _ptr(t):
     return t.data_ptr() if t is not None else None
 
@@ -978,7 +984,7 @@ def _autograd_function_band():
         @once_differentiable
         def backward(ctx, grad_out):
             q, k, v, bias, buckets, q_start, q_len, k_len, out, lse = ctx.saved_tensors
-            grads = band_backward(ctx.p, q, k, v, out, lse, grad_out.contiguous(), bias, buckets, q_start, q_len,
+            grads = band_backward(ctx.p, q, k, v, out, lse, _upstream(grad_out), bias, buckets, q_start, q_len,
                                   k_len, want_bias=ctx.needs_input_grad[3])
             return grads + (None,) * 5
 
@@ -1003,8 +1009,8 @@ def _autograd_function_qknorm():
         @once_differentiable
         def backward(ctx, grad_q_out, grad_k_out):
             q, k, wq, wk, pos, inv_freq = ctx.saved_tensors
-            grads = qknorm_backward(ctx.p, q, k, wq, wk, pos, inv_freq, grad_q_out.contiguous(),
-                                    grad_k_out.contiguous(), *ctx.needs_input_grad[2:4])
+            grads = qknorm_backward(ctx.p, q, k, wq, wk, pos, inv_freq, _upstream(grad_q_out),
+                                    _upstream(grad_k_out), *ctx.needs_input_grad[2:4])
             return grads + (None,) * 3
 
     return QkNorm

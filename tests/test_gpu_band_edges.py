@@ -308,3 +308,19 @@ def test_frozen_norm_weights_change_nothing_else(dcn):  # noqa: F811
     a, b = q.clone().requires_grad_(True), k.clone().requires_grad_(True)
     grads = torch.autograd.grad(dcn.qk_norm_rotate(a, b, w, w), (a, b), (q, k))
     assert torch.equal(grads[0], full[0]) and torch.equal(grads[1], full[1])
+
+
+def test_gradients_from_outside_may_start_anywhere(dcn):  # noqa: F811
+    """A contiguous upstream gradient that starts at an odd element, as a part of a longer buffer does."""
+    gen = torch.Generator().manual_seed(5)
+    q, k, v, w = (torch.randn(*s, generator=gen).half().cuda() for s in ((2, 9, 4, 32), (2, 9, 2, 32), (2, 9, 2, 32), (32,)))
+    g = torch.randn(2, 9, 4, 32, generator=gen).half().cuda()
+    odd = torch.empty(g.numel() + 1, dtype=g.dtype, device="cuda")[1:].view(g.shape).copy_(g)
+    leaves = [x.clone().requires_grad_(True) for x in (q, k, v, w)]
+    out = dcn.band_attention(*dcn.qk_norm_rotate(leaves[0], leaves[1], leaves[3], None), leaves[2])
+    want = torch.autograd.grad(out, leaves, g, retain_graph=True)
+    for x, y in zip(want, torch.autograd.grad(out, leaves, odd)):
+        assert torch.equal(x, y)
+    qn, _ = dcn.qk_norm_rotate(leaves[0], leaves[1], leaves[3], None)
+    want = torch.autograd.grad(qn, leaves[0], g, retain_graph=True)
+    assert torch.equal(want[0], torch.autograd.grad(qn, leaves[0], odd)[0])
