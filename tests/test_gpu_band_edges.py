@@ -8,6 +8,7 @@ import torch
 from _band import E32, check
 from _band_far import far_reference
 from test_gpu_band import DTYPES, case, compare, dcn, make, run  # noqa: F401  (dcn is a fixture)
+from test_gpu_band import test_qknorm_matches_the_definition as qknorm_case
 
 pytestmark = pytest.mark.gpu
 
@@ -324,3 +325,17 @@ def test_gradients_from_outside_may_start_anywhere(dcn):  # noqa: F811
     qn, _ = dcn.qk_norm_rotate(leaves[0], leaves[1], leaves[3], None)
     want = torch.autograd.grad(qn, leaves[0], g, retain_graph=True)
     assert torch.equal(want[0], torch.autograd.grad(qn, leaves[0], odd)[0])
+
+
+MANY = [dict(dtype="bf16", N=3, L=1501, Hq=4, Hk=2, D=64, R=64, packed=True, far=3000),
+        dict(dtype="f16", N=3, L=5003, Hq=2, Hk=1, D=32, R=16, axes=2),
+        dict(dtype="f32", N=2, L=3001, Hq=5, Hk=1, D=80, R=40, interleaved=True, far=5000),
+        dict(dtype="f16", N=3, L=2222, Hq=3, Hk=1, D=104, R=52, axes=2, packed=True),
+        dict(dtype="bf16", N=7, L=700, Hq=3, Hk=0, D=128, R=0), dict(dtype="f32", N=2, L=4000, Hq=0, Hk=2, D=16, R=16),
+        dict(dtype="f16", N=4999, L=3, Hq=1, Hk=1, D=8, R=8)]
+
+
+@pytest.mark.parametrize("c", MANY, ids=lambda c: "-".join(f"{k}{v}" for k, v in c.items()))
+def test_norms_of_several_tokens_a_warp(dcn, c):  # noqa: F811
+    """Units of several tokens, warps with several units, units over the end of an image."""
+    qknorm_case(dcn, c)
