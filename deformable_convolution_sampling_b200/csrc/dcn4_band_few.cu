@@ -24,10 +24,13 @@
 namespace dcn4 {
 namespace {
 
+using tc::kLog2e;
+using tc::pack2;
+
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kTile = 16 * kWarps;  // keys of a step: 16 a warp
 constexpr int kRows = 16;
-constexpr float kLog2e = 1.4426950408889634f, kRescale = 8.f;
+constexpr float kRescale = 8.f;
 
 template <typename T>
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -39,19 +42,6 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
         asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-template <typename T>
-__device__ __forceinline__ uint32_t pair_of(float lo, float hi) {
-    uint32_t u;
-    if constexpr (std::is_same<T, __half>::value) {
-        const __half2 h = __floats2half2_rn(lo, hi);
-        memcpy(&u, &h, 4);
-    } else {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-        memcpy(&u, &h, 4);
-    }
-    return u;
 }
 
 template <typename T>
@@ -208,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<KG>::ctas)
                 const float ref = m[h] == -INFINITY ? 0.f : m[h];
                 const float lo = exp2f((s[x][2 * h] - ref) * kLog2e), hi = exp2f((s[x][2 * h + 1] - ref) * kLog2e);
                 l[h] += lo + hi;
-                p[2 * x + h] = pair_of<T>(lo, hi);
+                p[2 * x + h] = pack2<T>(lo, hi);
             }
 #pragma unroll
         for (int g = 0; g < VG; ++g) {
@@ -270,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<KG>::ctas)
         } else {
             const float inv = ll != 0.f ? 1.f / ll : 0.f;  // (a sum of NaN stays one)
             T* to = out + ((static_cast<long long>(n) * a.Lq + i) * a.Hq + hq) * a.D + d;
-            *reinterpret_cast<uint2*>(to) = make_uint2(pair_of<T>(s.x * inv, s.y * inv), pair_of<T>(s.z * inv, s.w * inv));
+            *reinterpret_cast<uint2*>(to) = make_uint2(pack2<T>(s.x * inv, s.y * inv), pack2<T>(s.z * inv, s.w * inv));
             if (d == 0) lse[at] = ll != 0.f ? mm + logf(ll) : -INFINITY;
         }
     }
