@@ -676,12 +676,13 @@ def band_params_for(q, k, v, *, left=-1, right=-1, sinks=0, scale=None, bias=Non
 def _same(name, t, shape, dtype, device, batch, row):
     """ValueError unless t is the tensor (its shape, device and all strides, 0 for dense ones) that the parameters
     are for.  A dimension of length 1 has no stride that matters."""
+    N, L, H, D = shape
+    row = row or H * D
+    batch = batch or row * L
     ok = t.shape == shape and t.dtype == dtype and t.device == device
-    if ok and t.numel():
-        N, L, H, D = shape
+    if ok and t.stride() != (batch, row, D, 1) and t.numel():
         sb, sl, sh, sd = t.stride()
-        row = row or H * D
-        ok = (N == 1 or sb == (batch or row * L)) and (L == 1 or sl == row) and (H == 1 or sh == D) and (D == 1 or sd == 1)
+        ok = (N == 1 or sb == batch) and (L == 1 or sl == row) and (H == 1 or sh == D) and (D == 1 or sd == 1)
     if not ok:
         raise ValueError(f"{name} is not the tensor these parameters were made for")
 

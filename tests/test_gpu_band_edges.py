@@ -339,3 +339,56 @@ MANY = [dict(dtype="bf16", N=3, L=1501, Hq=4, Hk=2, D=64, R=64, packed=True, far
 def test_norms_of_several_tokens_a_warp(dcn, c):  # noqa: F811
     """Units of several tokens, warps with several units, units over the end of an image."""
     qknorm_case(dcn, c)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_far_rows_of_a_ragged_batch(dcn, dtype):  # noqa: F811
+    """Rows of lowest biases with lengths, starts and sinks: each image's as its own call's on what it has.  (Both
+    hold the same tiles; where fewer keys are split otherwise, sums of 32 bits differ by their order.)"""
+    c = case(dtype, 3, 200, 330, 4, 2, 64, left=90, right=20, sinks=3, nb=4, M=100, q_start=[0, 130, 40], q_len=[200, 77, 130],
+             k_len=[150, 330, 61], poison=True)
+    t = make(c, 2)
+    t["bias"][:3] = torch.finfo(DTYPES[dtype]).min
+    t["buckets"] = torch.where(torch.arange(201) < 60, torch.full((201,), 3), torch.arange(201) % 3).int()
+    got = run(dcn, c, t)
+    gb = 0
+    for n in range(3):
+        a, b = c["q_len"][n], c["k_len"][n]
+        one = case(dtype, 1, a, b, 4, 2, 64, left=90, right=20, sinks=3, nb=4, M=100)
+        s = dict(t, q=t["q"][n:n + 1, :a].contiguous(), g=t["g"][n:n + 1, :a].contiguous(), k=t["k"][n:n + 1, :b].contiguous(),
+                 v=t["v"][n:n + 1, :b].contiguous(), q_start=t["q_start"][n:n + 1], q_len=None, k_len=None)
+        alone = run(dcn, one, s)
+        for x, y, m in zip(got, alone, (a, a, a, b, b)):
+            x = x[n, :, :m] if x.dim() == 3 else x[n, :m]
+            assert torch.allclose(x.float(), y[0].float(), rtol=4 * torch.finfo(DTYPES[dtype]).eps, atol=2e-5 if dtype == "f32" else 2e-2)
+            assert x.isfinite().all()
+        gb = gb + alone[5].float()
+    assert torch.allclose(got[5].float(), gb, rtol=8 * torch.finfo(DTYPES[dtype]).eps, atol=1e-3 if dtype == "f32" else 0.1)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_a_captured_step_meets_far_rows_at_its_replay(dcn, dtype):  # noqa: F811
+    c = case(dtype, 1, 150, 700, 4, 2, 64, nb=4, M=50)
+    t = make(c, 4)
+    cu = {k: None if v is None else v.cuda() for k, v in t.items()}
+    low = torch.full_like(cu["bias"], torch.finfo(DTYPES[dtype]).min)
+
+    def step(bias):
+        leaves = [x.detach().requires_grad_(True) for x in (cu["q"], cu["k"], cu["v"], bias)]
+        out = dcn.band_attention(*leaves[:3], bias=leaves[3], buckets=cu["buckets"])
+        return (out.detach(),) + torch.autograd.grad(out, leaves, cu["g"])
+    static = cu["bias"].clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(static)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        replayed = step(static)
+    for bias in (cu["bias"], low, cu["bias"]):
+        static.copy_(bias)
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(replayed, step(bias)):
+            assert torch.equal(x, y) and x.isfinite().all()
