@@ -353,9 +353,9 @@ __global__ void __launch_bounds__(Cfg<NB>::threads, Cfg<NB>::ctas)
         // keys that every row of the tile sees; relative positions at which a chunk has one bias
         const int all_lo = rb.phi - a.left, all_hi = min(klen, rb.plo + a.right + 1) - kTcChunk;
         float rm = -INFINITY, rl = 0.f;  // reference (log2 units without a bias, natural with one) and sum
-        // a scale of 0 is held at 1e-30, so that 0 times a mask's infinity does not arise (products below
-        // 1e20 still vanish next to any score)
-        const float scale = a.scale == 0.f ? 1e-30f : fabsf(a.scale);
+        // a scale of 0 is held at 1e-38, so that 0 times a mask's infinity does not arise (a normal number, also times
+        // log2 e; products below 1e31 still vanish next to any score)
+        const float scale = a.scale == 0.f ? 1e-38f : fabsf(a.scale);
         const float sc = BIAS ? scale : scale * kLog2e;
         constexpr float unit = BIAS ? kLog2e : 1.f;  // of the reference, to log2
         const float* tab = table + g * sh.table + a.M + kTableExtra - pos;

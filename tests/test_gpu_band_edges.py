@@ -392,3 +392,12 @@ def test_a_captured_step_meets_far_rows_at_its_replay(dcn, dtype):  # noqa: F811
         torch.cuda.synchronize()
         for x, y in zip(replayed, step(bias)):
             assert torch.equal(x, y) and x.isfinite().all()
+
+
+@pytest.mark.parametrize("c", [case("bf16", 1, 100, 150, 2, 1, 64, scale=0.0, right=0), case("bf16", 1, 2, 150, 2, 1, 64, scale=0.0),
+                               case("f32", 1, 30, 50, 2, 1, 64, scale=0.0, left=9)], ids=str)
+def test_a_scale_of_zero_hides_large_products(dcn, c):  # noqa: F811
+    """Products of 10^29 times 0 are 0: uniform rows."""
+    t = make(c)
+    t["q"], t["k"] = t["q"] * 1e14, t["k"] * 1e14
+    compare(dcn, c, t)
