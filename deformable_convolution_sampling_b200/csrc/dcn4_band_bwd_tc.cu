@@ -23,10 +23,18 @@
 // kBandExactKeys), over the scores they came from in
 // tensor memory; the sums stay there in fp32 until they are rounded once.
 //
-// 2 x 4096 causal tokens, window 1024, 16 heads of 128 on 4: grad_q 122 us (its 90
-// GFLOP at 740 TFLOP/s), grad_kv 160 us (120 GFLOP), stats 20 us, bound by MMAs of
-// N = 64 from shared memory; 16 x 785 ragged tokens with a bias, 8 heads of 64: 77, 93
-// and 10 us, bound by the latency of a step's chain (products, exponentials, products).
+// A row whose lse is far from 0 (band_far) gets its maximum and sum anew in grad_q's first
+// pass; `weights`, 1 for all other rows, is the inverse of that sum for grad_kv.
+//
+// With a bias the tables of all heads that share a key head are held in shared memory;
+// where they pass kTableBytes grad_q's tiles are of one head each, and grad_kv, which goes
+// head by head, reloads the present head's.
+//
+// 2 x 4096 causal tokens, window 1024, 16 heads of 128 on 4: grad_q 129 us (its 90
+// GFLOP at 700 TFLOP/s), grad_kv 158 us (120 GFLOP), stats 20 us, bound by MMAs of
+// N = 64 from shared memory; 16 x 785 ragged tokens with a bias, 8 heads of 64: 80, 94
+// and 10 us, bound by the latency of a step's chain (products, exponentials, products);
+// 8 x 785 tokens, reach 128, 16 heads of 64: 98 and 135 us, on one key head 98 and 190.
 #include "dcn4_band_tc.cuh"
 
 namespace dcn4 {

@@ -21,11 +21,14 @@
 // band's edge are masked element by element.
 //
 // Bound by MMAs of N = 64 from shared memory (49 cycles, not 32: its bandwidth) and by
-// exponentials in equal parts for heads of 128, by issue slots for heads of 32.  Tiles of
-// 128 keys would run the MMAs at their full rate, but leave tensor memory no room for a
-// second tile's scores: 203 us against 145 for 8192 causal tokens with a window of 2048
-// and 16 heads of 128 on 4 (831 TFLOP/s); 8 maps of 64 x 64, eight rows of pixels and a
-// bias, 8 heads of 32: 122 us.
+// exponentials in equal parts for heads of 128; for heads of 32 with a bias by what a
+// pair costs beside its exponential (a shared read of its bias near the diagonal, mask,
+// maximum) on eight softmax warps a CTA: 52 % of the issue slots, 9 % of the tensor pipe.
+// Tiles of 128 keys would run the MMAs at their full rate, but leave tensor memory room
+// for one tile's scores a half: 203 us against 145 at 8192 causal tokens with a window of
+// 2048 and 16 heads of 128 on 4, before an issuing warp a half and waits that end on a
+// vote; not measured since.  That call now: 147 us (818 TFLOP/s); 8 maps of 64 x 64, eight
+// rows of pixels and a bias, 8 heads of 32: 123 us.
 #include "dcn4_band_tc.cuh"
 
 namespace dcn4 {

@@ -19,7 +19,8 @@
 // pieces p and p + R / 2 of the "halves" form (any two where pairs are neighbours), so
 // that turning is arithmetic on registers; the sums are shuffles.  Only where R / 2 is
 // no whole number of pieces does a head go through shared memory.  4 x 4096 tokens, 20
-// heads of 128, bf16: 42 us forward (4.0 TB/s; a copy takes 28), 68 us backward.
+// heads of 128, bf16: 42 us forward (4.0 TB/s; a copy takes 28), 67 us backward, 3 the
+// weights' sums.  Few loads are in flight (20 and 12 warps an SM, one item each).
 #include <algorithm>
 
 #include "dcn4_band.cuh"
@@ -45,8 +46,10 @@ struct Shape {
     long long units;
     int grid;
 };
-// CTAs an SM: without spills (at 6 and 4 the registers spill, and uneven shares of the
-// tokens cost a round: 46 and 77 us for 4 x 4096 tokens of 20 heads of 128).
+// CTAs an SM.  The 16-bit forwards spill a little at 5 (24 bytes where pairs are halves, 56
+// through shared memory), the backwards at 3 only there (16).  At 6 and 4 they spill more,
+// and uneven shares of the tokens cost a round: 46 and 77 us for 4 x 4096 tokens of 20 heads
+// of 128.
 constexpr int kForwardCtas = 5, kBackwardCtas = 3;
 
 // The units of a warp: all heads of a run of tokens, every warp's as long as the next
