@@ -241,9 +241,9 @@ def test_rotation_keeps_the_angle_beyond_32_bits(dcn, interleaved):  # noqa: F81
     f = torch.remainder(pos + torch.pi, 2 * torch.pi) - torch.pi
     pos = pos[(f.abs() > 2.9) & (f.abs() < 3.1)].float().cuda()[None]
     L = pos.shape[1]
-    x = torch.zeros(1, L, 2, 4, device="cuda")
+    x = torch.zeros(1, L, 2, 4, dtype=torch.float32, device="cuda")
     x[..., 0] = 2.0
-    inv = torch.tensor([1.0, 0.5], device="cuda")
+    inv = torch.tensor([1.0, 0.5], dtype=torch.float32, device="cuda")
     a = (x, x[:, :, :1].contiguous(), None, None, pos, inv)
     p = dcn.qknorm_params_for(*a, interleaved=interleaved, eps=1e-30)
     out, _ = dcn.qknorm_forward(p, *a)
@@ -259,8 +259,8 @@ def test_weight_gradients_are_rounded_once(dcn):  # noqa: F811
     gen = torch.Generator().manual_seed(11)
     N, L, D = 3, 296, 256
     x = torch.randint(0, 2, (N, L, 1, D), generator=gen).float() * 2 - 1
-    gq, gk = torch.randn(x.shape, generator=gen), torch.randn(x.shape, generator=gen)
-    one = torch.ones(D).cuda()
+    gq, gk = (torch.randn(x.shape, generator=gen, dtype=torch.float32) for _ in range(2))
+    one = torch.ones(D, dtype=torch.float32).cuda()
     a = (x.cuda(), x.cuda(), one, one, None, None)
     p = dcn.qknorm_params_for(*a, eps=1e-30)
     got = dcn.qknorm_backward(p, *a, gq.cuda(), gk.cuda())[2:]
@@ -271,7 +271,7 @@ def test_weight_gradients_are_rounded_once(dcn):  # noqa: F811
 
 def test_norm_of_zeros_with_a_tiny_eps(dcn):  # noqa: F811
     """1 / eps beyond the type's largest number: the gradient at zero is g w / sqrt(eps), a number."""
-    x, g = torch.zeros(1, 5, 2, 16).cuda(), torch.ones(1, 5, 2, 16).cuda()
+    x, g = (torch.full((1, 5, 2, 16), v, dtype=torch.float32).cuda() for v in (0.0, 1.0))
     p = dcn.qknorm_params_for(x, x, eps=1e-40)
     gx = dcn.qknorm_backward(p, x, x, None, None, None, None, g, g)[0]
     assert ((gx * 1e-20 - 1).abs() < 1e-4).all()  # eps is a subnormal: 1e-40 to 17 bits
