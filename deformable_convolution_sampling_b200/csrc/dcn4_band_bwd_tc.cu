@@ -413,8 +413,6 @@ __global__ void __launch_bounds__(QCfg<NB, BIAS>::threads, 1)
 #pragma unroll
                         for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(fmaf(__uint_as_float(x[e]), sc, tab[j + e]));
                     }
-                }
-                if (BIAS) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) sub_mul2(x[e], x[e + 1], ref, kLog2e);
                 } else {
